@@ -17,7 +17,7 @@
  *    nvfp4_last_error() gives a one-line reason for the last failure on the
  *    calling thread.  Errors found on the device (a bounded wait that timed
  *    out) are recorded in a device status word: for the calls that take a
- *    workspace (MoE forward, calibration, shared expert) the int at byte 0 of
+ *    workspace (MoE forwards, calibration, shared expert) the int at byte 0 of
  *    that workspace, cleared by the call's first kernel and read with
  *    nvfp4_read_device_status(); for the others (nvfp4_grouped_gemm) one word
  *    per device inside the library, read with nvfp4_device_status().
@@ -486,6 +486,91 @@ int nvfp4_moe_set_swap_l2(int enable, int* prev_enable);
  * with events NULL to switch it off.  Process-wide; not thread-safe.
  */
 int nvfp4_moe_set_stage_events(void* const* events, int n_events);
+
+/*
+ * nvfp4_add_rmsnorm_fp8 -- residual addition, RMSNorm and FP8 quantization of
+ * hidden states in one pass over them.
+ *
+ *   s = x + residual (FP32; x alone with residual NULL)
+ *   y = s * rsqrt(mean over the row of s^2 + eps) * weight (FP32)
+ *   scales[t][c] = max(max |y| over columns 128c..128c+127, 2^-40) / 448
+ *   q[t][i] = E4M3(y / scale of its block), round to nearest even
+ * Every output is rounded once, from the FP32 value.  A NaN or an infinity in
+ * a row makes the row's y NaN where 32-bit arithmetic gives NaN, scales included.
+ *   x, residual   device bf16 [T][H], row strides ld_x, ld_residual (elements)
+ *   weight        device bf16 [H], or f32 [H] with weight_is_f32 != 0
+ *   residual_out  device bf16 [T][H] (bf16(s)), row stride ld_residual_out, or
+ *                 NULL; may be x or residual itself (same stride)
+ *   normed        device bf16 [T][H] contiguous (bf16(y)), or NULL
+ *   q, scales     device E4M3 [T][H] contiguous and f32 [T][ceil(H/128)], both
+ *                 or neither NULL
+ * At least one output is required.  H a multiple of 16, 16 <= H <= 32768;
+ * strides >= H and multiples of 8; T >= 0 (0: no work); eps >= 0.  Pointers
+ * 16-byte aligned, scales 4-byte aligned.  Outputs overlap neither each other
+ * nor an input, but for the in-place residual.
+ */
+int nvfp4_add_rmsnorm_fp8(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
+                          int weight_is_f32, int64_t T, int64_t H, float eps, void* residual_out,
+                          int64_t ld_residual_out, void* normed, void* q, float* scales, void* stream);
+
+/*
+ * nvfp4_fp8_linear -- FP8 (E4M3) matrix product with a scale for each block of
+ * 128: rows of activations scaled per 1 x 128, weights per 128 x 128.
+ *
+ *   out[m][n] = sum over c of a_scale[m][c] * w_scale[n/128][c] *
+ *               (sum over k in 128c..128c+127 of a[m][k] * w[n][k])
+ * FP32 accumulation; the result is rounded once to the output type.
+ *   a        device E4M3 [M][K], row stride ld_a (bytes)
+ *   a_scale  device f32 [M][ceil(K/128)] (the layout nvfp4_add_rmsnorm_fp8 writes)
+ *   w        device E4M3 [N][K] contiguous
+ *   w_scale  device f32 [ceil(N/128)][ceil(K/128)]
+ *   out      device bf16 [M][N], or f32 with out_is_f32 != 0, row stride ld_out
+ * N % 8 == 0, K % 16 == 0, ld_a >= K and a multiple of 16, ld_out >= N and a
+ * multiple of 8, 0 <= M <= 1048576 (0: no work), N, K <= 1048576.  Pointers
+ * 16-byte aligned, scales 4-byte aligned.
+ */
+int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const void* w, const float* w_scale, int64_t M,
+                     int64_t N, int64_t K, void* out, int64_t ld_out, int out_is_f32, void* stream);
+
+/*
+ * nvfp4_moe_few_tokens -- the whole MoE FFN layer for at most
+ * NVFP4_MOE_FEW_TOKENS_MAX tokens, without quantizing the activations.
+ *
+ * Routing, SwiGLU and combine as nvfp4_moe_forward (top-k of the FP32 logits,
+ * ties -> lower expert; softmax over the k chosen); the weights are the same
+ * NVFP4 tensors.  The activations stay as they are: x is used exactly, h =
+ * silu(min(g, gate_limit)) * clamp(u, +-up_limit) is kept to 11 bits or more,
+ * sums are FP32, and each output is rounded to bf16 once.  So no activation
+ * scales are needed, and the result is nearer to the weights' exact layer than
+ * nvfp4_moe_forward's (which is the faster one for more tokens).
+ *   hidden   device bf16 [T][H], row stride ld_hidden (elements, a multiple of 8)
+ *   router_logits  device f32 [T][E]
+ *   w13 .. w2_gs   as nvfp4_moe_forward
+ *   out      device bf16 [T][H]
+ * An assignment whose weight is 0 (a -inf logit) is not computed; a token with
+ * none left (all logits -inf) gets a zero row.
+ * 0 <= T <= NVFP4_MOE_FEW_TOKENS_MAX (0: no work), H % 256 == 0, I % 128 == 0,
+ * H and I <= 8192, E <= 256, top_k <= min(8, E), limits > 0.  The workspace (256-byte aligned,
+ * nvfp4_moe_few_tokens_workspace_size() bytes; 0 for sizes out of range) serves
+ * one call at a time; its status word (byte 0) is cleared by the call and read
+ * with nvfp4_read_device_status().
+ *
+ * nvfp4_moe_few_tokens_routed: routing as nvfp4_moe_forward_routed (global ids
+ * i32 [T][top_k], weights f32 [T][top_k] used as given, experts_start); an
+ * expert that a token names twice is computed once, with the two weights' sum.
+ * Here top_k may exceed E, the experts held.
+ */
+#define NVFP4_MOE_FEW_TOKENS_MAX 32
+size_t nvfp4_moe_few_tokens_workspace_size(int64_t T, int64_t H, int64_t I, int E, int top_k);
+int nvfp4_moe_few_tokens(const void* hidden, int64_t ld_hidden, const float* router_logits, int64_t T, int64_t H,
+                         int64_t I, int E, int top_k, const void* w13, const void* w13_sf, const float* w13_gs,
+                         const void* w2, const void* w2_sf, const float* w2_gs, float gate_limit, float up_limit,
+                         void* workspace, size_t workspace_bytes, void* out, void* stream);
+int nvfp4_moe_few_tokens_routed(const void* hidden, int64_t ld_hidden, const int32_t* topk_ids,
+                                const float* topk_weights, int32_t experts_start, int64_t T, int64_t H, int64_t I,
+                                int E, int top_k, const void* w13, const void* w13_sf, const float* w13_gs,
+                                const void* w2, const void* w2_sf, const float* w2_gs, float gate_limit,
+                                float up_limit, void* workspace, size_t workspace_bytes, void* out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -198,6 +198,133 @@ class SharedExpertForward:
         return out
 
 
+def _empty(shape, dtype, device, stream):
+    """An output in the pool of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, name, dtype, T=None, cols=None):
+    """Checks a 2-D CUDA tensor with contiguous rows; returns its row stride."""
+    _need(t.dtype == dtype and t.dim() == 2 and t.is_cuda, f"{name} must be a 2-D {dtype} CUDA tensor")
+    _need(T is None or t.shape[0] == T, f"{name} must have {T} rows, not {t.shape[0]}")
+    _need(cols is None or t.shape[1] == cols, f"{name} must have {cols} columns, not {t.shape[1]}")
+    _need(t.stride(1) == 1 or t.shape[1] == 1, f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def add_rms_norm_fp8(x, residual, weight, eps=1e-6, normed=True, quantized=True, residual_out=None, stream=None):
+    """s = x + residual, y = s * rsqrt(mean(s^2) + eps) * weight, and y in FP8 blocks
+    of 128 columns (see nvfp4_add_rmsnorm_fp8).  x, residual bf16 [T, H] (rows
+    may be strided; residual may be None), weight bf16 or f32 [H].
+
+    Returns (q, scales, y, s): float8_e4m3fn [T, H] and f32 [T, ceil(H/128)]
+    (None with quantized=False), bf16 y (None with normed=False), bf16 s (None
+    without a residual).  residual_out: where s goes; x or residual for in place."""
+    ld_x = _rows(x, "x", torch.bfloat16)
+    T, H = x.shape
+    dev = x.device
+    _need(weight.shape == (H,) and weight.is_contiguous() and weight.device == dev and
+          weight.dtype in (torch.bfloat16, torch.float32), f"weight must be a contiguous bf16 or f32 [{H}]")
+    ld_r = ld_o = 0
+    if residual is not None:
+        ld_r = _rows(residual, "residual", torch.bfloat16, T, H)
+        if residual_out is None:
+            residual_out = _empty((T, H), torch.bfloat16, dev, stream)
+    if residual_out is not None:
+        ld_o = _rows(residual_out, "residual_out", torch.bfloat16, T, H)
+    y = _empty((T, H), torch.bfloat16, dev, stream) if normed else None
+    q = scales = None
+    if quantized:
+        q = _empty((T, H), torch.float8_e4m3fn, dev, stream)
+        scales = _empty((T, (H + 127) // 128), torch.float32, dev, stream)
+    B.nvfp4_add_rmsnorm_fp8(x, ld_x, residual, ld_r, weight, weight.dtype == torch.float32, T, H, eps, residual_out,
+                            ld_o, y, q, scales, stream)
+    return q, scales, y, residual_out
+
+
+def fp8_linear(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stream=None):
+    """a @ w.T of FP8 tensors with a scale for each block of 128 (see nvfp4_fp8_linear):
+    a float8_e4m3fn [M, K] (rows may be strided) with a_scale f32 [M, ceil(K/128)],
+    w float8_e4m3fn [N, K] with w_scale f32 [ceil(N/128), ceil(K/128)]; bf16 or f32 [M, N]."""
+    ld_a = _rows(a, "a", torch.float8_e4m3fn)
+    M, K = a.shape
+    _rows(w, "w", torch.float8_e4m3fn, None, K)
+    N = w.shape[0]
+    kb = (K + 127) // 128
+    _rows(a_scale, "a_scale", torch.float32, M, kb)
+    _rows(w_scale, "w_scale", torch.float32, (N + 127) // 128, kb)
+    _need(w.is_contiguous() and a_scale.is_contiguous() and w_scale.is_contiguous(),
+          "w and the scales must be contiguous")
+    if out is None:
+        _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+        out = _empty((M, N), out_dtype, a.device, stream)
+    else:
+        _need(out.dtype in (torch.bfloat16, torch.float32), "out must be bfloat16 or float32")
+    ld_out = _rows(out, "out", out.dtype, M, N)
+    B.nvfp4_fp8_linear(a, ld_a, a_scale, w, w_scale, M, N, K, out, ld_out, out.dtype == torch.float32, stream)
+    return out
+
+
+class MoEFewTokens:
+    """The MoE FFN layer for up to T <= 32 tokens with unquantized activations
+    (see nvfp4_moe_few_tokens), with its workspace: one call at a time."""
+
+    def __init__(self, T, H, I, E, top_k, device="cuda"):
+        self.T, self.H, self.I, self.E, self.top_k = T, H, I, E, top_k
+        self.ws_bytes = B.nvfp4_moe_few_tokens_workspace_size(T, H, I, E, top_k)
+        _need(self.ws_bytes > 0, f"unsupported sizes: T={T} H={H} I={I} E={E} top_k={top_k}")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+
+    def _check(self, hidden, w, out, stream):
+        H, I, E = self.H, self.I, self.E
+        ld = _rows(hidden, "hidden", torch.bfloat16, None, H)
+        T = hidden.shape[0]
+        _need(T <= self.T, f"{T} tokens; this layer was made for {self.T}")
+        _need(w.w13.shape == (E, 2 * I, H // 2) and w.w2.shape == (E, H, I // 2), "weights of another layer")
+        if out is None:
+            out = _empty((T, H), torch.bfloat16, hidden.device, stream)
+        else:
+            _rows(out, "out", torch.bfloat16, T, H)
+            _need(out.is_contiguous(), "out must be contiguous")
+        return T, ld, out
+
+    def __call__(self, hidden, logits, w: MoEWeights, gate_limit=10.0, up_limit=10.0, out=None, stream=None):
+        """hidden bf16 [t, H], t <= T (rows may be strided); logits f32 [t, E]."""
+        T, ld, out = self._check(hidden, w, out, stream)
+        _rows(logits, "logits", torch.float32, T, self.E)
+        _need(logits.is_contiguous(), "logits must be contiguous")
+        B.nvfp4_moe_few_tokens(hidden, ld, logits, T, self.H, self.I, self.E, self.top_k, w.w13, w.w13_sf, w.w13_gs,
+                               w.w2, w.w2_sf, w.w2_gs, gate_limit, up_limit, self.workspace, self.ws_bytes, out,
+                               stream)
+        return out
+
+    def routed(self, hidden, topk_ids, topk_weights, experts_start, w: MoEWeights, gate_limit=10.0, up_limit=10.0,
+               out=None, stream=None):
+        """The layer from the model router's global top-k (int32 / f32 [t, k]); it
+        holds the experts [experts_start, experts_start + E)."""
+        T, ld, out = self._check(hidden, w, out, stream)
+        _rows(topk_ids, "topk_ids", torch.int32, T, self.top_k)
+        _rows(topk_weights, "topk_weights", torch.float32, T, self.top_k)
+        _need(topk_ids.is_contiguous() and topk_weights.is_contiguous(), "ids and weights must be contiguous")
+        B.nvfp4_moe_few_tokens_routed(hidden, ld, topk_ids, topk_weights, experts_start, T, self.H, self.I, self.E,
+                                      self.top_k, w.w13, w.w13_sf, w.w13_gs, w.w2, w.w2_sf, w.w2_gs, gate_limit,
+                                      up_limit, self.workspace, self.ws_bytes, out, stream)
+        return out
+
+    def status(self, stream=None, reset=False):
+        """Device status word of the last call on this workspace (waits for the stream)."""
+        return B.nvfp4_read_device_status(self.workspace, stream, reset)
+
+
 class HostPipeline:
     """Streams batches from pinned host memory through one MoEForward.
 

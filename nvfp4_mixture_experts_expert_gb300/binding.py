@@ -36,6 +36,7 @@ NVFP4_ERR_WORKSPACE = 3
 NVFP4_ERR_CUDA = 4
 NVFP4_ERR_DEVICE = 5
 NVFP4_ERR_DEVICE_TIMEOUT = 6
+NVFP4_MOE_FEW_TOKENS_MAX = 32
 
 
 class Nvfp4Error(RuntimeError):
@@ -105,6 +106,17 @@ _mma_rate = _sig("nvfp4_debug_mma_rate", c_int, [c_ptr, c_size, c_ptr, c_size, c
 _stage_events = _sig("nvfp4_moe_set_stage_events", c_int, [ctypes.POINTER(c_ptr), c_int])
 _moe_set_overlap = _sig("nvfp4_moe_set_overlap", c_int, [c_int, ctypes.POINTER(c_int)])
 _gemm_set_cta_pair = _sig("nvfp4_gemm_set_cta_pair", c_int, [c_int, ctypes.POINTER(c_int)])
+_add_rmsnorm_fp8 = _sig("nvfp4_add_rmsnorm_fp8", c_int, [c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_int, c_i64, c_i64,
+                                                         c_float, c_ptr, c_i64, c_ptr, c_ptr, c_ptr, c_ptr])
+_fp8_linear = _sig("nvfp4_fp8_linear", c_int, [c_ptr, c_i64, c_ptr, c_ptr, c_ptr, c_i64, c_i64, c_i64, c_ptr, c_i64,
+                                               c_int, c_ptr])
+_few_ws = _sig("nvfp4_moe_few_tokens_workspace_size", c_size, [c_i64, c_i64, c_i64, c_int, c_int])
+_few = _sig("nvfp4_moe_few_tokens", c_int, [c_ptr, c_i64, c_ptr, c_i64, c_i64, c_i64, c_int, c_int, c_ptr, c_ptr,
+                                            c_ptr, c_ptr, c_ptr, c_ptr, c_float, c_float, c_ptr, c_size, c_ptr,
+                                            c_ptr])
+_few_routed = _sig("nvfp4_moe_few_tokens_routed", c_int, [c_ptr, c_i64, c_ptr, c_ptr, ctypes.c_int32, c_i64, c_i64,
+                                                          c_i64, c_int, c_int, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr,
+                                                          c_ptr, c_float, c_float, c_ptr, c_size, c_ptr, c_ptr])
 _moe_set_swap_l2 = _sig("nvfp4_moe_set_swap_l2", c_int, [c_int, ctypes.POINTER(c_int)])
 
 
@@ -311,3 +323,33 @@ def nvfp4_moe_set_stage_events(events):
         raise ValueError("stage events must have been recorded once (torch creates CUDA events lazily)")
     arr = (c_ptr * len(events))(*handles)
     _check(_stage_events(arr, len(events)))
+
+
+def nvfp4_add_rmsnorm_fp8(x, ld_x, residual, ld_residual, weight, weight_is_f32, T, H, eps, residual_out,
+                          ld_residual_out, normed, q, scales, stream=None):
+    _check(_add_rmsnorm_fp8(_p(x), ld_x, _p(residual), ld_residual, _p(weight), weight_is_f32, T, H, eps,
+                            _p(residual_out), ld_residual_out, _p(normed), _p(q), _p(scales), _stream(stream)))
+
+
+def nvfp4_fp8_linear(a, ld_a, a_scale, w, w_scale, M, N, K, out, ld_out, out_is_f32, stream=None):
+    _check(_fp8_linear(_p(a), ld_a, _p(a_scale), _p(w), _p(w_scale), M, N, K, _p(out), ld_out, out_is_f32,
+                       _stream(stream)))
+
+
+def nvfp4_moe_few_tokens_workspace_size(T, H, I, E, top_k):
+    return _few_ws(T, H, I, E, top_k)
+
+
+def nvfp4_moe_few_tokens(hidden, ld_hidden, router_logits, T, H, I, E, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs,
+                         gate_limit, up_limit, workspace, workspace_bytes, out, stream=None):
+    _check(_few(_p(hidden), ld_hidden, _p(router_logits), T, H, I, E, top_k, _p(w13), _p(w13_sf), _p(w13_gs), _p(w2),
+                _p(w2_sf), _p(w2_gs), gate_limit, up_limit, _p(workspace), workspace_bytes, _p(out),
+                _stream(stream)))
+
+
+def nvfp4_moe_few_tokens_routed(hidden, ld_hidden, topk_ids, topk_weights, experts_start, T, H, I, E, top_k, w13,
+                                w13_sf, w13_gs, w2, w2_sf, w2_gs, gate_limit, up_limit, workspace, workspace_bytes,
+                                out, stream=None):
+    _check(_few_routed(_p(hidden), ld_hidden, _p(topk_ids), _p(topk_weights), experts_start, T, H, I, E, top_k,
+                       _p(w13), _p(w13_sf), _p(w13_gs), _p(w2), _p(w2_sf), _p(w2_gs), gate_limit, up_limit,
+                       _p(workspace), workspace_bytes, _p(out), _stream(stream)))

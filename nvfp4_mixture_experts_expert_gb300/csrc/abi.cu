@@ -917,4 +917,185 @@ int nvfp4_moe_set_stage_events(void* const* events, int n_events) {
   return NVFP4_OK;
 }
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int nvfp4_add_rmsnorm_fp8(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
+                          int weight_is_f32, int64_t T, int64_t H, float eps, void* residual_out,
+                          int64_t ld_residual_out, void* normed, void* q, float* scales, void* stream) {
+  g_err[0] = 0;
+  if (T < 0 || T > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+  if (H < 16 || H % 16 || H > 32768) return fail(NVFP4_ERR_UNSUPPORTED, "H must be a multiple of 16, at most 32768");
+  if (!(eps >= 0.f)) return fail(NVFP4_ERR_INVALID_ARG, "eps must not be negative");
+  if (T == 0) return NVFP4_OK;
+  if (!residual_out && !normed && !q) return fail(NVFP4_ERR_INVALID_ARG, "no output given");
+  if (!q != !scales) return fail(NVFP4_ERR_INVALID_ARG, "q and scales go together");
+  if (!x || !weight) return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (ld_x < H || ld_x % 8 || (residual && (ld_residual < H || ld_residual % 8)) ||
+      (residual_out && (ld_residual_out < H || ld_residual_out % 8)))
+    return fail(NVFP4_ERR_INVALID_ARG, "row strides must be >= H and multiples of 8");
+  if ((residual_out == x && ld_residual_out != ld_x) ||
+      (residual && residual_out == residual && ld_residual_out != ld_residual))
+    return fail(NVFP4_ERR_INVALID_ARG, "an in-place residual_out needs its input's stride");
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(normed) ||
+      !aligned16(q) || !aligned4(scales))
+    return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (scales 4)");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  NormArgs a = {};
+  a.x = (const uint16_t*)x;
+  a.residual = (const uint16_t*)residual;
+  a.weight = weight;
+  a.residual_out = (uint16_t*)residual_out;
+  a.normed = (uint16_t*)normed;
+  a.q = (uint8_t*)q;
+  a.scales = scales;
+  a.ld_x = ld_x;
+  a.ld_residual = ld_residual;
+  a.ld_residual_out = ld_residual_out;
+  a.T = T;
+  a.H = (int)H;
+  a.weight_f32 = weight_is_f32 != 0;
+  a.eps = eps;
+  cudaError_t e = launch_add_rmsnorm_fp8(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "add_rmsnorm_fp8 launch");
+}
+
+int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const void* w, const float* w_scale, int64_t M,
+                     int64_t N, int64_t K, void* out, int64_t ld_out, int out_is_f32, void* stream) {
+  g_err[0] = 0;
+  constexpr int64_t kMost = 1 << 20;
+  if (M < 0 || M > kMost) return fail(NVFP4_ERR_INVALID_ARG, "M must be in [0, 1048576]");
+  if (N <= 0 || N % 8 || N > kMost) return fail(NVFP4_ERR_INVALID_ARG, "N must be a positive multiple of 8");
+  if (K <= 0 || K % 16 || K > kMost) return fail(NVFP4_ERR_INVALID_ARG, "K must be a positive multiple of 16");
+  if (M == 0) return NVFP4_OK;
+  if (ld_a < K || ld_a % 16 || ld_out < N || ld_out % 8)
+    return fail(NVFP4_ERR_INVALID_ARG, "need ld_a >= K, ld_a % 16 == 0, ld_out >= N, ld_out % 8 == 0");
+  if (!a || !a_scale || !w || !w_scale || !out) return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || !aligned4(a_scale) || !aligned4(w_scale))
+    return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (scales 4)");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  Fp8Args g = {};
+  g.a = (const uint8_t*)a;
+  g.a_scale = a_scale;
+  g.w = (const uint8_t*)w;
+  g.w_scale = w_scale;
+  g.out = out;
+  g.M = M;
+  g.ld_a = ld_a;
+  g.ld_out = ld_out;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.out_f32 = out_is_f32 != 0;
+  cudaError_t e = launch_fp8_small(g, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
+}
+
+// Workspace of the few-token layer: status word, routing tables, h, y.
+static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* route, size_t* h, size_t* y) {
+  const int64_t A = T * top_k;
+  size_t off = 256;
+  *route = off;
+  off += (size_t)round_up((int64_t)moe_few_route_words() * 4, 256);
+  *h = off;
+  off += (size_t)round_up(A * I * 4, 256);
+  *y = off;
+  off += (size_t)round_up(A * H * 4, 256);
+  return off;
+}
+
+static bool few_tokens_sizes(int64_t T, int64_t H, int64_t I, int E, int top_k) {
+  return T >= 0 && T <= NVFP4_MOE_FEW_TOKENS_MAX && H > 0 && H % 256 == 0 && H <= 8192 && I > 0 && I % 128 == 0 &&
+         I <= 8192 && E >= 1 && E <= 256 && top_k >= 1 && top_k <= 8;
+}
+
+size_t nvfp4_moe_few_tokens_workspace_size(int64_t T, int64_t H, int64_t I, int E, int top_k) {
+  size_t r, h, y;
+  return few_tokens_sizes(T, H, I, E, top_k) ? few_tokens_layout(T, H, I, top_k, &r, &h, &y) : 0;
+}
+
+static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt, int64_t T, int64_t H, int64_t I,
+                        int E, int top_k, const void* w13, const void* w13_sf, const float* w13_gs, const void* w2,
+                        const void* w2_sf, const float* w2_gs, float gate_limit, float up_limit, void* workspace,
+                        size_t workspace_bytes, void* out, void* stream) {
+  g_err[0] = 0;
+  if (T > NVFP4_MOE_FEW_TOKENS_MAX)
+    return fail(NVFP4_ERR_UNSUPPORTED, "at most %d tokens (nvfp4_moe_forward takes more)", NVFP4_MOE_FEW_TOKENS_MAX);
+  if (T < 0) return fail(NVFP4_ERR_INVALID_ARG, "T must be >= 0");
+  if (top_k < 1 || top_k > 8) return fail(NVFP4_ERR_INVALID_ARG, "top_k must be in [1, 8]");
+  if (!few_tokens_sizes(T, H, I, E, top_k))
+    return fail(NVFP4_ERR_UNSUPPORTED, "need H %% 256 == 0, I %% 128 == 0, H and I <= 8192, E in [1, 256]");
+  if (!rt.topk_ids && top_k > E) return fail(NVFP4_ERR_INVALID_ARG, "top_k must be at most E");
+  if (!(gate_limit > 0.f) || !(up_limit > 0.f)) return fail(NVFP4_ERR_INVALID_ARG, "limits must be positive");
+  if (T == 0) return NVFP4_OK;
+  if (!hidden || !w13 || !w13_sf || !w13_gs || !w2 || !w2_sf || !w2_gs || !out ||
+      !(rt.topk_ids ? (const void*)rt.topk_w : (const void*)rt.logits))
+    return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (ld_hidden < H || ld_hidden % 8) return fail(NVFP4_ERR_INVALID_ARG, "ld_hidden must be >= H and a multiple of 8");
+  if (!aligned16(hidden) || !aligned16(w13) || !aligned16(w13_sf) || !aligned16(w2) || !aligned16(w2_sf) ||
+      !aligned16(out) || !aligned4(rt.logits) || !aligned4(rt.topk_ids) || !aligned4(rt.topk_w) ||
+      !aligned4(w13_gs) || !aligned4(w2_gs))
+    return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (f32 and i32 vectors 4)");
+  size_t route, h, y;
+  const size_t need = few_tokens_layout(T, H, I, top_k, &route, &h, &y);
+  if (!workspace || workspace_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes needed", need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  uint8_t* ws = (uint8_t*)workspace;
+  FewArgs a = {};
+  a.x = (const uint16_t*)hidden;
+  a.ld_x = ld_hidden;
+  a.logits = rt.topk_ids ? nullptr : rt.logits;
+  a.ext_ids = rt.topk_ids;
+  a.ext_w = rt.topk_w;
+  a.start = rt.experts_start;
+  a.w13 = (const uint8_t*)w13;
+  a.sf13 = (const uint8_t*)w13_sf;
+  a.gs13 = w13_gs;
+  a.w2 = (const uint8_t*)w2;
+  a.sf2 = (const uint8_t*)w2_sf;
+  a.gs2 = w2_gs;
+  a.out = (uint16_t*)out;
+  a.status = (int*)ws;
+  a.route = (int32_t*)(ws + route);
+  a.h = (float*)(ws + h);
+  a.y = (float*)(ws + y);
+  a.T = (int)T;
+  a.H = (int)H;
+  a.I = (int)I;
+  a.E = E;
+  a.k = top_k;
+  a.gate_limit = gate_limit;
+  a.up_limit = up_limit;
+  cudaError_t e = launch_moe_few(a, dev->sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "moe_few_tokens launch");
+}
+
+int nvfp4_moe_few_tokens(const void* hidden, int64_t ld_hidden, const float* router_logits, int64_t T, int64_t H,
+                         int64_t I, int E, int top_k, const void* w13, const void* w13_sf, const float* w13_gs,
+                         const void* w2, const void* w2_sf, const float* w2_gs, float gate_limit, float up_limit,
+                         void* workspace, size_t workspace_bytes, void* out, void* stream) {
+  Routing rt = {};
+  rt.logits = router_logits;
+  return moe_few_impl(hidden, ld_hidden, rt, T, H, I, E, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gate_limit,
+                      up_limit, workspace, workspace_bytes, out, stream);
+}
+
+int nvfp4_moe_few_tokens_routed(const void* hidden, int64_t ld_hidden, const int32_t* topk_ids,
+                                const float* topk_weights, int32_t experts_start, int64_t T, int64_t H, int64_t I,
+                                int E, int top_k, const void* w13, const void* w13_sf, const float* w13_gs,
+                                const void* w2, const void* w2_sf, const float* w2_gs, float gate_limit,
+                                float up_limit, void* workspace, size_t workspace_bytes, void* out, void* stream) {
+  g_err[0] = 0;
+  if (T > 0 && (!topk_ids || !topk_weights)) return fail(NVFP4_ERR_INVALID_ARG, "topk_ids and topk_weights required");
+  Routing rt = {};
+  rt.topk_ids = topk_ids;
+  rt.topk_w = topk_weights;
+  rt.experts_start = experts_start;
+  return moe_few_impl(hidden, ld_hidden, rt, T, H, I, E, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gate_limit,
+                      up_limit, workspace, workspace_bytes, out, stream);
+}
+
 }  // extern "C"

@@ -226,4 +226,53 @@ void gemm_get_trace(unsigned long long** buf, int* stages, int* kind);
 cudaError_t gemm_status_ptr(int** ptr);
 cudaError_t gemm_read_status(int* out, int reset);
 
+// ---------------------------------------------------------------- norm_fp8.cu
+struct NormArgs {
+  const uint16_t* x;         // bf16 [T][H], row stride ld_x
+  const uint16_t* residual;  // bf16, or null
+  const void* weight;        // bf16 or f32 [H]
+  uint16_t* residual_out;    // bf16, or null; may be x or residual
+  uint16_t* normed;          // bf16 [T][H] or null
+  uint8_t* q;                // E4M3 [T][H] or null
+  float* scales;             // [T][ceil(H / 128)], with q
+  int64_t ld_x, ld_residual, ld_residual_out, T;
+  int H, weight_f32;
+  float eps;
+};
+cudaError_t launch_add_rmsnorm_fp8(const NormArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- fp8_small.cu
+struct Fp8Args {
+  const uint8_t* a;      // E4M3 [M][K], row stride ld_a
+  const float* a_scale;  // [M][ceil(K / 128)]
+  const uint8_t* w;      // E4M3 [N][K]
+  const float* w_scale;  // [ceil(N / 128)][ceil(K / 128)]
+  void* out;             // bf16 or f32 [M][N], row stride ld_out
+  int64_t M, ld_a, ld_out;
+  int N, K, out_f32;
+};
+cudaError_t launch_fp8_small(const Fp8Args& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- moe_few.cu
+constexpr int kFewTokens = 32;        // tokens of one call at most
+constexpr int kFewAssignments = 256;  // kFewTokens * 8
+struct FewArgs {
+  const uint16_t* x;      // bf16 [T][H], row stride ld_x
+  const float* logits;    // [T][E], or null: ext_ids / ext_w
+  const int32_t* ext_ids;
+  const float* ext_w;
+  const uint8_t *w13, *sf13, *w2, *sf2;
+  const float *gs13, *gs2;
+  uint16_t* out;          // bf16 [T][H]
+  int* status;            // workspace byte 0
+  int32_t* route;         // routing tables (moe_few.cu)
+  float* h;               // [T * k][I]
+  float* y;               // [T * k][H]
+  int64_t ld_x;
+  int T, H, I, E, k, start;
+  float gate_limit, up_limit;
+};
+size_t moe_few_route_words();
+cudaError_t launch_moe_few(const FewArgs& a, int num_sms, cudaStream_t s);
+
 }  // namespace nvfp4

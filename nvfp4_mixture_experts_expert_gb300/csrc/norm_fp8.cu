@@ -1,0 +1,124 @@
+// Residual addition, RMSNorm and FP8 quantization of hidden states in one pass.
+//
+//   s = x + residual                       (FP32; bf16(s) is the next residual)
+//   y = s * rsqrt(mean(s^2) + eps) * w     (FP32; bf16(y) is the normed output)
+//   per block of 128 columns of a row:
+//     scale = max(max|y|, 2^-40) / 448,  q = E4M3(y * (448 / max(max|y|, 2^-40)))
+//
+// s and y stay in FP32 registers; every output is rounded once.  The floor of
+// 2^-40 keeps the scale of an all-zero block finite (its codes are 0).  A NaN
+// in a row makes the whole row NaN (scales included).
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "nvfp4_format.cuh"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr float kMinAmax = 9.094947017729282e-13f;  // 2^-40
+constexpr int kMaxVec = 4;                          // 8-element vectors per thread
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+  f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+// One row per block; thread i holds vectors i, i + blockDim, ... (8 columns
+// each), so 16 consecutive lanes hold one 128-column block.
+template <int V>
+__global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const NormArgs p) {
+  const int64_t row = blockIdx.x;
+  const int nvec = p.H / 8, nt = blockDim.x, tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  __shared__ float s_sum[32];
+  float s[V][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int at = v * nt + tid;
+    if (at < nvec) {
+      unpack8(*reinterpret_cast<const uint4*>(p.x + row * p.ld_x + at * 8), s[v]);
+      if (p.residual) {
+        float r[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.residual + row * p.ld_residual + at * 8), r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[v][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(s[v][i], s[v][i], sum);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  sum = lane < (nt >> 5) ? s_sum[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float rstd = rsqrtf(sum / (float)p.H + p.eps);
+  const int cols = (p.H + 127) / 128;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int at = v * nt + tid;
+    const bool in = at < nvec;
+    float y[8], amax = 0.f;
+    if (in) {
+      float w[8];
+      if (p.weight_f32) {
+        const float4* wp = reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + at * 8);
+        const float4 a = __ldg(wp), b = __ldg(wp + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      } else {
+        unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + at * 8)), w);
+      }
+      if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + row * p.ld_residual_out + at * 8) = pack8(s[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = s[v][i] * rstd * w[i];
+        amax = max_nan(amax, fabsf(y[i]));
+      }
+      if (p.normed) *reinterpret_cast<uint4*>(p.normed + row * p.H + at * 8) = pack8(y);
+    }
+    if (p.q) {
+#pragma unroll
+      for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      amax = max_nan(amax, kMinAmax);
+      const float inv = 448.f / amax;
+      if (in) {
+        uint2 c;
+        c.x = e4m3x2_code(y[0] * inv, y[1] * inv) | (e4m3x2_code(y[2] * inv, y[3] * inv) << 16);
+        c.y = e4m3x2_code(y[4] * inv, y[5] * inv) | (e4m3x2_code(y[6] * inv, y[7] * inv) << 16);
+        *reinterpret_cast<uint2*>(p.q + row * p.H + at * 8) = c;
+        if ((lane & 15) == 0) p.scales[row * cols + at / 16] = amax / 448.f;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm_fp8(const NormArgs& a, cudaStream_t s) {
+  const int nvec = a.H / 8;
+  // two vectors a thread up to H = 4096, four above (1024 threads reach H = 32768)
+  const int v = nvec <= 512 ? 2 : kMaxVec;
+  const int nt = ((nvec + v - 1) / v + 31) / 32 * 32;
+  const dim3 grid((unsigned)a.T);
+  if (v == 2)
+    return launch_kernel(add_rmsnorm_fp8_kernel<2>, grid, dim3(nt), 0, s, false, a);
+  return launch_kernel(add_rmsnorm_fp8_kernel<4>, grid, dim3(nt), 0, s, false, a);
+}
+
+}  // namespace nvfp4
