@@ -122,17 +122,22 @@ _moe_set_swap_l2 = _sig("nvfp4_moe_set_swap_l2", c_int, [c_int, ctypes.POINTER(c
 
 def _p(t):
     """Device address of a torch tensor / int / None."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or t.__class__ is int else t.data_ptr()
+
+
+_raw_stream = _device = None
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream, _device
+        if _raw_stream is None:
+            import torch
+            # the handle alone: a Stream object costs more host time than a small launch
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+            _device = torch.cuda.current_device
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -100,6 +100,21 @@ int make_fp4_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, in
   return NVFP4_OK;
 }
 
+// Byte matrix [rows][cols] with a row stride; box 128 bytes x box_rows, 128-byte swizzle.
+int make_byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return NVFP4_OK;
+}
+
 // bf16 matrix [rows][cols] (row stride cols elements); box 64 columns (128 bytes)
 // x 32 rows, 128-byte swizzle: the staging layout of the routing-weighted L2
 // epilogue's bulk stores.
@@ -975,6 +990,25 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
     return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (scales 4)");
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
+  if (M > kFp8SmallRows) {
+    Fp8GemmArgs t;
+    memset(&t, 0, sizeof(t));
+    const int bn = fp8_gemm_bn(M, N, dev->sms);
+    if (int rc = make_byte_map(&t.map_a, a, M, K, ld_a, 128)) return rc;
+    if (int rc = make_byte_map(&t.map_w, w, N, K, K, bn)) return rc;
+    t.a_scale = a_scale;
+    t.w_scale = w_scale;
+    t.out = out;
+    t.status = dev->status;
+    t.timeout_ns = 2000000000ull;
+    t.ld_out = ld_out;
+    t.M = (int)M;
+    t.N = (int)N;
+    t.kbs = (int)((K + 127) / 128);
+    t.out_f32 = out_is_f32 != 0;
+    cudaError_t e = launch_fp8_gemm(t, bn, dev->sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
+  }
   Fp8Args g = {};
   g.a = (const uint8_t*)a;
   g.a_scale = a_scale;

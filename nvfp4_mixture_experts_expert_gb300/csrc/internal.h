@@ -242,6 +242,7 @@ struct NormArgs {
 cudaError_t launch_add_rmsnorm_fp8(const NormArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- fp8_small.cu
+constexpr int64_t kFp8SmallRows = 32;  // rows of a up to which this kernel is used
 struct Fp8Args {
   const uint8_t* a;      // E4M3 [M][K], row stride ld_a
   const float* a_scale;  // [M][ceil(K / 128)]
@@ -252,6 +253,22 @@ struct Fp8Args {
   int N, K, out_f32;
 };
 cudaError_t launch_fp8_small(const Fp8Args& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- fp8_gemm.cu
+struct Fp8GemmArgs {
+  CUtensorMap map_a;  // a: [M][K] bytes, box 128 x 128, 128-byte swizzle
+  CUtensorMap map_w;  // w: [N][K] bytes, box 128 x BN rows
+  const float* a_scale;
+  const float* w_scale;
+  void* out;
+  int* status;
+  uint64_t timeout_ns;
+  int64_t ld_out;
+  int M, N, kbs, out_f32;
+  int m_tiles, tiles;  // set by the launch
+};
+int fp8_gemm_bn(int64_t M, int64_t N, int num_sms);
+cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- moe_few.cu
 constexpr int kFewTokens = 32;        // tokens of one call at most
