@@ -115,19 +115,21 @@ int make_byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
   return NVFP4_OK;
 }
 
-// bf16 matrix [rows][cols] (row stride cols elements); box 64 columns (128 bytes)
-// x 32 rows, 128-byte swizzle: the staging layout of the routing-weighted L2
-// epilogue's bulk stores.
-int make_bf16_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols) {
+// Output matrix [rows][cols] of bf16 or f32 (row stride ld elements); box of
+// `bytes` (128 or 64) x 32 rows with the swizzle of that width: the staging
+// layout of the epilogues' bulk stores.
+int make_store_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32, int bytes) {
   auto fn = encode_fn();
   if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const int size = f32 ? 4 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {64, 32};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(bytes / size), 32};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return NVFP4_OK;
 }
@@ -423,7 +425,7 @@ int moe_forward_impl(const void* hidden, const Routing& rt, int64_t T, int64_t H
   if (int rc = make_fp4_map(&g1.tmap_b, w13, (int64_t)E * 2 * I, H)) return rc;
   if (int rc = make_fp4_map(&g2.tmap_a, a2, cap, I)) return rc;
   if (int rc = make_fp4_map(&g2.tmap_b, w2, (int64_t)E * H, I)) return rc;
-  if (int rc = make_bf16_store_map(&g2.tmap_y, ybuf, cap, H)) return rc;
+  if (int rc = make_store_map(&g2.tmap_y, ybuf, cap, H, H, false, 128)) return rc;
   g1.sfa = sfa1;
   g1.sfb = (const uint8_t*)w13_sf;
   g1.padded_offsets = offsets;
@@ -996,17 +998,14 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
     const int bn = fp8_gemm_bn(M, N, dev->sms);
     if (int rc = make_byte_map(&t.map_a, a, M, K, ld_a, 128)) return rc;
     if (int rc = make_byte_map(&t.map_w, w, N, K, K, bn)) return rc;
+    if (int rc = make_store_map(&t.map_out, out, M, N, ld_out, out_is_f32 != 0, 64)) return rc;
     t.a_scale = a_scale;
     t.w_scale = w_scale;
-    t.out = out;
     t.status = dev->status;
-    t.timeout_ns = 2000000000ull;
-    t.ld_out = ld_out;
     t.M = (int)M;
     t.N = (int)N;
     t.kbs = (int)((K + 127) / 128);
-    t.out_f32 = out_is_f32 != 0;
-    cudaError_t e = launch_fp8_gemm(t, bn, dev->sms, (cudaStream_t)stream);
+    cudaError_t e = launch_fp8_gemm(t, bn, out_is_f32 != 0, dev->sms, (cudaStream_t)stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
   }
   Fp8Args g = {};

@@ -15,9 +15,15 @@
 //   warp 0      TMA: per K-block a 128 x 128 box of a and a BN x 128 box of w
 //               (SWIZZLE_128B) into a ring; rows and columns past the matrices
 //               read as zero
-//   warp 1      TMEM allocator, MMA issuer (4 MMAs of K = 32 per block)
+//   warps 1, 2  MMA issuers (4 MMAs of K = 32 per block); warp 1 allocates TMEM
+//   warp 3      a's scales, transposed into shared memory
 //   warps 4-11  epilogue: a TMEM lane quarter and half of the columns each
-// Every wait is bounded (see ptx.cuh) and reports in the library's status word.
+// Every wait is bounded and reports in the library's status word.
+//
+// Measured (8192 x 4096 x 4096, bf16 out): 113 us, 2.44 PFLOP/s, 0.63 of twice
+// the measured bf16 rate.  The tile's operands are 48 KB a block and SM, 15 TB/s
+// out of L2 over the SMs at this rate; without the copies (operands stale,
+// timing only) the kernel took a tenth less.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -33,12 +39,22 @@ constexpr int kBM = 128;
 constexpr int kBK = 128;
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
+constexpr int kMmaWarps = 2;  // warps 1 and 2
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kRegsLaunch = 168;  // per thread at launch: 65,536 registers over 384 threads, in steps of 8
 constexpr int kRegsSmall = 56;    // warps 0-3
 constexpr int kRegsEpi = 224;     // epilogue: up to 128 sums and 64 loaded values
 static_assert(128 * (kRegsSmall + 2 * kRegsEpi) <= kThreads * kRegsLaunch,
               "the register split must fit the launch allocation");
+
+constexpr int kStagingBytes = 32 * 64;  // an epilogue warp's output buffer
+// a's scales pass through shared memory transposed, kScaleKb blocks of 128 rows
+// a slot: read from global memory by the epilogue, a row per lane, each block's
+// loads would touch 32 lines (256 cycles of the load unit over the 8 warps).
+constexpr int kScaleKb = 8;
+constexpr int kScaleSlots = 3;
+constexpr int kScalePitch = kBM + 4;  // floats; the transposing stores then hit 32 banks
+constexpr int kScaleSlotBytes = kScaleKb * kScalePitch * 4;
 
 template <int BN>
 struct Cfg {
@@ -48,7 +64,11 @@ struct Cfg {
   static constexpr int BUFS = BN == 256 ? 2 : 4;  // TMEM accumulators
   static constexpr int TMEM_COLS = BUFS * BN;
   static constexpr int COLS = BN / 2;             // columns of an epilogue warp
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + 8 * (2 * STAGES + 2 * BUFS + 1) + 16;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kEpiWarps * kStagingBytes +
+                                 kScaleSlots * kScaleSlotBytes + 8 * (2 * STAGES + BUFS + kMmaWarps + 2 * kScaleSlots) + 16;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static_assert(STAGES % kMmaWarps == 0 && BUFS % kMmaWarps == 0, "each MMA warp has slots of its own");
+  static_assert(STAGES >= BUFS, "a stage's barrier may not complete twice before the epilogue has seen it once");
 };
 
 // E4M3 x E4M3 -> FP32, K-major operands, M = 128.
@@ -65,7 +85,7 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t (&a)[32]) {
+__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&a)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -77,10 +97,13 @@ __device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t (&a)[32]) 
       : "memory");
 }
 
+// Shared-memory addresses: the ring, the output buffers, the barriers (full[STAGES]: a block's
+// operands have landed; done[STAGES]: its product is complete, which frees the
+// ring slot and hands the accumulator to the epilogue; acc_empty[BUFS]: the
+// epilogue has read an accumulator; sc_full, sc_empty[kScaleSlots]).
 template <int BN>
 struct Smem {
-  uint8_t* stages;
-  uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+  uint32_t stages, staging, scales, full, done, acc_empty, drain, sc_full, sc_empty;
   uint32_t* tmem_slot;
   int* abort_flag;
 };
@@ -89,15 +112,55 @@ template <int BN>
 __device__ __forceinline__ Smem<BN> carve(uint8_t* raw) {
   using C = Cfg<BN>;
   Smem<BN> s;
-  s.stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  s.full = reinterpret_cast<uint64_t*>(s.stages + C::STAGES * C::STAGE_BYTES);
-  s.empty = s.full + C::STAGES;
-  s.acc_full = s.empty + C::STAGES;
-  s.acc_empty = s.acc_full + C::BUFS;
-  s.drain = s.acc_empty + C::BUFS;
-  s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  s.stages = smem_u32(base);
+  s.staging = s.stages + C::STAGES * C::STAGE_BYTES;
+  s.scales = s.staging + kEpiWarps * kStagingBytes;
+  s.full = s.scales + kScaleSlots * kScaleSlotBytes;
+  s.done = s.full + 8 * C::STAGES;
+  s.acc_empty = s.done + 8 * C::STAGES;
+  s.drain = s.acc_empty + 8 * C::BUFS;
+  s.sc_full = s.drain + 8 * kMmaWarps;
+  s.sc_empty = s.sc_full + 8 * kScaleSlots;
+  s.tmem_slot = reinterpret_cast<uint32_t*>(base + (s.sc_empty + 8 * kScaleSlots - s.stages));
   s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
   return s;
+}
+
+// A bounded wait of the whole warp, without divergence: lane 0 tests (a
+// predicated instruction) and all lanes branch on a vote.  A lane that loops by
+// itself costs the code around it more than the wait: the epilogue's block,
+// ~350 cycles of TMEM reads and multiply-adds, took 860 with such a loop in it,
+// although the barrier was ready.  After kTries the role gives up.
+constexpr uint64_t kDrainNs = 2000000000ull;  // for what is in flight when a role gives up
+constexpr uint32_t kTries = 1u << 26;
+__device__ __forceinline__ uint32_t lane0_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 q, %3, 0;\nsetp.eq.b32 p, 0, 0;\n"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"((uint32_t)((threadIdx.x & 31) == 0))
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  for (uint32_t n = 1; !__all_sync(0xffffffffu, lane0_test(bar, parity)); ++n)
+    if (n % 256 == 0 && __any_sync(0xffffffffu, n >= kTries || *abort)) {
+      *abort = 1;
+      atomicExch(status, 6 /* NVFP4_ERR_DEVICE_TIMEOUT */);
+      return false;
+    }
+  return true;
+}
+
+// mbarrier.arrive by the lanes with `on` set, as a predicated instruction.
+__device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 st;\nsetp.ne.b32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(
+          bar),
+      "r"((int)on)
+      : "memory");
 }
 
 // Tiles m-fastest: the CTAs at work share few column tiles of w and every row of a.
@@ -110,6 +173,15 @@ __device__ __forceinline__ Tile tile_at(const Fp8GemmArgs& p, int it) {
   return {(it - nt * p.m_tiles) * kBM, nt * BN};
 }
 
+__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&a)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 template <int BN>
 __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
   using C = Cfg<BN>;
@@ -117,15 +189,14 @@ __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
-  int ok = 1;
+  bool ok = true;
   for (int it = blockIdx.x; it < p.tiles && ok && !*abort; it += gridDim.x) {
     const Tile t = tile_at<BN>(p, it);
     for (int kb = 0; kb < p.kbs; ++kb) {
-      if (lane == 0) ok = wait_bounded_spin(smem_u32(&L.empty[stage]), phase ^ 1u, abort, p.status, p.timeout_ns);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = warp_wait(L.done + 8 * stage, phase ^ 1u, abort, p.status);
       if (!ok) break;
       if (leader) {
-        const uint32_t at = smem_u32(L.stages) + stage * C::STAGE_BYTES, bar = smem_u32(&L.full[stage]);
+        const uint32_t at = L.stages + stage * C::STAGE_BYTES, bar = L.full + 8 * stage;
         mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
         tma_load_2d(at, &p.map_a, kb * kBK, t.m0, bar);
         tma_load_2d(at + C::A_BYTES, &p.map_w, kb * kBK, t.n0, bar);
@@ -143,160 +214,221 @@ __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
     for (int s = 0; s < C::STAGES; ++s)
       if (issued & (1u << s)) {
         volatile int no_abort = 0;
-        wait_bounded(smem_u32(&L.full[s]), (issued_parity >> s) & 1u, &no_abort, nullptr, p.timeout_ns);
+        wait_bounded(L.full + 8 * s, (issued_parity >> s) & 1u, &no_abort, nullptr, kDrainNs);
       }
   }
   __syncwarp();
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Slot by slot: 128 rows x kScaleKb blocks, four rows of eight to a copy, up to
+// kScaleSlots ahead.  Asynchronous, because behind the operand copies that the
+// ring keeps in flight a load takes microseconds.
 template <int BN>
-__device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem) {
+__device__ void scale_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
+  volatile int* abort = L.abort_flag;
+  const int lane = threadIdx.x & 31, r0 = lane >> 3, k = lane & 7;
+  uint32_t slot = 0, phase = 0;
+  bool ok = true;
+  for (int it = blockIdx.x; it < p.tiles && ok; it += gridDim.x) {
+    const Tile t = tile_at<BN>(p, it);
+    for (int c0 = 0; c0 < p.kbs; c0 += kScaleKb) {
+      ok = warp_wait(L.sc_empty + 8 * slot, phase ^ 1u, abort, p.status);
+      if (!ok) break;
+      const uint32_t to = L.scales + slot * kScaleSlotBytes + (k * kScalePitch + r0) * 4;
+      // past the last row or block: some valid scale, for sums that nobody stores or uses
+      const float* from = p.a_scale + min(c0 + k, p.kbs - 1);
+#pragma unroll 8
+      for (int i = 0; i < kBM / 4; ++i)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + i * 16),
+                     "l"(from + (int64_t)min(t.m0 + i * 4 + r0, p.M - 1) * p.kbs)
+                     : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(L.sc_full + 8 * slot) : "memory");
+      if (++slot == kScaleSlots) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Two warps issue alternate blocks (different ring slots and accumulators, so
+// their order does not matter): waiting for a block's barriers and issuing its
+// four MMAs takes a warp ~400 cycles, the MMAs of a 128 x 128 block 256.  One
+// elected lane issues; the loop runs on the whole warp so that descriptors,
+// addresses and phases are warp-uniform.
+template <int BN>
+__device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem, int which) {
   using C = Cfg<BN>;
   volatile int* abort = L.abort_flag;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   constexpr uint32_t idesc = idesc_e4m3(BN);
-  const uint64_t a0 = smem_desc(smem_u32(L.stages), 16, 1024, 2);
-  const uint64_t b0 = smem_desc(smem_u32(L.stages) + C::A_BYTES, 16, 1024, 2);
-  uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+  const uint64_t a0 = smem_desc(L.stages, 16, 1024, 2);
+  const uint64_t b0 = smem_desc(L.stages + C::A_BYTES, 16, 1024, 2);
+  uint32_t stage = which, phase = 0, buf = which, buf_phase = 1;
+  const int blocks = p.kbs * ((p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x);
   bool issued = false;
-  int ok = 1;
-  for (int it = blockIdx.x; it < p.tiles && ok && !*abort; it += gridDim.x) {
-    for (int kb = 0; kb < p.kbs; ++kb) {
-      if (lane == 0) {
-        ok = wait_bounded_spin(smem_u32(&L.acc_empty[buf]), buf_phase ^ 1u, abort, p.status, p.timeout_ns);
-        if (ok) ok = wait_bounded_spin(smem_u32(&L.full[stage]), phase, abort, p.status, p.timeout_ns);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t ad = a0 + (uint64_t)stage * (C::STAGE_BYTES >> 4);
-        const uint64_t bd = b0 + (uint64_t)stage * (C::STAGE_BYTES >> 4);
+  for (int b = which; b < blocks; b += kMmaWarps) {
+    if (!warp_wait(L.full + 8 * stage, phase, abort, p.status) ||
+        !warp_wait(L.acc_empty + 8 * buf, buf_phase, abort, p.status))
+      break;
+    tc_fence_after();
+    if (leader) {
+      const uint64_t ad = a0 + (uint64_t)stage * (C::STAGE_BYTES >> 4);
+      const uint64_t bd = b0 + (uint64_t)stage * (C::STAGE_BYTES >> 4);
+      const uint32_t d = tmem + buf * BN;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tc_mma_f8(tmem + buf * BN, ad + 2 * i, bd + 2 * i, idesc, i != 0);
-        tc_commit(smem_u32(&L.empty[stage]));
-        tc_commit(smem_u32(&L.acc_full[buf]));
-      }
-      __syncwarp();
-      issued = true;
-      if (++stage == C::STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      if (++buf == C::BUFS) {
-        buf = 0;
-        buf_phase ^= 1u;
-      }
+      for (int i = 0; i < 4; ++i) tc_mma_f8(d, ad + 2 * i, bd + 2 * i, idesc, i != 0);
+      tc_commit(L.done + 8 * stage);
+    }
+    __syncwarp();
+    issued = true;
+    if ((stage += kMmaWarps) >= C::STAGES) {
+      stage -= C::STAGES;
+      phase ^= 1u;
+    }
+    if ((buf += kMmaWarps) >= C::BUFS) {
+      buf -= C::BUFS;
+      buf_phase ^= 1u;
     }
   }
-  if (*abort && issued) {  // every MMA issued finishes before TMEM is freed
-    if (leader) tc_commit(smem_u32(L.drain));
+  if (__any_sync(0xffffffffu, *abort) && issued) {  // every MMA issued finishes before TMEM is freed
+    if (leader) tc_commit(L.drain + 8 * which);
     __syncwarp();
     if (lane == 0) {
       volatile int no_abort = 0;
-      wait_bounded(smem_u32(L.drain), 0, &no_abort, nullptr, p.timeout_ns);
+      wait_bounded(L.drain + 8 * which, 0, &no_abort, nullptr, kDrainNs);
     }
     __syncwarp();
   }
 }
 
-// acc += s * d for 32 columns.
-__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&d)[32], uint64_t s2) {
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+// acc += s * d.
+template <int W>
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&d)[W], uint64_t s2) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < W / 2; ++i)
     acc[i] = f2_fma(f2_pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), s2, acc[i]);
 }
 
-template <int BN>
+// A block costs a warp pair of one SM quarter 64 packed multiply-adds a thread
+// (256 cycles of the FP32 pipe for a 128 x 256 tile) and its TMEM reads (~150
+// cycles for all eight warps); measured alone, both together take ~340, of the
+// 512 that the block's MMAs take.  The rows' scales are loaded by warp 3; the
+// columns' (one number a warp) one block ahead, and multiplied when used: a
+// product any earlier would wait for the load.
+template <int BN, bool F32>
 __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem) {
   using C = Cfg<BN>;
-  constexpr int CHUNKS = C::COLS / 32;
+  constexpr int W = BN == 256 ? 16 : 32, CHUNKS = C::COLS / W;  // measured: 112 / 142 us at 256, 130 / 122 at 128
   volatile int* abort = L.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
   const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::COLS;
-  uint32_t buf = 0, buf_phase = 0;
-  int ok = 1;
+  const uint32_t staging = L.staging + (warp - kEpiWarp0) * kStagingBytes;
+  const uint32_t my_scales = L.scales + (quarter * 32 + lane) * 4;
+  uint32_t stage = 0, phase = 0, buf = 0, sc = 0, sc_phase = 0;
+  bool ok = true;
   for (int it = blockIdx.x; it < p.tiles && ok; it += gridDim.x) {
     const Tile t = tile_at<BN>(p, it);
-    const int m = t.m0 + quarter * 32 + lane, n0 = t.n0 + half * C::COLS;
-    const bool row = m < p.M, live = n0 < p.N;
-    const float* sa = p.a_scale + (int64_t)(row ? m : 0) * p.kbs;
-    const float* sw = p.w_scale + (int64_t)(live ? n0 / 128 : 0) * p.kbs;
-    // the block scales are loaded two blocks ahead
-    auto scale_at = [&](int kb) { return kb < p.kbs ? __ldg(sa + kb) * __ldg(sw + kb) : 0.f; };
-    float s0 = scale_at(0), s1 = scale_at(1);
+    const int n0 = t.n0 + half * C::COLS;
+    const float* sw = p.w_scale + (int64_t)(n0 < p.N ? n0 / 128 : 0) * p.kbs;
+    float sw0 = __ldg(sw);
     uint64_t acc[C::COLS / 2];
 #pragma unroll
     for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
     for (int kb = 0; kb < p.kbs; ++kb) {
-      const float s2 = scale_at(kb + 2);
-      if (lane == 0) ok = wait_bounded_spin(smem_u32(&L.acc_full[buf]), buf_phase, abort, p.status, p.timeout_ns);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      const float sw1 = kb + 1 < p.kbs ? __ldg(sw + kb + 1) : 0.f;
+      if (kb % kScaleKb == 0) {
+        ok = warp_wait(L.sc_full + 8 * sc, sc_phase, abort, p.status);
+        if (!ok) break;
+      }
+      const float sa0 = ld_shared_f32(my_scales + sc * kScaleSlotBytes + kb % kScaleKb * (kScalePitch * 4));
+      ok = warp_wait(L.done + 8 * stage, phase, abort, p.status);
       if (!ok) break;
       tc_fence_after();
       const uint32_t at = t0 + buf * BN;
+      const float s0 = sa0 * sw0;
       const uint64_t ss = f2_pack(s0, s0);
-      uint32_t d[2][32];
-      tmem_load_32(at, d[0]);
+      uint32_t d[W];
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c) {
+        tmem_load_cols(at + W * c, d);
         tmem_load_wait();
-        if (c + 1 < CHUNKS) {
-          tmem_load_32(at + 32 * (c + 1), d[(c + 1) & 1]);
-        } else {  // everything is in registers: the accumulator is free
+#pragma unroll
+        for (int i = 0; i < W; ++i) asm volatile("" : "+r"(d[i]));  // no use of d moves above the wait
+        if (c + 1 == CHUNKS) {  // everything is in registers: the accumulator is free
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&L.acc_empty[buf]));
+          arrive_if(lane == 0, L.acc_empty + 8 * buf);
         }
-        add_scaled(acc + 16 * c, d[c & 1], ss);
+        add_scaled(acc + W / 2 * c, d, ss);
       }
-      s0 = s1;
-      s1 = s2;
-      if (++buf == C::BUFS) {
-        buf = 0;
-        buf_phase ^= 1u;
+      sw0 = sw1;
+      if (kb % kScaleKb == kScaleKb - 1 || kb + 1 == p.kbs) {
+        __syncwarp();
+        arrive_if(lane == 0, L.sc_empty + 8 * sc);
+        if (++sc == kScaleSlots) {
+          sc = 0;
+          sc_phase ^= 1u;
+        }
       }
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (++buf == C::BUFS) buf = 0;
     }
     if (!ok) break;
-    if (!row) continue;
-    const int cols = min(C::COLS, p.N - n0);  // a multiple of 8
-    if (p.out_f32) {
-      float* to = static_cast<float*>(p.out) + (int64_t)m * p.ld_out + n0;
+    // 32 rows x 64 bytes at a time through the warp's staging buffer
+    constexpr int PIECE = F32 ? 16 : 32;  // columns
 #pragma unroll
-      for (int i = 0; i < C::COLS / 8; ++i)
-        if (8 * i < cols) {
-          uint32_t v[8];
+    for (int c = 0; c < C::COLS / PIECE; ++c) {
+      if (lane == 0) bulk_wait_read_all();  // the copy before has left the buffer
+      __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x, y;
-            f2_unpack(acc[4 * i + j], x, y);
+      for (int i = 0; i < 4; ++i) {  // 16 bytes each, at their place in the 64-byte swizzle
+        constexpr int PER = F32 ? 2 : 4;  // pairs of sums
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          float x, y;
+          f2_unpack(acc[c * PIECE / 2 + i * PER + j], x, y);
+          if (F32) {
             v[2 * j] = __float_as_uint(x);
             v[2 * j + 1] = __float_as_uint(y);
-          }
-          reinterpret_cast<uint4*>(to + 8 * i)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-          reinterpret_cast<uint4*>(to + 8 * i)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-        }
-    } else {
-      uint16_t* to = static_cast<uint16_t*>(p.out) + (int64_t)m * p.ld_out + n0;
-#pragma unroll
-      for (int i = 0; i < C::COLS / 8; ++i)
-        if (8 * i < cols) {
-          uint32_t v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x, y;
-            f2_unpack(acc[4 * i + j], x, y);
+          } else {
             v[j] = pack_bf16x2(x, y);
           }
-          *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
         }
+        st_shared_v4(staging + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), v);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int x = n0 + c * PIECE, y = t.m0 + quarter * 32;
+        if (x < p.N && y < p.M) tma_store_2d(&p.map_out, staging, x, y);  // clipped to the matrix
+        bulk_commit();
+      }
     }
   }
+  if (lane == 0) bulk_wait_all();
+  __syncwarp();
 }
 
-template <int BN>
+template <int BN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmArgs p) {
   using C = Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -304,18 +436,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(smem_u32(&L.full[s]), 1);
-      mbar_init(smem_u32(&L.empty[s]), 1);
+      mbar_init(L.full + 8 * s, 1);
+      mbar_init(L.done + 8 * s, 1);
     }
-    for (int b = 0; b < C::BUFS; ++b) {
-      mbar_init(smem_u32(&L.acc_full[b]), 1);
-      mbar_init(smem_u32(&L.acc_empty[b]), kEpiWarps);
+    for (int b = 0; b < C::BUFS; ++b) mbar_init(L.acc_empty + 8 * b, kEpiWarps);
+    for (int w = 0; w < kMmaWarps; ++w) mbar_init(L.drain + 8 * w, 1);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(L.sc_full + 8 * i, 32);
+      mbar_init(L.sc_empty + 8 * i, kEpiWarps);
     }
-    mbar_init(smem_u32(L.drain), 1);
     *L.abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&p.map_a);
     prefetch_tmap(&p.map_w);
+    prefetch_tmap(&p.map_out);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(L.tmem_slot), C::TMEM_COLS);
@@ -328,10 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   if (warp < kEpiWarp0) {
     regs_dec<kRegsSmall>();
     if (warp == 0) load_loop<BN>(p, L);
-    if (warp == 1) mma_loop<BN>(p, L, tmem);
+    if (warp == 1 || warp == 2) mma_loop<BN>(p, L, tmem, warp - 1);
+    if (warp == 3) scale_loop<BN>(p, L);
   } else {
     regs_inc<kRegsEpi>();
-    epilogue_loop<BN>(p, L, tmem);
+    epilogue_loop<BN, F32>(p, L, tmem);
   }
   __syncwarp();
   tc_fence_before();
@@ -342,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
 }
 
-template <int BN>
+template <int BN, bool F32>
 cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
   static int configured = -1;
   int dev = 0;
@@ -351,30 +486,40 @@ cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
   if (configured != dev) {
     // setmaxnreg.inc waits for what the other warps give back: launch only with the allocation it is sized for
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN, F32>)) != cudaSuccess) return e;
     if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::SMEM);
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Cfg<BN>::SMEM);
     if (e != cudaSuccess) return e;
     configured = dev;
   }
   p.m_tiles = (int)((p.M + kBM - 1) / kBM);
   p.tiles = p.m_tiles * ((p.N + BN - 1) / BN);
-  return launch_kernel(fp8_gemm_kernel<BN>, dim3(p.tiles < num_sms ? p.tiles : num_sms), dim3(kThreads),
+  return launch_kernel(fp8_gemm_kernel<BN, F32>, dim3(p.tiles < num_sms ? p.tiles : num_sms), dim3(kThreads),
                        Cfg<BN>::SMEM, s, false, p);
+}
+template <int BN>
+cudaError_t launch_out(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s) {
+  return f32 ? launch<BN, true>(p, num_sms, s) : launch<BN, false>(p, num_sms, s);
 }
 
 }  // namespace
 
-// Columns of a tile: the widest whose tiles fill the SMs.
+// Columns of a tile: those whose rounds of tiles over the SMs take least.  A
+// K-block of a tile measured 503, 279 and 199 ns at 256, 128 and 64 columns
+// (8192 x 4096 x 4096: 113, 125 and 172 us), so 64 pays when 256 leaves most SMs
+// without a tile (128 x 4096 x 4096: 10.4 against 18.5 us).
 int fp8_gemm_bn(int64_t M, int64_t N, int num_sms) {
   const int64_t mt = (M + kBM - 1) / kBM;
-  if (mt * ((N + 255) / 256) >= num_sms) return 256;
-  if (mt * ((N + 127) / 128) >= num_sms) return 128;
-  return 64;
+  auto time = [&](int64_t bn, int64_t ns) { return (mt * ((N + bn - 1) / bn) + num_sms - 1) / num_sms * ns; };
+  const int64_t t256 = time(256, 503), t128 = time(128, 279), t64 = time(64, 199);
+  return t256 <= t128 && t256 <= t64 ? 256 : t128 <= t64 ? 128 : 64;
 }
 
-cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, int num_sms, cudaStream_t s) {
-  return bn == 256 ? launch<256>(p, num_sms, s) : bn == 128 ? launch<128>(p, num_sms, s) : launch<64>(p, num_sms, s);
+cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, bool f32, int num_sms, cudaStream_t s) {
+  return bn == 256   ? launch_out<256>(p, f32, num_sms, s)
+         : bn == 128 ? launch_out<128>(p, f32, num_sms, s)
+                     : launch_out<64>(p, f32, num_sms, s);
 }
 
 }  // namespace nvfp4
