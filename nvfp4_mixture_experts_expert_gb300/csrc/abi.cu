@@ -1024,12 +1024,12 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
 }
 
-// Workspace of the few-token layer: status word, routing tables, h, y.
-static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* route, size_t* h, size_t* y) {
+// Workspace of the few-token layer: status word, counters, h, y.
+static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* done, size_t* h, size_t* y) {
   const int64_t A = T * top_k;
   size_t off = 256;
-  *route = off;
-  off += (size_t)round_up((int64_t)moe_few_route_words() * 4, 256);
+  *done = off;
+  off += kFewMaxTiles * 4;
   *h = off;
   off += (size_t)round_up(A * I * 4, 256);
   *y = off;
@@ -1069,8 +1069,8 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
       !aligned16(out) || !aligned4(rt.logits) || !aligned4(rt.topk_ids) || !aligned4(rt.topk_w) ||
       !aligned4(w13_gs) || !aligned4(w2_gs))
     return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (f32 and i32 vectors 4)");
-  size_t route, h, y;
-  const size_t need = few_tokens_layout(T, H, I, top_k, &route, &h, &y);
+  size_t done, h, y;
+  const size_t need = few_tokens_layout(T, H, I, top_k, &done, &h, &y);
   if (!workspace || workspace_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes needed", need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -1092,7 +1092,7 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
   a.gs2 = w2_gs;
   a.out = (uint16_t*)out;
   a.status = (int*)ws;
-  a.route = (int32_t*)(ws + route);
+  a.done = (int32_t*)(ws + done);
   a.h = (float*)(ws + h);
   a.y = (float*)(ws + y);
   a.T = (int)T;

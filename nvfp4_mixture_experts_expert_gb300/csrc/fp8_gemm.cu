@@ -127,42 +127,6 @@ __device__ __forceinline__ Smem<BN> carve(uint8_t* raw) {
   return s;
 }
 
-// A bounded wait of the whole warp, without divergence: lane 0 tests (a
-// predicated instruction) and all lanes branch on a vote.  A lane that loops by
-// itself costs the code around it more than the wait: the epilogue's block,
-// ~350 cycles of TMEM reads and multiply-adds, took 860 with such a loop in it,
-// although the barrier was ready.  After kTries the role gives up.
-constexpr uint64_t kDrainNs = 2000000000ull;  // for what is in flight when a role gives up
-constexpr uint32_t kTries = 1u << 26;
-__device__ __forceinline__ uint32_t lane0_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 q, %3, 0;\nsetp.eq.b32 p, 0, 0;\n"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"((uint32_t)((threadIdx.x & 31) == 0))
-      : "memory");
-  return ok;
-}
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
-  for (uint32_t n = 1; !__all_sync(0xffffffffu, lane0_test(bar, parity)); ++n)
-    if (n % 256 == 0 && __any_sync(0xffffffffu, n >= kTries || *abort)) {
-      *abort = 1;
-      atomicExch(status, 6 /* NVFP4_ERR_DEVICE_TIMEOUT */);
-      return false;
-    }
-  return true;
-}
-
-// mbarrier.arrive by the lanes with `on` set, as a predicated instruction.
-__device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 st;\nsetp.ne.b32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(
-          bar),
-      "r"((int)on)
-      : "memory");
-}
-
 // Tiles m-fastest: the CTAs at work share few column tiles of w and every row of a.
 struct Tile {
   int m0, n0;
