@@ -115,6 +115,31 @@ int make_byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
   return NVFP4_OK;
 }
 
+// Packed FP4 matrices [rows][K/2] and their scale tiles as the few-token layer
+// copies them (moe_few.cu): `lines` rows r, r+1, .. and r+32, r+64, r+96 on, over
+// all of K in slabs of 64 bytes (64-byte swizzle); the same lines' scales.
+int make_few_maps(FewMaps* m, const void* w, const void* sf, int64_t rows, int64_t K, int lines) {
+  auto fn = encode_fn();
+  if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const cuuint64_t row = (cuuint64_t)(K / 2);
+  const cuuint64_t wd[5] = {64, 32, 4, (cuuint64_t)(K / 128), (cuuint64_t)(rows / 128)};
+  const cuuint64_t ws[4] = {row, 32 * row, 64, 128 * row};
+  const cuuint32_t wb[5] = {64, (cuuint32_t)lines, 4, (cuuint32_t)(K / 128), 1};
+  CUresult r = fn(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(w), wd, ws, wb, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  const cuuint64_t sd[3] = {512, (cuuint64_t)(K / 64), (cuuint64_t)(rows / 128)};
+  const cuuint64_t ss[2] = {512, (cuuint64_t)(K / 64 * 512)};
+  const cuuint32_t sb[3] = {(cuuint32_t)(16 * lines), (cuuint32_t)(K / 64), 1};
+  r = fn(&m->sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(sf), sd, ss, sb, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return NVFP4_OK;
+}
+
 // Output matrix [rows][cols] of bf16 or f32 (row stride ld elements); box of
 // `bytes` (128 or 64) x 32 rows with the swizzle of that width: the staging
 // layout of the epilogues' bulk stores.
@@ -1102,7 +1127,10 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
   a.k = top_k;
   a.gate_limit = gate_limit;
   a.up_limit = up_limit;
-  cudaError_t e = launch_moe_few(a, dev->sms, (cudaStream_t)stream);
+  FewMaps m13 = {}, m2 = {};
+  if (int rc = make_few_maps(&m13, w13, w13_sf, (int64_t)E * 2 * I, H, 2)) return rc;
+  if (int rc = make_few_maps(&m2, w2, w2_sf, (int64_t)E * H, I, 4)) return rc;
+  cudaError_t e = launch_moe_few(a, m13, m2, dev->sms, (cudaStream_t)stream);
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "moe_few_tokens launch");
 }
 

@@ -288,6 +288,11 @@ struct FewArgs {
   int T, H, I, E, k, start;
   float gate_limit, up_limit;
 };
-cudaError_t launch_moe_few(const FewArgs& a, int num_sms, cudaStream_t s);
+// Tensor maps of one product's weights and scales (the box of an m16 tile, see
+// moe_few.cu), and of the next product's weights.
+struct FewMaps {
+  CUtensorMap w, sf, next_w;
+};
+cudaError_t launch_moe_few(const FewArgs& a, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s);
 
 }  // namespace nvfp4

@@ -22,6 +22,11 @@
 // line, so the rows of an m16 tile are taken as whole lines: W13, 2 lines of
 // gate rows and the same 2 of up rows (8 features; gate in accumulator rows
 // 0-7, up in rows 8-15, so a lane holds both of its feature); W2, 4 lines.
+// A tensor map with the dimensions (64 bytes, line, row of the line, slab,
+// 128-row block) then brings all of a tile's rows, slab by slab, in one or two
+// copies; row by row, a warp's issue of the copies took longer than their
+// arrival.  A slab of a row is 64 bytes and the 64-byte swizzle makes the
+// consumers' reads conflict-free.
 //
 // Two launches of one kernel, h between them; one CTA per SM, which takes an
 // equal share of the (list entry, tile) pairs in order, so that it changes
@@ -31,13 +36,12 @@
 //                    their activations stay in registers while the entry lasts
 //   warp 16          joins the KG sums in a fixed order; SwiGLU, or the weighted
 //                    row; the last to add to an output tile sums the experts
-//   warp 17          weights: one bulk copy a row into the ring, whose row pitch
-//                    (64 mod 128 bytes) makes the consumers' reads conflict-free
-//   warp 18          scales: the lines of the tile, 16 bytes a copy
+//   warp 17          the copies into the ring
 // Every CTA routes for itself (a microsecond, no launch in between).  The second
 // launch starts as CTAs of the first leave (programmatic dependent launch) and
 // fills its rings before it waits for h, and the first asks for the second's
 // first weights to be brought into L2, so HBM does not idle between the two.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -76,14 +80,16 @@ __device__ __forceinline__ float clamp_up(float v, float hi) { return v > hi ? h
 // One warp per token: lane j < k gets the j-th choice.  An assignment of weight
 // 0 (a -inf logit, a zero weight of the caller's) is not computed; a token with
 // none left gets a zero row.  An expert named twice is computed once, with the
-// sum of the two weights.
-__device__ void route_one(const FewArgs& p, int t, int lane, int32_t* s_id, float* s_w, uint32_t* s_mask) {
+// sum of the two weights.  NK: logits a lane.
+template <int NK>
+__device__ __forceinline__ void route_one(const FewArgs& p, int t, int lane, int32_t* s_id, float* s_w,
+                                          uint32_t* s_mask) {
   int id = -1;
   float w = 0.f;
   if (p.logits) {
-    uint64_t key[8];
+    uint64_t key[NK];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NK; ++i) {
       const int e = i * 32 + lane;
       key[i] = e < p.E ? route_key(__ldg(p.logits + (int64_t)t * p.E + e), e) : 0ull;
     }
@@ -91,12 +97,12 @@ __device__ void route_one(const FewArgs& p, int t, int lane, int32_t* s_id, floa
     for (int j = 0; j < p.k; ++j) {
       uint64_t best = key[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) best = key[i] > best ? key[i] : best;
+      for (int i = 1; i < NK; ++i) best = key[i] > best ? key[i] : best;
       const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
       const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
       const uint64_t win = ((uint64_t)hi << 32) | lo;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < NK; ++i)
         if (key[i] == win) key[i] = 0ull;
       if (lane == j) mine = win;
     }
@@ -148,7 +154,14 @@ __device__ void route_all(const FewArgs& p, Route* r) {
   for (int e = tid; e < 256; e += kThreads) s_mask[e] = 0u;
   for (int i = tid; i < kFewAssignments * kGroup; i += kThreads) (&r->member[0][0])[i] = -1;
   __syncthreads();
-  for (int t = warp; t < p.T; t += kThreads / 32) route_one(p, t, lane, r->id, r->weight, s_mask);
+  for (int t = warp; t < p.T; t += kThreads / 32) {
+    if (p.E <= 32)
+      route_one<1>(p, t, lane, r->id, r->weight, s_mask);
+    else if (p.E <= 64)
+      route_one<2>(p, t, lane, r->id, r->weight, s_mask);
+    else
+      route_one<8>(p, t, lane, r->id, r->weight, s_mask);
+  }
   __syncthreads();
   if (warp == 0) {  // list entries of the experts, in expert order
     int n[8], sum = 0;
@@ -245,26 +258,25 @@ __device__ __forceinline__ float swiglu(float gate, float up, float gate_limit, 
   return gate / (1.f + expf(-gate)) * up;
 }
 
-// Where row g (and, in W2, row g + 8) of m16 tile `st` lies: feature (phase 0)
-// or output column (phase 1).
+// Where row m of m16 tile `st` lies: feature (phase 0, m < 8; its gate and up row
+// are accumulator rows m and m + 8) or output column (phase 1, m < 16).
 template <int PHASE>
-__device__ __forceinline__ int tile_row(int st, int g) {
-  const int i = g >> 2, j = g & 3;
-  return PHASE == 0 ? (st >> 4) * 128 + (st & 15) * 2 + i + 32 * j : (st >> 3) * 128 + (st & 7) * 4 + i + 32 * j;
+__device__ __forceinline__ int tile_row(int st, int m) {
+  return PHASE == 0 ? (st >> 4) * 128 + (st & 15) * 2 + (m & 1) + 32 * (m >> 1)
+                    : (st >> 3) * 128 + (st & 7) * 4 + (m & 3) + 32 * (m >> 2);
 }
 
 // What a launch needs to know of its product (0: W13 x, 1: W2 h).
 struct Phase {
-  int K, R, KG;      // R m16 tiles a tile, KG = 16 / R warps along K
-  int tiles;         // per list entry
-  int pitch;         // bytes of a weight row in the ring
-  int scale_off;     // of the tile's scales in a ring slot
+  int K, R, KG;       // R m16 tiles a tile, KG = 16 / R warps along K
+  int tiles;          // per list entry
+  int blocks;         // 128-row blocks of an expert's matrix
   int stage_bytes, stages;
 };
 
 struct Ring {
-  uint32_t slots, part;             // weights and scales of a tile; the warps' sums
-  uint32_t full, scales, empty;     // a slot's weights, its scales have landed; it has been read
+  uint32_t slots, part;  // a tile's weights (8K bytes an m16 tile), then its scales (K bytes each); the warps' sums
+  uint32_t full, empty;  // a slot has landed; it has been read
   uint32_t part_full, part_empty;
   volatile int* abort;
 };
@@ -278,6 +290,9 @@ __device__ __forceinline__ Unit unit_at(int u, int tiles) {
   return {v, u - v * tiles};
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
@@ -292,27 +307,37 @@ __device__ __forceinline__ void sts128(uint32_t at, float a, float b, float c, f
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
-// Global row of row m (0-15) of m16 tile st.
+// ------------------------------------------------------------------ producer
+// Copies of m16 tile st of an expert: coordinates (byte, line, row of the line,
+// slab, block) and (byte, scale column / 4, block).  Phase 0 has the gate rows
+// and, I rows on, the up rows.
 template <int PHASE>
-__device__ __forceinline__ int weight_row(int st, int m, int I) {
-  return tile_row<PHASE>(st, m & 7) + (m < 8 ? 0 : PHASE == 0 ? I : 2);
+struct TileAt {
+  int line, block;
+  __device__ TileAt(const Phase& g, int e, int st)
+      : line(PHASE == 0 ? (st & 15) * 2 : (st & 7) * 4), block(e * g.blocks + (PHASE == 0 ? st >> 4 : st >> 3)) {}
+};
+
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, int line, int block, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %2, "
+      "%4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(block), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int block, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(block), "r"(bar)
+      : "memory");
 }
 
 template <int PHASE>
-__device__ __forceinline__ const uint8_t* expert_weights(const FewArgs& p, int e, int K) {
-  const int64_t rows = PHASE == 0 ? 2 * (int64_t)p.I : p.H;
-  return (PHASE == 0 ? p.w13 : p.w2) + e * rows * (K / 2);
-}
-template <int PHASE>
-__device__ __forceinline__ const uint8_t* expert_scales(const FewArgs& p, int e, int K) {
-  const int64_t rows = PHASE == 0 ? 2 * (int64_t)p.I : p.H;
-  return (PHASE == 0 ? p.sf13 : p.sf2) + e * rows * (K / 16);
-}
-
-// ------------------------------------------------------------------ producers
-template <int PHASE>
-__device__ void weight_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
-  const int lane = threadIdx.x & 31, rows = 16 * g.R;
+__device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, const Ring& L, const Route* r, int u0,
+                          int u1) {
+  const int lane = threadIdx.x & 31;
+  const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   for (int u = u0; u < u1; ++u) {
     if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) {
@@ -326,13 +351,21 @@ __device__ void weight_loop(const FewArgs& p, const Phase& g, const Ring& L, con
       return;
     }
     const Unit t = unit_at(u, g.tiles);
-    const uint8_t* W = expert_weights<PHASE>(p, r->expert[t.v], g.K);
-    const uint32_t to = L.slots + stage * g.stage_bytes, bar = L.full + 8 * stage;
-    if (lane == 0) mbar_arrive_expect_tx(bar, rows * (g.K / 2));
-    __syncwarp();
-    for (int i = lane; i < rows; i += 32)
-      bulk_load(to + i * g.pitch, W + (int64_t)weight_row<PHASE>(t.tile * g.R + (i >> 4), i & 15, p.I) * (g.K / 2),
-                g.K / 2, bar);
+    const int e = r->expert[t.v];
+    if (leader) {
+      const uint32_t w = L.slots + stage * g.stage_bytes, sf = w + 8 * g.K * g.R, bar = L.full + 8 * stage;
+      mbar_arrive_expect_tx(bar, 9 * g.K * g.R);
+      for (int i = 0; i < g.R; ++i) {
+        const TileAt<PHASE> at(g, e, t.tile * g.R + i);
+        const uint32_t wi = w + i * 8 * g.K, si = sf + i * g.K;
+        load_5d(wi, &m.w, at.line, at.block, bar);
+        load_3d(si, &m.sf, at.line * 16, at.block, bar);
+        if (PHASE == 0) {
+          load_5d(wi + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar);
+          load_3d(si + g.K / 2, &m.sf, at.line * 16, at.block + g.blocks / 2, bar);
+        }
+      }
+    }
     __syncwarp();
     issued |= 1u << stage;
     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -343,44 +376,20 @@ __device__ void weight_loop(const FewArgs& p, const Phase& g, const Ring& L, con
   }
 }
 
-template <int PHASE>
-__device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
-  const int lane = threadIdx.x & 31, cts = g.K / 64, lines = g.R * cts * 4;
-  uint32_t stage = 0, phase = 0;
-  for (int u = u0; u < u1; ++u) {
-    if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) break;
-    const Unit t = unit_at(u, g.tiles);
-    const uint8_t* SF = expert_scales<PHASE>(p, r->expert[t.v], g.K);
-    const uint32_t to = L.slots + stage * g.stage_bytes + g.scale_off;
-    for (int i = lane; i < lines; i += 32) {
-      const int line = i & 3, c = i >> 2, sub = c / cts, ct = c - sub * cts, st = t.tile * g.R + sub;
-      const int row = PHASE == 0 ? (line >> 1) * p.I + (st >> 4) * 128 + (st & 15) * 2 + (line & 1)
-                                 : (st >> 3) * 128 + (st & 7) * 4 + line;
-      const uint8_t* from = SF + ((int64_t)(row >> 7) * cts + ct) * 512 + (row & 31) * 16;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(from) : "memory");
-    }
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(L.scales + 8 * stage) : "memory");
-    if (++stage == (uint32_t)g.stages) {
-      stage = 0;
-      phase ^= 1u;
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 // The first W2 tiles of this CTA's share of the second launch, into L2.
-__device__ void prefetch_w2(const FewArgs& p, const Phase& g, const Route* r) {
-  const int lane = threadIdx.x & 31;
+__device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
   const int64_t units = (int64_t)r->n_list * g.tiles;
   const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  if (!elect_one()) return;
   for (int u = u0; u < min(u1, u0 + kPrefetch); ++u) {
     const Unit t = unit_at(u, g.tiles);
-    const uint8_t* W = expert_weights<1>(p, r->expert[t.v], g.K);
-    for (int i = lane; i < 16 * g.R; i += 32)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                       W + (int64_t)weight_row<1>(t.tile * g.R + (i >> 4), i & 15, p.I) * (g.K / 2)),
-                   "r"(g.K / 2)
+    for (int i = 0; i < g.R; ++i) {
+      const TileAt<1> at(g, r->expert[t.v], t.tile * g.R + i);
+      asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %1, %1, %3}];" ::"l"(
+                       reinterpret_cast<uint64_t>(&m.next_w)),
+                   "r"(0), "r"(at.line), "r"(at.block)
                    : "memory");
+    }
   }
 }
 
@@ -443,8 +452,13 @@ template <int PHASE, int SPW>
 __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
   const int kg = warp % g.KG, sub = warp / g.KG, slabs = g.K / 128;
-  const uint32_t w_off = (sub * 16 + gr) * g.pitch + q * 16;
-  const uint32_t s_off = g.scale_off + sub * g.K + (q >> 1) * 64 + (gr >> 2) * 16 + (gr & 3) * 4 + (q & 1) * 2;
+  // rows gr and gr + 8 of the m16 tile in a slab, and their scales
+  constexpr uint32_t slab_w = PHASE == 0 ? 512 : 1024, slab_s = PHASE == 0 ? 64 : 128;
+  const uint32_t w_off = sub * 8 * g.K + gr * 64 + ((q ^ (gr >> 1 & 3)) << 4);
+  const uint32_t w_off2 = w_off + (PHASE == 0 ? 4 * g.K : 512);
+  const uint32_t s_off = 8 * g.K * g.R + sub * g.K + (q >> 1) * (slab_s / 2) + (q & 1) * 2 +
+                         (PHASE == 0 ? (gr & 1) * 16 + (gr >> 1) * 4 : (gr & 3) * 16 + (gr >> 2) * 4);
+  const uint32_t s_off2 = s_off + (PHASE == 0 ? g.K / 2 : 8);
   const uint32_t part = L.part + warp * 512 + lane * 16;
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
   uint32_t b[SPW][16];
@@ -459,17 +473,15 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
       i0 = __shfl_sync(0xffffffffu, inv, q * 8);
       i1 = __shfl_sync(0xffffffffu, inv, q * 8 + 4);
     }
-    if (!warp_wait(L.scales + 8 * stage, phase, L.abort, p.status) ||
-        !warp_wait(L.full + 8 * stage, phase, L.abort, p.status))
-      return;
+    if (!warp_wait(L.full + 8 * stage, phase, L.abort, p.status)) return;
     const uint32_t at = L.slots + stage * g.stage_bytes;
     float c[4] = {}, d[4] = {};
 #pragma unroll
     for (int s = 0; s < SPW; ++s) {
       const int slab = kg + s * g.KG;
       if (slab < slabs) {
-        const uint4 w0 = lds128(at + w_off + slab * 64), w1 = lds128(at + w_off + 8 * g.pitch + slab * 64);
-        const uint32_t s0 = lds16(at + s_off + slab * 128), s1 = lds16(at + s_off + slab * 128 + 32);
+        const uint4 w0 = lds128(at + w_off + slab * slab_w), w1 = lds128(at + w_off2 + slab * slab_w);
+        const uint32_t s0 = lds16(at + s_off + slab * slab_s), s1 = lds16(at + s_off2 + slab * slab_s);
         mma_slab(c, d, w0, w1, s0, s1, b[s]);
       }
     }
@@ -493,38 +505,25 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
 }
 
 // ------------------------------------------------------------------ join
-template <int PHASE>
-__device__ void join_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
+template <int PHASE, int R>
+__device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0,
+                                          int u1) {
+  constexpr int KG = kWarps / R;
   const int lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
   uint32_t buf = 0, phase = 0;
   for (int u = u0; u < u1; ++u) {
     const Unit t = unit_at(u, g.tiles);
     const int a0 = r->member[t.v][2 * q], a1 = r->member[t.v][2 * q + 1];
+    const float p0 = PHASE == 1 && a0 >= 0 ? r->weight[a0] : 0.f, p1 = PHASE == 1 && a1 >= 0 ? r->weight[a1] : 0.f;
     if (!warp_wait(L.part_full + 8 * buf, phase, L.abort, p.status)) return;
-    for (int sub = 0; sub < g.R; ++sub) {
-      const uint32_t from = L.part + buf * (kWarps * 512) + sub * g.KG * 512 + lane * 16;
-      float c[4] = {};
-      for (int i = 0; i < g.KG; ++i) {
-        const uint4 v = lds128(from + i * 512);
-        c[0] += __uint_as_float(v.x), c[1] += __uint_as_float(v.y);
-        c[2] += __uint_as_float(v.z), c[3] += __uint_as_float(v.w);
-      }
-      const int row = tile_row<PHASE>(t.tile * g.R + sub, gr);
-      if (PHASE == 0) {
-        if (a0 >= 0) p.h[(int64_t)a0 * p.I + row] = swiglu(c[0], c[2], p.gate_limit, p.up_limit);
-        if (a1 >= 0) p.h[(int64_t)a1 * p.I + row] = swiglu(c[1], c[3], p.gate_limit, p.up_limit);
-      } else {
-        if (a0 >= 0) {
-          float* y = p.y + (int64_t)a0 * p.H + row;
-          y[0] = c[0] * r->weight[a0];
-          y[2] = c[2] * r->weight[a0];
-        }
-        if (a1 >= 0) {
-          float* y = p.y + (int64_t)a1 * p.H + row;
-          y[0] = c[1] * r->weight[a1];
-          y[2] = c[3] * r->weight[a1];
-        }
-      }
+    const uint32_t from = L.part + buf * (kWarps * 512) + lane * 16;
+    float c[R][4];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const uint4 v = lds128(from + i * 512);
+      const float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+#pragma unroll
+      for (int n = 0; n < 4; ++n) c[i / KG][n] = i % KG ? c[i / KG][n] + f[n] : f[n];
     }
     __syncwarp();
     arrive_if(lane == 0, L.part_empty + 8 * buf);
@@ -532,6 +531,36 @@ __device__ void join_loop(const FewArgs& p, const Phase& g, const Ring& L, const
       buf = 0;
       phase ^= 1u;
     }
+#pragma unroll
+    for (int sub = 0; sub < R; ++sub) {
+      const int row = tile_row<PHASE>(t.tile * R + sub, gr);
+      if (PHASE == 0) {
+        if (a0 >= 0) p.h[(int64_t)a0 * p.I + row] = swiglu(c[sub][0], c[sub][2], p.gate_limit, p.up_limit);
+        if (a1 >= 0) p.h[(int64_t)a1 * p.I + row] = swiglu(c[sub][1], c[sub][3], p.gate_limit, p.up_limit);
+      } else {  // accumulator row gr + 8 is output column row + 64
+        if (a0 >= 0) {
+          float* y = p.y + (int64_t)a0 * p.H + row;
+          y[0] = c[sub][0] * p0;
+          y[64] = c[sub][2] * p0;
+        }
+        if (a1 >= 0) {
+          float* y = p.y + (int64_t)a1 * p.H + row;
+          y[0] = c[sub][1] * p1;
+          y[64] = c[sub][3] * p1;
+        }
+      }
+    }
+  }
+}
+
+template <int PHASE>
+__device__ void join_tiles(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
+  switch (g.R) {
+    case 1: return join_loop<PHASE, 1>(p, g, L, r, u0, u1);
+    case 2: return join_loop<PHASE, 2>(p, g, L, r, u0, u1);
+    case 4: return join_loop<PHASE, 4>(p, g, L, r, u0, u1);
+    case 8: return join_loop<PHASE, 8>(p, g, L, r, u0, u1);
+    default: return join_loop<PHASE, 16>(p, g, L, r, u0, u1);
   }
 }
 
@@ -554,7 +583,7 @@ __device__ void sum_tiles(const FewArgs& p, const Phase& g, const Route* r, cons
   const int cols = 16 * g.R, per = p.T * cols;
   for (int i = threadIdx.x; i < count * per; i += kThreads) {
     const int tile = s_mine[i / per], t = i % per / cols, c = i % cols;
-    const int n = weight_row<1>(tile * g.R + (c >> 4), c & 15, 0);
+    const int n = tile_row<1>(tile * g.R + (c >> 4), c & 15);
     float sum = 0.f;
     for (int j = 0; j < p.k; ++j) {
       const int a = t * p.k + j;
@@ -565,26 +594,25 @@ __device__ void sum_tiles(const FewArgs& p, const Phase& g, const Route* r, cons
 }
 
 template <int PHASE, int SPW>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewArgs p, const Phase g, const Phase next) {
-  extern __shared__ uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewMaps m, const FewArgs p, const Phase g,
+                                                           const Phase next) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Route route;
-  __shared__ uint64_t s_bars[3 * kMaxStages + 2 * kPartBufs];
+  __shared__ uint64_t s_bars[2 * kMaxStages + 2 * kPartBufs];
   __shared__ int s_abort, s_count;
   __shared__ int s_mine[kFewMaxTiles];
   const int warp = threadIdx.x >> 5;
   Ring L;
-  L.slots = smem_u32(smem);
+  L.slots = (smem_u32(smem) + 1023u) & ~1023u;
   L.part = L.slots + g.stages * g.stage_bytes;
   L.full = smem_u32(s_bars);
-  L.scales = L.full + 8 * kMaxStages;
-  L.empty = L.scales + 8 * kMaxStages;
+  L.empty = L.full + 8 * kMaxStages;
   L.part_full = L.empty + 8 * kMaxStages;
   L.part_empty = L.part_full + 8 * kPartBufs;
   L.abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) {
       mbar_init(L.full + 8 * i, 1);
-      mbar_init(L.scales + 8 * i, 32);
       mbar_init(L.empty + 8 * i, kWarps);
     }
     for (int i = 0; i < kPartBufs; ++i) {
@@ -594,6 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewArgs p, const
     s_abort = 0;
     s_count = 0;
     fence_mbar_init();
+    prefetch_tmap(&m.w);
+    prefetch_tmap(&m.sf);
   }
   if (PHASE == 0) {
     pdl_wait();  // logits and activations may come from the kernel just before, and its caller may still use h
@@ -601,6 +631,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewArgs p, const
     if (blockIdx.x == 0) {
       if (threadIdx.x == 0) *p.status = 0;
       for (int i = threadIdx.x; i < kFewMaxTiles; i += kThreads) p.done[i] = 0;
+    }
+    // on their way to L2 while the tokens are routed
+    const int lines = (p.H + 63) / 64;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.T * lines; i += gridDim.x * kThreads)
+      prefetch_l2(p.x + (int64_t)(i / lines) * p.ld_x + i % lines * 64);
+    if (threadIdx.x < p.E) {
+      prefetch_l2(p.gs13 + threadIdx.x);
+      prefetch_l2(p.gs2 + threadIdx.x);
     }
   }
   // The second launch reads the router's output before it waits for the first:
@@ -617,13 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewArgs p, const
     if constexpr (SPW > 2) regs_dec<kRegsOther>();
     if (warp == kWarps) {
       if (PHASE == 1) pdl_wait();
-      join_loop<PHASE>(p, g, L, &route, u0, u1);
+      join_tiles<PHASE>(p, g, L, &route, u0, u1);
       if (PHASE == 1) count_tiles(p, g, &route, u0, u1, s_mine, &s_count);
     } else if (warp == kWarps + 1) {
-      weight_loop<PHASE>(p, g, L, &route, u0, u1);
-      if (PHASE == 0) prefetch_w2(p, next, &route);
-    } else if (warp == kWarps + 2) {
-      scale_loop<PHASE>(p, g, L, &route, u0, u1);
+      copy_loop<PHASE>(p, m, g, L, &route, u0, u1);
+      if (PHASE == 0) prefetch_w2(m, next, &route);
     }
   }
   __syncthreads();
@@ -640,23 +676,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewArgs p, const
   }
 }
 
-Phase phase_of(int K, int m16_tiles, size_t smem) {
+Phase phase_of(int K, int m16_tiles, int blocks, size_t smem) {
   Phase g = {};
   g.K = K;
   g.R = 1;
   while (g.R < kWarps && 2 * g.R * K <= 4096) g.R *= 2;
   g.KG = kWarps / g.R;
   g.tiles = m16_tiles / g.R;  // 16 or more m16 tiles, in sixteens
-  g.pitch = (K / 2) % 128 == 64 ? K / 2 : K / 2 + 64;
-  g.scale_off = 16 * g.R * g.pitch;
-  g.stage_bytes = g.scale_off + g.R * K;
-  const int n = (int)((smem - kPartBufs * kWarps * 512) / g.stage_bytes);
+  g.blocks = blocks;
+  g.stage_bytes = (9 * K * g.R + 1023) / 1024 * 1024;
+  const int n = (int)((smem - 1024 - kPartBufs * kWarps * 512) / g.stage_bytes);
   g.stages = n < kMaxStages ? n : kMaxStages;
   return g;
 }
 
 template <int PHASE, int SPW>
-cudaError_t launch(const FewArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch(const FewArgs& a, const FewMaps& m, int num_sms, cudaStream_t s) {
   static int configured = -1;
   static size_t dynamic = 0;
   int dev = 0;
@@ -672,22 +707,25 @@ cudaError_t launch(const FewArgs& a, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured = dev;
   }
-  const Phase first = phase_of(a.H, a.I / 8, dynamic), second = phase_of(a.I, a.H / 16, dynamic);
+  const Phase first = phase_of(a.H, a.I / 8, 2 * a.I / 128, dynamic);
+  const Phase second = phase_of(a.I, a.H / 16, a.H / 128, dynamic);
   const Phase& g = PHASE == 0 ? first : second;
-  const size_t smem = (size_t)g.stages * g.stage_bytes + kPartBufs * kWarps * 512;
-  return launch_kernel(few_kernel<PHASE, SPW>, dim3(num_sms), dim3(kThreads), smem, s, true, a, g, second);
+  const size_t smem = 1024 + (size_t)g.stages * g.stage_bytes + kPartBufs * kWarps * 512;
+  return launch_kernel(few_kernel<PHASE, SPW>, dim3(num_sms), dim3(kThreads), smem, s, true, m, a, g, second);
 }
 
 template <int PHASE>
-cudaError_t launch_phase(const FewArgs& a, int K, int num_sms, cudaStream_t s) {
-  return K > 4096 ? launch<PHASE, 4>(a, num_sms, s) : launch<PHASE, 2>(a, num_sms, s);
+cudaError_t launch_phase(const FewArgs& a, const FewMaps& m, int K, int num_sms, cudaStream_t s) {
+  return K > 4096 ? launch<PHASE, 4>(a, m, num_sms, s) : launch<PHASE, 2>(a, m, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_moe_few(const FewArgs& a, int num_sms, cudaStream_t s) {
-  const cudaError_t e = launch_phase<0>(a, a.H, num_sms, s);
-  return e == cudaSuccess ? launch_phase<1>(a, a.I, num_sms, s) : e;
+cudaError_t launch_moe_few(const FewArgs& a, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s) {
+  FewMaps m = w13;
+  m.next_w = w2.w;
+  const cudaError_t e = launch_phase<0>(a, m, a.H, num_sms, s);
+  return e == cudaSuccess ? launch_phase<1>(a, w2, a.I, num_sms, s) : e;
 }
 
 }  // namespace nvfp4
