@@ -115,27 +115,22 @@ int make_byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
   return NVFP4_OK;
 }
 
-// Packed FP4 matrices [rows][K/2] and their scale tiles as the few-token layer
-// copies them (moe_few.cu): `lines` rows r, r+1, .. and r+32, r+64, r+96 on, over
-// all of K in slabs of 64 bytes (64-byte swizzle); the same lines' scales.
-int make_few_maps(FewMaps* m, const void* w, const void* sf, int64_t rows, int64_t K, int lines) {
+// Packed FP4 matrices [rows][K/2] as the few-token layer copies them
+// (moe_few.cu): `lines` rows r, r+1, .. and r+32, r+64, r+96 on, over all of K in
+// pieces of 128 bytes where they fit a row, else of 64, swizzled in that width.
+int make_few_map(CUtensorMap* m, const void* w, int64_t rows, int64_t K, int lines) {
   auto fn = encode_fn();
   if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint32_t piece = K % 256 ? 64 : 128;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const cuuint64_t row = (cuuint64_t)(K / 2);
-  const cuuint64_t wd[5] = {64, 32, 4, (cuuint64_t)(K / 128), (cuuint64_t)(rows / 128)};
-  const cuuint64_t ws[4] = {row, 32 * row, 64, 128 * row};
-  const cuuint32_t wb[5] = {64, (cuuint32_t)lines, 4, (cuuint32_t)(K / 128), 1};
-  CUresult r = fn(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(w), wd, ws, wb, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  const cuuint64_t sd[3] = {512, (cuuint64_t)(K / 64), (cuuint64_t)(rows / 128)};
-  const cuuint64_t ss[2] = {512, (cuuint64_t)(K / 64 * 512)};
-  const cuuint32_t sb[3] = {(cuuint32_t)(16 * lines), (cuuint32_t)(K / 64), 1};
-  r = fn(&m->sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(sf), sd, ss, sb, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[5] = {piece, 32, 4, row / piece, (cuuint64_t)(rows / 128)};
+  const cuuint64_t strides[4] = {row, 32 * row, piece, 128 * row};
+  const cuuint32_t box[5] = {piece, (cuuint32_t)lines, 4, (cuuint32_t)(row / piece), 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(w), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        piece == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return NVFP4_OK;
 }
@@ -1049,12 +1044,12 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
 }
 
-// Workspace of the few-token layer: status word, counters, h, y.
-static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* done, size_t* h, size_t* y) {
+// Workspace of the few-token layer: status word, ids, h, y.
+static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* ids, size_t* h, size_t* y) {
   const int64_t A = T * top_k;
   size_t off = 256;
-  *done = off;
-  off += kFewMaxTiles * 4;
+  *ids = off;
+  off += kFewAssignments * 4;
   *h = off;
   off += (size_t)round_up(A * I * 4, 256);
   *y = off;
@@ -1094,8 +1089,8 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
       !aligned16(out) || !aligned4(rt.logits) || !aligned4(rt.topk_ids) || !aligned4(rt.topk_w) ||
       !aligned4(w13_gs) || !aligned4(w2_gs))
     return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (f32 and i32 vectors 4)");
-  size_t done, h, y;
-  const size_t need = few_tokens_layout(T, H, I, top_k, &done, &h, &y);
+  size_t ids, h, y;
+  const size_t need = few_tokens_layout(T, H, I, top_k, &ids, &h, &y);
   if (!workspace || workspace_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes needed", need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -1117,7 +1112,7 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
   a.gs2 = w2_gs;
   a.out = (uint16_t*)out;
   a.status = (int*)ws;
-  a.done = (int32_t*)(ws + done);
+  a.ids = (int32_t*)(ws + ids);
   a.h = (float*)(ws + h);
   a.y = (float*)(ws + y);
   a.T = (int)T;
@@ -1128,8 +1123,8 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
   a.gate_limit = gate_limit;
   a.up_limit = up_limit;
   FewMaps m13 = {}, m2 = {};
-  if (int rc = make_few_maps(&m13, w13, w13_sf, (int64_t)E * 2 * I, H, 2)) return rc;
-  if (int rc = make_few_maps(&m2, w2, w2_sf, (int64_t)E * H, I, 4)) return rc;
+  if (int rc = make_few_map(&m13.w, w13, (int64_t)E * 2 * I, H, 2)) return rc;
+  if (int rc = make_few_map(&m2.w, w2, (int64_t)E * H, I, 4)) return rc;
   cudaError_t e = launch_moe_few(a, m13, m2, dev->sms, (cudaStream_t)stream);
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "moe_few_tokens launch");
 }

@@ -271,7 +271,6 @@ cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, bool f32, int num_sms, cudaS
 // ---------------------------------------------------------------- moe_few.cu
 constexpr int kFewTokens = 32;        // tokens of one call at most
 constexpr int kFewAssignments = 256;  // kFewTokens * 8
-constexpr int kFewMaxTiles = 512;     // output tiles: 8192 columns in sixteens
 struct FewArgs {
   const uint16_t* x;      // bf16 [T][H], row stride ld_x
   const float* logits;    // [T][E], or null: ext_ids / ext_w
@@ -281,17 +280,17 @@ struct FewArgs {
   const float *gs13, *gs2;
   uint16_t* out;          // bf16 [T][H]
   int* status;            // workspace byte 0
-  int32_t* done;          // [kFewMaxTiles] list entries added to an output tile
+  int32_t* ids;           // [kFewAssignments] local expert of an assignment, -1: not computed
   float* h;               // [T * k][I]
   float* y;               // [T * k][H]
   int64_t ld_x;
   int T, H, I, E, k, start;
   float gate_limit, up_limit;
 };
-// Tensor maps of one product's weights and scales (the box of an m16 tile, see
-// moe_few.cu), and of the next product's weights.
+// Tensor maps of one product's weights (the box of an m16 tile, see moe_few.cu)
+// and of the next product's.
 struct FewMaps {
-  CUtensorMap w, sf, next_w;
+  CUtensorMap w, next_w;
 };
 cudaError_t launch_moe_few(const FewArgs& a, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s);
 

@@ -22,21 +22,24 @@
 // line, so the rows of an m16 tile are taken as whole lines: W13, 2 lines of
 // gate rows and the same 2 of up rows (8 features; gate in accumulator rows
 // 0-7, up in rows 8-15, so a lane holds both of its feature); W2, 4 lines.
-// A tensor map with the dimensions (64 bytes, line, row of the line, slab,
-// 128-row block) then brings all of a tile's rows, slab by slab, in one or two
-// copies; row by row, a warp's issue of the copies took longer than their
-// arrival.  A slab of a row is 64 bytes and the 64-byte swizzle makes the
-// consumers' reads conflict-free.
+// A tensor map with the dimensions (64 or 128 bytes of a row, line, row of the
+// line, piece of the row, 128-row block) then brings all of a tile's rows, piece
+// by piece, in one or two copies; row by row, a warp's issue of the copies took
+// longer than their arrival.  The copy engine takes about as long for 64 bytes
+// of a row as for 128, so the pieces are 128 bytes where K % 256 == 0.  The
+// swizzle of the piece's width makes the consumers' reads conflict-free.
 //
-// Two launches of one kernel, h between them; one CTA per SM, which takes an
+// Two launches of one kernel, h between them, and a sum; one CTA per SM, which takes an
 // equal share of the (list entry, tile) pairs in order, so that it changes
 // expert once or twice.  A tile is R m16 tiles (about 32 KB of packed weights)
 // over all of K.  Its warps:
 //   16 consumers     KG = 16 / R of them share an m16 tile and split K by slabs;
 //                    their activations stay in registers while the entry lasts
 //   warp 16          joins the KG sums in a fixed order; SwiGLU, or the weighted
-//                    row; the last to add to an output tile sums the experts
-//   warp 17          the copies into the ring
+//                    row of W2 h
+//   warp 17          the weights' copies into the ring
+//   warp 18          the scales', 16 bytes a line: as 32-byte pieces they would
+//                    be a third of the copy engine's work
 // Every CTA routes for itself (a microsecond, no launch in between).  The second
 // launch starts as CTAs of the first leave (programmatic dependent launch) and
 // fills its rings before it waits for h, and the first asks for the second's
@@ -214,8 +217,7 @@ __device__ __forceinline__ void scale_pairs(uint32_t codes, uint32_t& s0, uint32
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -258,25 +260,31 @@ __device__ __forceinline__ float swiglu(float gate, float up, float gate_limit, 
   return gate / (1.f + expf(-gate)) * up;
 }
 
-// Where row m of m16 tile `st` lies: feature (phase 0, m < 8; its gate and up row
-// are accumulator rows m and m + 8) or output column (phase 1, m < 16).
+// Where row r of m16 tile `st` lies in the order of its copy (line fastest):
+// feature (phase 0, r < 8: its gate row; the up rows are a copy of their own) or
+// output column (phase 1, r < 16).
 template <int PHASE>
-__device__ __forceinline__ int tile_row(int st, int m) {
-  return PHASE == 0 ? (st >> 4) * 128 + (st & 15) * 2 + (m & 1) + 32 * (m >> 1)
-                    : (st >> 3) * 128 + (st & 7) * 4 + (m & 3) + 32 * (m >> 2);
+__device__ __forceinline__ int tile_row(int st, int r) {
+  return PHASE == 0 ? (st >> 4) * 128 + (st & 15) * 2 + (r & 1) + 32 * (r >> 1)
+                    : (st >> 3) * 128 + (st & 7) * 4 + (r & 3) + 32 * (r >> 2);
 }
+// The copied row that accumulator row g (0-7) takes.  With 128-byte pieces, two
+// rows that eight lanes read together have to differ in bit 2 to miss each
+// other's banks under the swizzle.
+__device__ __forceinline__ int copied_row(int g, int wide) { return wide ? (g & 1) << 2 | g >> 1 : g; }
 
 // What a launch needs to know of its product (0: W13 x, 1: W2 h).
 struct Phase {
   int K, R, KG;       // R m16 tiles a tile, KG = 16 / R warps along K
   int tiles;          // per list entry
   int blocks;         // 128-row blocks of an expert's matrix
+  int wide;           // 128-byte pieces of a row, else 64
   int stage_bytes, stages;
 };
 
 struct Ring {
   uint32_t slots, part;  // a tile's weights (8K bytes an m16 tile), then its scales (K bytes each); the warps' sums
-  uint32_t full, empty;  // a slot has landed; it has been read
+  uint32_t full, scales, empty;  // a slot's weights, its scales have landed; it has been read
   uint32_t part_full, part_empty;
   volatile int* abort;
 };
@@ -308,8 +316,7 @@ __device__ __forceinline__ void sts128(uint32_t at, float a, float b, float c, f
 }
 
 // ------------------------------------------------------------------ producer
-// Copies of m16 tile st of an expert: coordinates (byte, line, row of the line,
-// slab, block) and (byte, scale column / 4, block).  Phase 0 has the gate rows
+// Line and 128-row block of m16 tile st of an expert.  Phase 0 has the gate rows
 // and, I rows on, the up rows.
 template <int PHASE>
 struct TileAt {
@@ -325,14 +332,6 @@ __device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, in
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(block), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int block, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(block), "r"(bar)
-      : "memory");
-}
-
 template <int PHASE>
 __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, const Ring& L, const Route* r, int u0,
                           int u1) {
@@ -353,17 +352,12 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
     const Unit t = unit_at(u, g.tiles);
     const int e = r->expert[t.v];
     if (leader) {
-      const uint32_t w = L.slots + stage * g.stage_bytes, sf = w + 8 * g.K * g.R, bar = L.full + 8 * stage;
-      mbar_arrive_expect_tx(bar, 9 * g.K * g.R);
+      const uint32_t w = L.slots + stage * g.stage_bytes, bar = L.full + 8 * stage;
+      mbar_arrive_expect_tx(bar, 8 * g.K * g.R);
       for (int i = 0; i < g.R; ++i) {
         const TileAt<PHASE> at(g, e, t.tile * g.R + i);
-        const uint32_t wi = w + i * 8 * g.K, si = sf + i * g.K;
-        load_5d(wi, &m.w, at.line, at.block, bar);
-        load_3d(si, &m.sf, at.line * 16, at.block, bar);
-        if (PHASE == 0) {
-          load_5d(wi + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar);
-          load_3d(si + g.K / 2, &m.sf, at.line * 16, at.block + g.blocks / 2, bar);
-        }
+        load_5d(w + i * 8 * g.K, &m.w, at.line, at.block, bar);
+        if (PHASE == 0) load_5d(w + i * 8 * g.K + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar);
       }
     }
     __syncwarp();
@@ -374,6 +368,41 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
       phase ^= 1u;
     }
   }
+}
+
+// The tile's scale lines, 16 bytes (four rows by four columns) a copy: per m16
+// tile and scale column / 4, the gate's two lines and the up's, or W2's four.
+template <int PHASE>
+__device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
+  const int lane = threadIdx.x & 31, line = lane & 3, cts = g.K / 64;
+  const uint8_t* all = PHASE == 0 ? p.sf13 : p.sf2;
+  uint32_t stage = 0, phase = 0;
+  Unit t = unit_at(u0, g.tiles);
+  for (int u = u0; u < u1; ++u) {
+    if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) break;
+    const int e = r->expert[t.v];
+    uint32_t to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + lane * 16;
+    for (int i = 0; i < g.R; ++i) {
+      const TileAt<PHASE> at(g, e, t.tile * g.R + i);
+      const int block = at.block + (PHASE == 0 ? (line >> 1) * (g.blocks / 2) : 0);
+      const uint8_t* from = all + ((int64_t)block * cts + (lane >> 2)) * 512 +
+                            (at.line + (PHASE == 0 ? line & 1 : line)) * 16;
+      for (int ct = lane >> 2; ct < cts; ct += 8, from += 8 * 512, to += 512)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+      // K = 64 * cts: the lanes past an odd end have made one copy less
+      to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + (i + 1) * g.K + lane * 16;
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(L.scales + 8 * stage) : "memory");
+    if (++stage == (uint32_t)g.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    if (++t.tile == g.tiles) {
+      t.tile = 0;
+      ++t.v;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // The first W2 tiles of this CTA's share of the second launch, into L2.
@@ -452,46 +481,62 @@ template <int PHASE, int SPW>
 __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
   const int kg = warp % g.KG, sub = warp / g.KG, slabs = g.K / 128;
-  // rows gr and gr + 8 of the m16 tile in a slab, and their scales
-  constexpr uint32_t slab_w = PHASE == 0 ? 512 : 1024, slab_s = PHASE == 0 ? 64 : 128;
-  const uint32_t w_off = sub * 8 * g.K + gr * 64 + ((q ^ (gr >> 1 & 3)) << 4);
-  const uint32_t w_off2 = w_off + (PHASE == 0 ? 4 * g.K : 512);
-  const uint32_t s_off = 8 * g.K * g.R + sub * g.K + (q >> 1) * (slab_s / 2) + (q & 1) * 2 +
-                         (PHASE == 0 ? (gr & 1) * 16 + (gr >> 1) * 4 : (gr & 3) * 16 + (gr >> 2) * 4);
-  const uint32_t s_off2 = s_off + (PHASE == 0 ? g.K / 2 : 8);
+  // this lane's two rows, slab by slab, and their scales
+  const int row = copied_row(gr, g.wide);
+  uint32_t w_off[SPW];
+#pragma unroll
+  for (int s = 0; s < SPW; ++s) {
+    const int slab = kg + s * g.KG;
+    w_off[s] = sub * 8 * g.K + (g.wide ? (slab >> 1) * (PHASE == 0 ? 1024 : 2048) + row * 128 +
+                                             ((((slab & 1) * 4 + q) ^ row) << 4)
+                                       : slab * (PHASE == 0 ? 512 : 1024) + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
+  }
+  const uint32_t second = PHASE == 0 ? 4 * g.K : g.wide ? 1024 : 512;
+  const uint32_t s_off = 8 * g.K * g.R + sub * g.K + kg * 128 + (q >> 1) * 64 + (q & 1) * 2 +
+                         (PHASE == 0 ? (row & 1) * 16 + (row >> 1) * 4 : (row & 3) * 16 + (row >> 2) * 4);
+  constexpr uint32_t s_second = PHASE == 0 ? 32 : 8;
   const uint32_t part = L.part + warp * 512 + lane * 16;
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
   uint32_t b[SPW][16];
   float i0 = 0.f, i1 = 0.f, alpha = 0.f;
-  int have = -1;
+  Unit t = unit_at(u0, g.tiles);
+  bool fresh = true;
   for (int u = u0; u < u1; ++u) {
-    const Unit t = unit_at(u, g.tiles);
-    if (t.v != have) {
-      have = t.v;
+    if (fresh) {
       alpha = 1.f / __ldg((PHASE == 0 ? p.gs13 : p.gs2) + r->expert[t.v]);
       const float inv = load_activations<PHASE, SPW>(p, g, r->member[t.v][gr], kg, q, b);
       i0 = __shfl_sync(0xffffffffu, inv, q * 8);
       i1 = __shfl_sync(0xffffffffu, inv, q * 8 + 4);
     }
-    if (!warp_wait(L.full + 8 * stage, phase, L.abort, p.status)) return;
+    // the tile has landed and a buffer for its sums is free: lanes 0, 1 and 2 ask
+    const uint32_t bar = lane == 0 ? L.full + 8 * stage : lane == 1 ? L.scales + 8 * stage : L.part_empty + 8 * buf;
+    if (!warp_wait_lanes(3, bar, lane < 2 ? phase : buf_phase, L.abort, p.status)) return;
     const uint32_t at = L.slots + stage * g.stage_bytes;
     float c[4] = {}, d[4] = {};
 #pragma unroll
-    for (int s = 0; s < SPW; ++s) {
-      const int slab = kg + s * g.KG;
-      if (slab < slabs) {
-        const uint4 w0 = lds128(at + w_off + slab * slab_w), w1 = lds128(at + w_off2 + slab * slab_w);
-        const uint32_t s0 = lds16(at + s_off + slab * slab_s), s1 = lds16(at + s_off2 + slab * slab_s);
-        mma_slab(c, d, w0, w1, s0, s1, b[s]);
+    for (int s = 0; s < SPW; s += 2) {  // two slabs' weights on their way at a time
+      const int sa = kg + s * g.KG, sb = sa + g.KG;
+      const bool has_a = sa < slabs, has_b = sb < slabs;
+      uint4 w[4];
+      uint32_t sc[4];
+      if (has_a) {
+        const uint32_t ss = at + s_off + s * g.KG * 128;
+        w[0] = lds128(at + w_off[s]), w[1] = lds128(at + w_off[s] + second);
+        sc[0] = lds16(ss), sc[1] = lds16(ss + s_second);
       }
+      if (has_b) {
+        const uint32_t ss = at + s_off + (s + 1) * g.KG * 128;
+        w[2] = lds128(at + w_off[s + 1]), w[3] = lds128(at + w_off[s + 1] + second);
+        sc[2] = lds16(ss), sc[3] = lds16(ss + s_second);
+      }
+      if (has_a) mma_slab(c, d, w[0], w[1], sc[0], sc[1], b[s]);
+      if (has_b) mma_slab(c, d, w[2], w[3], sc[2], sc[3], b[s + 1]);
     }
-    __syncwarp();
-    arrive_if(lane == 0, L.empty + 8 * stage);
-    if (!warp_wait(L.part_empty + 8 * buf, buf_phase, L.abort, p.status)) return;
     // alpha first: neither factor leaves FP32's range
     sts128(part + buf * (kWarps * 512), (c[0] + d[0]) * alpha * i0, (c[1] + d[1]) * alpha * i1,
            (c[2] + d[2]) * alpha * i0, (c[3] + d[3]) * alpha * i1);
     __syncwarp();
+    arrive_if(lane == 0, L.empty + 8 * stage);
     arrive_if(lane == 0, L.part_full + 8 * buf);
     if (++stage == (uint32_t)g.stages) {
       stage = 0;
@@ -500,6 +545,11 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
     if (++buf == kPartBufs) {
       buf = 0;
       buf_phase ^= 1u;
+    }
+    fresh = ++t.tile == g.tiles;
+    if (fresh) {
+      t.tile = 0;
+      ++t.v;
     }
   }
 }
@@ -533,7 +583,7 @@ __device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, cons
     }
 #pragma unroll
     for (int sub = 0; sub < R; ++sub) {
-      const int row = tile_row<PHASE>(t.tile * R + sub, gr);
+      const int row = tile_row<PHASE>(t.tile * R + sub, copied_row(gr, g.wide));
       if (PHASE == 0) {
         if (a0 >= 0) p.h[(int64_t)a0 * p.I + row] = swiglu(c[sub][0], c[sub][2], p.gate_limit, p.up_limit);
         if (a1 >= 0) p.h[(int64_t)a1 * p.I + row] = swiglu(c[sub][1], c[sub][3], p.gate_limit, p.up_limit);
@@ -564,33 +614,22 @@ __device__ void join_tiles(const FewArgs& p, const Phase& g, const Ring& L, cons
   }
 }
 
-// Second launch, after its tiles: a CTA counts each of them at its output tile
-// (the n_list-th to do so sums that tile's rows over the experts, j ascending,
-// so the order of arrival does not show).  Its own rows are published first.
-__device__ void count_tiles(const FewArgs& p, const Phase& g, const Route* r, int u0, int u1, int* s_mine,
-                            int* s_count) {
-  const int lane = threadIdx.x & 31;
-  __threadfence();
-  __syncwarp();
-  for (int u = u0 + lane; u < u1; u += 32) {
-    const int tile = unit_at(u, g.tiles).tile;
-    if (atomicAdd(p.done + tile, 1) == r->n_list - 1) s_mine[atomicAdd(s_count, 1)] = tile;
-  }
-  __threadfence();
-}
-
-__device__ void sum_tiles(const FewArgs& p, const Phase& g, const Route* r, const int* s_mine, int count) {
-  const int cols = 16 * g.R, per = p.T * cols;
-  for (int i = threadIdx.x; i < count * per; i += kThreads) {
-    const int tile = s_mine[i / per], t = i % per / cols, c = i % cols;
-    const int n = tile_row<1>(tile * g.R + (c >> 4), c & 15);
-    float sum = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      const int a = t * p.k + j;
-      if (r->id[a] >= 0) sum += __ldcg(p.y + (int64_t)a * p.H + n);
+// out[t] = bf16(the sum of the token's weighted rows, j ascending).
+__global__ void __launch_bounds__(256) few_sum_kernel(const FewArgs p) {
+  pdl_wait();
+  const int i = blockIdx.x * 256 + threadIdx.x, per = p.H / 4;  // four columns a thread
+  if (i >= p.T * per) return;
+  const int t = i / per, n = i - t * per;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < p.k; ++j) {
+    const int a = t * p.k + j;
+    if (p.ids[a] >= 0) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.y + (int64_t)a * p.H) + n);
+      sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
     }
-    p.out[(int64_t)t * p.H + n] = (uint16_t)pack_bf16x2(sum, sum);
   }
+  reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H)[n] = make_uint2(pack_bf16x2(sum.x, sum.y),
+                                                                     pack_bf16x2(sum.z, sum.w));
 }
 
 template <int PHASE, int SPW>
@@ -598,21 +637,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                                                            const Phase next) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Route route;
-  __shared__ uint64_t s_bars[2 * kMaxStages + 2 * kPartBufs];
-  __shared__ int s_abort, s_count;
-  __shared__ int s_mine[kFewMaxTiles];
+  __shared__ uint64_t s_bars[3 * kMaxStages + 2 * kPartBufs];
+  __shared__ int s_abort;
   const int warp = threadIdx.x >> 5;
   Ring L;
   L.slots = (smem_u32(smem) + 1023u) & ~1023u;
   L.part = L.slots + g.stages * g.stage_bytes;
   L.full = smem_u32(s_bars);
-  L.empty = L.full + 8 * kMaxStages;
+  L.scales = L.full + 8 * kMaxStages;
+  L.empty = L.scales + 8 * kMaxStages;
   L.part_full = L.empty + 8 * kMaxStages;
   L.part_empty = L.part_full + 8 * kPartBufs;
   L.abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) {
       mbar_init(L.full + 8 * i, 1);
+      mbar_init(L.scales + 8 * i, 32);
       mbar_init(L.empty + 8 * i, kWarps);
     }
     for (int i = 0; i < kPartBufs; ++i) {
@@ -620,18 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       mbar_init(L.part_empty + 8 * i, 1);
     }
     s_abort = 0;
-    s_count = 0;
     fence_mbar_init();
     prefetch_tmap(&m.w);
-    prefetch_tmap(&m.sf);
   }
   if (PHASE == 0) {
     pdl_wait();  // logits and activations may come from the kernel just before, and its caller may still use h
     pdl_trigger();
-    if (blockIdx.x == 0) {
-      if (threadIdx.x == 0) *p.status = 0;
-      for (int i = threadIdx.x; i < kFewMaxTiles; i += kThreads) p.done[i] = 0;
-    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     // on their way to L2 while the tokens are routed
     const int lines = (p.H + 63) / 64;
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.T * lines; i += gridDim.x * kThreads)
@@ -645,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   // that started only when whatever wrote it was complete.
   route_all(p, &route);
   __syncthreads();
+  if (PHASE == 0 && blockIdx.x == 0 && threadIdx.x < p.T * p.k) p.ids[threadIdx.x] = route.id[threadIdx.x];
   const int64_t units = (int64_t)route.n_list * g.tiles;
   const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
   if (warp < kWarps) {
@@ -656,24 +692,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     if (warp == kWarps) {
       if (PHASE == 1) pdl_wait();
       join_tiles<PHASE>(p, g, L, &route, u0, u1);
-      if (PHASE == 1) count_tiles(p, g, &route, u0, u1, s_mine, &s_count);
     } else if (warp == kWarps + 1) {
       copy_loop<PHASE>(p, m, g, L, &route, u0, u1);
       if (PHASE == 0) prefetch_w2(m, next, &route);
+    } else if (warp == kWarps + 2) {
+      scale_loop<PHASE>(p, g, L, &route, u0, u1);
     }
   }
-  __syncthreads();
-  if (PHASE == 1 && !s_abort) {
-    pdl_trigger();
-    if (route.n_list == 0) {  // no expert at all: zero rows
-      pdl_wait();
-      for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < (int64_t)p.T * p.H;
-           i += (int64_t)gridDim.x * kThreads)
-        p.out[i] = 0;
-    } else {
-      sum_tiles(p, g, &route, s_mine, s_count);
-    }
-  }
+  __syncthreads();  // no warp's copies outlive the CTA
 }
 
 Phase phase_of(int K, int m16_tiles, int blocks, size_t smem) {
@@ -684,6 +710,7 @@ Phase phase_of(int K, int m16_tiles, int blocks, size_t smem) {
   g.KG = kWarps / g.R;
   g.tiles = m16_tiles / g.R;  // 16 or more m16 tiles, in sixteens
   g.blocks = blocks;
+  g.wide = K % 256 == 0;
   g.stage_bytes = (9 * K * g.R + 1023) / 1024 * 1024;
   const int n = (int)((smem - 1024 - kPartBufs * kWarps * 512) / g.stage_bytes);
   g.stages = n < kMaxStages ? n : kMaxStages;
@@ -724,8 +751,10 @@ cudaError_t launch_phase(const FewArgs& a, const FewMaps& m, int K, int num_sms,
 cudaError_t launch_moe_few(const FewArgs& a, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s) {
   FewMaps m = w13;
   m.next_w = w2.w;
-  const cudaError_t e = launch_phase<0>(a, m, a.H, num_sms, s);
-  return e == cudaSuccess ? launch_phase<1>(a, w2, a.I, num_sms, s) : e;
+  cudaError_t e = launch_phase<0>(a, m, a.H, num_sms, s);
+  if (e == cudaSuccess) e = launch_phase<1>(a, w2, a.I, num_sms, s);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(few_sum_kernel, dim3((a.T * (a.H / 4) + 255) / 256), dim3(256), 0, s, true, a);
 }
 
 }  // namespace nvfp4

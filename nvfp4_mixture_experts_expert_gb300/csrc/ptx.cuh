@@ -168,6 +168,26 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return true;
 }
 
+// Waits for `count` barriers at once: lane i < count tests its own.
+__device__ __forceinline__ bool warp_wait_lanes(uint32_t count, uint32_t bar, uint32_t parity, volatile int* abort,
+                                                int* status) {
+  for (uint32_t n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.lt.u32 q, %3, %4;\nsetp.eq.b32 p, 0, 0;\n"
+        "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(threadIdx.x & 31), "r"(count)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (n % 256 == 0 && __any_sync(0xffffffffu, n >= kTries || *abort)) {
+      *abort = 1;
+      atomicExch(status, 6 /* NVFP4_ERR_DEVICE_TIMEOUT */);
+      return false;
+    }
+  }
+}
+
 // mbarrier.arrive by the lanes with `on` set, as a predicated instruction.
 __device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {
   asm volatile(
