@@ -2,8 +2,10 @@
 
 Each .cu file under csrc/ is compiled in parallel to an object with
 ``-gencode arch=compute_103a,code=sm_103a``, then linked into one shared
-library (static CUDA runtime) next to this file.  Rebuilds only when a
-source or header is newer than the library.
+library (static CUDA runtime) next to this file.  csrc/torch_calls.cpp, the
+host side of the short operators on torch's tensors, becomes an extension
+module linked to that library.  Rebuilds only when a source or header is newer
+than the two.
 """
 from __future__ import annotations
 
@@ -13,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
+EXT_SRC = os.path.join(CSRC, "torch_calls.cpp")
+EXT = os.path.join(PKG, "_torch_calls.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -34,14 +39,14 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + [EXT_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -55,6 +60,32 @@ def _compile(src, extra):
     return obj, r.stderr
 
 
+def _compile_ext():
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = [f"-I{d}" for d in cpp_extension.include_paths() + [cuda, sysconfig.get_paths()["include"]]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", EXT_SRC, "-o", obj,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + inc
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj):
+    from torch.utils import cpp_extension
+    tmp = EXT + ".tmp"
+    cmd = ["g++", "-shared", obj, "-o", tmp] + [f"-L{d}" for d in cpp_extension.library_paths() + [PKG]] + [
+        "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-ltorch_python", "-l:libnvfp4moe.so",
+        "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link libnvfp4moe.so; returns its path."""
     if not force and up_to_date():
@@ -62,18 +93,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra_flags)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
+        ext = ex.submit(_compile_ext)
         results = list(ex.map(lambda s: _compile(s, extra), sources()))
+        ext_obj = ext.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:
             if log.strip():
                 print(log, file=sys.stderr)
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), ARCH, "-shared", "-o", tmp] + objs
+    cmd = [nvcc(), ARCH, "-shared", "-Xlinker", "-soname=libnvfp4moe.so", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
 
 

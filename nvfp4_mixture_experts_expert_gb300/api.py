@@ -1,13 +1,17 @@
 """Torch-side convenience layer over the C ABI: allocates outputs and
-workspaces with torch on the current CUDA device and calls the binding.
-No arithmetic of the method happens here."""
+workspaces with torch on the current CUDA device and calls the binding (the
+operators of a few microseconds: the extension of csrc/torch_calls.cpp, which
+checks, allocates and calls in C++).  No arithmetic of the method happens here."""
 from __future__ import annotations
 
 from dataclasses import dataclass
 
 import torch
 
+from . import _torch_calls as C
 from . import binding as B
+
+C.set_error(B.Nvfp4Error)
 
 
 def _round_up(x, m):
@@ -198,41 +202,9 @@ class SharedExpertForward:
         return out
 
 
-_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
-
-
-def _empty(shape, dtype, device, stream):
-    """An output in the pool of the stream that will write it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-# The checks below run on every call of operators that take a few microseconds,
-# so they are plain expressions; _refuse finds the words when one fails.
-def _refuse(name, t, dtype, shape):
-    got = f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
-    raise ValueError(f"{name} must be a CUDA tensor {dtype} {shape} with contiguous rows, not {got}")
-
-
-def _rows(t, name, dtype, T, cols):
-    """Checks a CUDA matrix [T, cols] with contiguous rows; returns its row stride."""
-    if t.dtype is not dtype or t.shape != (T, cols) or not t.is_cuda or t.stride(1) != 1:
-        _refuse(name, t, dtype, (T, cols))
-    return t.stride(0) if T > 1 else cols
-
-
-def _whole(t, name, dtype, shape):
-    """Checks a contiguous CUDA tensor."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _refuse(name, t, dtype, shape)
+def _handle(stream):
+    """A CUDA stream as torch_calls takes it: None for the current one, else its handle."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def add_rms_norm_fp8(x, residual, weight, eps=1e-6, normed=True, quantized=True, residual_out=None, stream=None):
@@ -243,50 +215,19 @@ def add_rms_norm_fp8(x, residual, weight, eps=1e-6, normed=True, quantized=True,
     Returns (q, scales, y, s): float8_e4m3fn [T, H] and f32 [T, ceil(H/128)]
     (None with quantized=False), bf16 y (None with normed=False), bf16 s (None
     without a residual).  residual_out: where s goes; x or residual for in place."""
-    _need(x.dim() == 2, "x must have two dimensions")
-    T, H = shape = x.shape
-    ld_x = _rows(x, "x", _BF16, T, H)
-    dev = x.device
-    f32 = weight.dtype is _F32
-    _whole(weight, "weight", _F32 if f32 else _BF16, (H,))
-    ld_r = ld_o = 0
-    if residual is not None:
-        ld_r = _rows(residual, "residual", _BF16, T, H)
-        if residual_out is None:
-            residual_out = _empty(shape, _BF16, dev, stream)
-    if residual_out is not None:
-        ld_o = _rows(residual_out, "residual_out", _BF16, T, H)
-    y = _empty(shape, _BF16, dev, stream) if normed else None
-    q = scales = None
-    if quantized:
-        q = _empty(shape, _E4M3, dev, stream)
-        scales = _empty((T, (H + 127) // 128), _F32, dev, stream)
-    B.nvfp4_add_rmsnorm_fp8(x, ld_x, residual, ld_r, weight, f32, T, H, eps, residual_out, ld_o, y, q, scales, stream)
-    return q, scales, y, residual_out
+    return C.add_rms_norm_fp8(x, residual, weight, eps, normed, quantized, residual_out, _handle(stream))
 
 
 def fp8_linear(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stream=None):
     """a @ w.T of FP8 tensors with a scale for each block of 128 (see nvfp4_fp8_linear):
     a float8_e4m3fn [M, K] (rows may be strided) with a_scale f32 [M, ceil(K/128)],
     w float8_e4m3fn [N, K] with w_scale f32 [ceil(N/128), ceil(K/128)]; bf16 or f32 [M, N]."""
-    _need(a.dim() == 2 and w.dim() == 2, "a and w must have two dimensions")
-    M, K = a.shape
-    N = w.shape[0]
-    kb = (K + 127) // 128
-    ld_a = _rows(a, "a", _E4M3, M, K)
-    _whole(w, "w", _E4M3, (N, K))
-    _whole(a_scale, "a_scale", _F32, (M, kb))
-    _whole(w_scale, "w_scale", _F32, ((N + 127) // 128, kb))
     if out is not None:
         out_dtype = out.dtype
-    f32 = out_dtype is _F32
-    _need(f32 or out_dtype is _BF16, "the output must be bfloat16 or float32")
-    if out is None:
-        out, ld_out = _empty((M, N), out_dtype, a.device, stream), N
-    else:
-        ld_out = _rows(out, "out", out_dtype, M, N)
-    B.nvfp4_fp8_linear(a, ld_a, a_scale, w, w_scale, M, N, K, out, ld_out, f32, stream)
-    return out
+    f32 = out_dtype is torch.float32
+    if not f32 and out_dtype is not torch.bfloat16:
+        raise ValueError(f"the output must be bfloat16 or float32, not {out_dtype}")
+    return C.fp8_linear(a, a_scale, w, w_scale, f32, out, _handle(stream))
 
 
 class MoEFewTokens:
@@ -294,46 +235,25 @@ class MoEFewTokens:
     (see nvfp4_moe_few_tokens), with its workspace: one call at a time."""
 
     def __init__(self, T, H, I, E, top_k, device="cuda"):
-        self.T, self.H, self.I, self.E, self.top_k = T, H, I, E, top_k
+        self.T, self.H, self.I, self.E, self.top_k = self.sizes = T, H, I, E, top_k
         self.ws_bytes = B.nvfp4_moe_few_tokens_workspace_size(T, H, I, E, top_k)
-        _need(self.ws_bytes > 0, f"unsupported sizes: T={T} H={H} I={I} E={E} top_k={top_k}")
+        if self.ws_bytes == 0:
+            raise ValueError(f"unsupported sizes: T={T} H={H} I={I} E={E} top_k={top_k}")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-
-    def _check(self, hidden, w, out, stream):
-        H, I, E = self.H, self.I, self.E
-        T = hidden.shape[0]
-        ld = _rows(hidden, "hidden", _BF16, T, H)
-        _need(T <= self.T, f"{T} tokens; this layer was made for {self.T}")
-        _whole(w.w13, "w13", torch.uint8, (E, 2 * I, H // 2))
-        _whole(w.w2, "w2", torch.uint8, (E, H, I // 2))
-        _need(w.w13_sf.numel() == E * I * (H // 8) and w.w2_sf.numel() == E * H * (I // 16) and
-              w.w13_gs.numel() == E and w.w2_gs.numel() == E, "weight scales of another layer")
-        if out is None:
-            out = _empty((T, H), _BF16, hidden.device, stream)
-        else:
-            _whole(out, "out", _BF16, (T, H))
-        return T, ld, out
 
     def __call__(self, hidden, logits, w: MoEWeights, gate_limit=10.0, up_limit=10.0, out=None, stream=None):
         """hidden bf16 [t, H], t <= T (rows may be strided); logits f32 [t, E]."""
-        T, ld, out = self._check(hidden, w, out, stream)
-        _whole(logits, "logits", _F32, (T, self.E))
-        B.nvfp4_moe_few_tokens(hidden, ld, logits, T, self.H, self.I, self.E, self.top_k, w.w13, w.w13_sf, w.w13_gs,
-                               w.w2, w.w2_sf, w.w2_gs, gate_limit, up_limit, self.workspace, self.ws_bytes, out,
-                               stream)
-        return out
+        return C.moe_few_tokens(hidden, logits, None, None, 0, self.sizes,
+                                (w.w13, w.w13_sf, w.w13_gs, w.w2, w.w2_sf, w.w2_gs), gate_limit, up_limit,
+                                self.workspace, out, _handle(stream))
 
     def routed(self, hidden, topk_ids, topk_weights, experts_start, w: MoEWeights, gate_limit=10.0, up_limit=10.0,
                out=None, stream=None):
         """The layer from the model router's global top-k (int32 / f32 [t, k]); it
         holds the experts [experts_start, experts_start + E)."""
-        T, ld, out = self._check(hidden, w, out, stream)
-        _whole(topk_ids, "topk_ids", torch.int32, (T, self.top_k))
-        _whole(topk_weights, "topk_weights", _F32, (T, self.top_k))
-        B.nvfp4_moe_few_tokens_routed(hidden, ld, topk_ids, topk_weights, experts_start, T, self.H, self.I, self.E,
-                                      self.top_k, w.w13, w.w13_sf, w.w13_gs, w.w2, w.w2_sf, w.w2_gs, gate_limit,
-                                      up_limit, self.workspace, self.ws_bytes, out, stream)
-        return out
+        return C.moe_few_tokens(hidden, None, topk_ids, topk_weights, experts_start, self.sizes,
+                                (w.w13, w.w13_sf, w.w13_gs, w.w2, w.w2_sf, w.w2_gs), gate_limit, up_limit,
+                                self.workspace, out, _handle(stream))
 
     def status(self, stream=None, reset=False):
         """Device status word of the last call on this workspace (waits for the stream)."""
