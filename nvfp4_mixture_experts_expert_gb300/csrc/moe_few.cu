@@ -22,12 +22,12 @@
 // line, so the rows of an m16 tile are taken as whole lines: W13, 2 lines of
 // gate rows and the same 2 of up rows (8 features; gate in accumulator rows
 // 0-7, up in rows 8-15, so a lane holds both of its feature); W2, 4 lines.
-// A tensor map with the dimensions (64 or 128 bytes of a row, line, row of the
-// line, piece of the row, 128-row block) then brings all of a tile's rows, piece
-// by piece, in one or two copies; row by row, a warp's issue of the copies took
-// longer than their arrival.  The copy engine takes about as long for 64 bytes
-// of a row as for 128, so the pieces are 128 bytes where K % 256 == 0.  The
-// swizzle of the piece's width makes the consumers' reads conflict-free.
+// A tensor map with the dimensions (8 bytes of a row, line, row of the line,
+// 128-row block) then brings all of a tile's rows in one or two copies, row by
+// row: pieces of up to 2 KB, as HBM likes them.  (Slab by slab over the rows,
+// in the order that a swizzle wants, the same copies ran at 4.4 TB/s.)  The rows
+// lie in the same banks and two of them share each cycle of a consumers' read, at
+// a quarter of the shared memory's rate.
 //
 // Two launches of one kernel, h between them, and a sum; one CTA per SM, which takes an
 // equal share of the (list entry, tile) pairs in order, so that it changes
@@ -63,7 +63,7 @@ constexpr int kRegsConsumer = 104; // with four slabs a warp: 64 of them activat
 constexpr int kRegsOther = 64;
 static_assert(128 * (4 * kRegsConsumer + kRegsOther) <= kThreads * kRegsLaunch, "the register split must fit");
 constexpr int kMaxStages = 16;
-constexpr int kPartBufs = 3;       // tiles whose sums wait to be joined
+constexpr int kPartBufs = 4;       // tiles whose sums wait to be joined
 constexpr int kPrefetch = 6;       // W2 tiles a CTA of the first launch brings into L2
 constexpr int kGroup = 8;  // tokens of one list entry
 
@@ -268,17 +268,13 @@ __device__ __forceinline__ int tile_row(int st, int r) {
   return PHASE == 0 ? (st >> 4) * 128 + (st & 15) * 2 + (r & 1) + 32 * (r >> 1)
                     : (st >> 3) * 128 + (st & 7) * 4 + (r & 3) + 32 * (r >> 2);
 }
-// The copied row that accumulator row g (0-7) takes.  With 128-byte pieces, two
-// rows that eight lanes read together have to differ in bit 2 to miss each
-// other's banks under the swizzle.
-__device__ __forceinline__ int copied_row(int g, int wide) { return wide ? (g & 1) << 2 | g >> 1 : g; }
 
 // What a launch needs to know of its product (0: W13 x, 1: W2 h).
 struct Phase {
   int K, R, KG;       // R m16 tiles a tile, KG = 16 / R warps along K
   int tiles;          // per list entry
   int blocks;         // 128-row blocks of an expert's matrix
-  int wide;           // 128-byte pieces of a row, else 64
+  int piece;          // bytes of a row that one copy takes: K / 2, or half of it
   int stage_bytes, stages;
 };
 
@@ -325,12 +321,15 @@ struct TileAt {
       : line(PHASE == 0 ? (st & 15) * 2 : (st & 7) * 4), block(e * g.blocks + (PHASE == 0 ? st >> 4 : st >> 3)) {}
 };
 
-__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, int line, int block, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %2, "
-      "%4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(block), "r"(bar)
-      : "memory");
+// All rows of a box, piece by piece: [piece][row of the line][line][bytes].
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, const Phase& g, int rows, int line,
+                                          int block, uint32_t bar) {
+  for (int x = 0; x < g.K / 2; x += g.piece, dst += rows * g.piece)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x / 8), "r"(line), "r"(0), "r"(block), "r"(bar)
+        : "memory");
 }
 template <int PHASE>
 __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, const Ring& L, const Route* r, int u0,
@@ -356,8 +355,8 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
       mbar_arrive_expect_tx(bar, 8 * g.K * g.R);
       for (int i = 0; i < g.R; ++i) {
         const TileAt<PHASE> at(g, e, t.tile * g.R + i);
-        load_5d(w + i * 8 * g.K, &m.w, at.line, at.block, bar);
-        if (PHASE == 0) load_5d(w + i * 8 * g.K + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar);
+        load_rows(w + i * 8 * g.K, &m.w, g, PHASE == 0 ? 8 : 16, at.line, at.block, bar);
+        if (PHASE == 0) load_rows(w + i * 8 * g.K + 4 * g.K, &m.w, g, 8, at.line, at.block + g.blocks / 2, bar);
       }
     }
     __syncwarp();
@@ -388,7 +387,7 @@ __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, cons
       const uint8_t* from = all + ((int64_t)block * cts + (lane >> 2)) * 512 +
                             (at.line + (PHASE == 0 ? line & 1 : line)) * 16;
       for (int ct = lane >> 2; ct < cts; ct += 8, from += 8 * 512, to += 512)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
       // K = 64 * cts: the lanes past an odd end have made one copy less
       to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + (i + 1) * g.K + lane * 16;
     }
@@ -414,10 +413,11 @@ __device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
     const Unit t = unit_at(u, g.tiles);
     for (int i = 0; i < g.R; ++i) {
       const TileAt<1> at(g, r->expert[t.v], t.tile * g.R + i);
-      asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %1, %1, %3}];" ::"l"(
-                       reinterpret_cast<uint64_t>(&m.next_w)),
-                   "r"(0), "r"(at.line), "r"(at.block)
-                   : "memory");
+      for (int x = 0; x < g.K / 2; x += g.piece)
+        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                         reinterpret_cast<uint64_t>(&m.next_w)),
+                     "r"(x / 8), "r"(at.line), "r"(0), "r"(at.block)
+                     : "memory");
     }
   }
 }
@@ -481,19 +481,17 @@ template <int PHASE, int SPW>
 __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
   const int kg = warp % g.KG, sub = warp / g.KG, slabs = g.K / 128;
-  // this lane's two rows, slab by slab, and their scales
-  const int row = copied_row(gr, g.wide);
+  // this lane's two rows (gr of the first copy and of the second, or gr and
+  // gr + 8 of the one), slab by slab, and their scales
   uint32_t w_off[SPW];
 #pragma unroll
   for (int s = 0; s < SPW; ++s) {
-    const int slab = kg + s * g.KG;
-    w_off[s] = sub * 8 * g.K + (g.wide ? (slab >> 1) * (PHASE == 0 ? 1024 : 2048) + row * 128 +
-                                             ((((slab & 1) * 4 + q) ^ row) << 4)
-                                       : slab * (PHASE == 0 ? 512 : 1024) + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
+    const int x = (kg + s * g.KG) * 64, piece = x / g.piece;
+    w_off[s] = sub * 8 * g.K + (piece * (PHASE == 0 ? 8 : 16) + gr) * g.piece + (x - piece * g.piece) + q * 16;
   }
-  const uint32_t second = PHASE == 0 ? 4 * g.K : g.wide ? 1024 : 512;
+  const uint32_t second = PHASE == 0 ? 4 * g.K : 8 * g.piece;
   const uint32_t s_off = 8 * g.K * g.R + sub * g.K + kg * 128 + (q >> 1) * 64 + (q & 1) * 2 +
-                         (PHASE == 0 ? (row & 1) * 16 + (row >> 1) * 4 : (row & 3) * 16 + (row >> 2) * 4);
+                         (PHASE == 0 ? (gr & 1) * 16 + (gr >> 1) * 4 : (gr & 3) * 16 + (gr >> 2) * 4);
   constexpr uint32_t s_second = PHASE == 0 ? 32 : 8;
   const uint32_t part = L.part + warp * 512 + lane * 16;
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
@@ -501,55 +499,74 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
   float i0 = 0.f, i1 = 0.f, alpha = 0.f;
   Unit t = unit_at(u0, g.tiles);
   bool fresh = true;
-  for (int u = u0; u < u1; ++u) {
+  for (int u = u0; u < u1;) {
     if (fresh) {
       alpha = 1.f / __ldg((PHASE == 0 ? p.gs13 : p.gs2) + r->expert[t.v]);
       const float inv = load_activations<PHASE, SPW>(p, g, r->member[t.v][gr], kg, q, b);
       i0 = __shfl_sync(0xffffffffu, inv, q * 8);
       i1 = __shfl_sync(0xffffffffu, inv, q * 8 + 4);
     }
-    // the tile has landed and a buffer for its sums is free: lanes 0, 1 and 2 ask
-    const uint32_t bar = lane == 0 ? L.full + 8 * stage : lane == 1 ? L.scales + 8 * stage : L.part_empty + 8 * buf;
-    if (!warp_wait_lanes(3, bar, lane < 2 ? phase : buf_phase, L.abort, p.status)) return;
-    const uint32_t at = L.slots + stage * g.stage_bytes;
-    float c[4] = {}, d[4] = {};
+    // Two tiles at a time while the list entry lasts: waiting, handing over the
+    // sums and coming back cost about half of what one tile's products take.
+    // Both have landed and buffers for their sums are free: six lanes ask.
+    const int n = min(2, min(u1 - u, g.tiles - t.tile));
+    const uint32_t stage2 = stage + 1 == (uint32_t)g.stages ? 0u : stage + 1, phase2 = stage2 ? phase : phase ^ 1u;
+    const uint32_t buf2 = buf + 1 == kPartBufs ? 0u : buf + 1, buf_phase2 = buf2 ? buf_phase : buf_phase ^ 1u;
+    {
+      const bool second = lane >= 3;
+      const uint32_t kind = second ? lane - 3 : lane, slot = second ? stage2 : stage;
+      const uint32_t bar = kind == 0 ? L.full + 8 * slot : kind == 1 ? L.scales + 8 * slot
+                                                                     : L.part_empty + 8 * (second ? buf2 : buf);
+      const uint32_t parity = kind < 2 ? (second ? phase2 : phase) : (second ? buf_phase2 : buf_phase);
+      if (!warp_wait_lanes(3 * n, bar, parity, L.abort, p.status)) return;
+    }
 #pragma unroll
-    for (int s = 0; s < SPW; s += 2) {  // two slabs' weights on their way at a time
-      const int sa = kg + s * g.KG, sb = sa + g.KG;
-      const bool has_a = sa < slabs, has_b = sb < slabs;
-      uint4 w[4];
-      uint32_t sc[4];
-      if (has_a) {
-        const uint32_t ss = at + s_off + s * g.KG * 128;
-        w[0] = lds128(at + w_off[s]), w[1] = lds128(at + w_off[s] + second);
-        sc[0] = lds16(ss), sc[1] = lds16(ss + s_second);
+    for (int i = 0; i < 2; ++i) {
+      if (i == n) break;
+      const uint32_t at = L.slots + (i ? stage2 : stage) * g.stage_bytes;
+      float c[4] = {}, d[4] = {};
+#pragma unroll
+      for (int s = 0; s < SPW; s += 2) {  // two slabs' weights on their way at a time
+        const int sa = kg + s * g.KG, sb = sa + g.KG;
+        const bool has_a = sa < slabs, has_b = sb < slabs;
+        uint4 w[4];
+        uint32_t sc[4];
+        if (has_a) {
+          const uint32_t ss = at + s_off + s * g.KG * 128;
+          w[0] = lds128(at + w_off[s]), w[1] = lds128(at + w_off[s] + second);
+          sc[0] = lds16(ss), sc[1] = lds16(ss + s_second);
+        }
+        if (has_b) {
+          const uint32_t ss = at + s_off + (s + 1) * g.KG * 128;
+          w[2] = lds128(at + w_off[s + 1]), w[3] = lds128(at + w_off[s + 1] + second);
+          sc[2] = lds16(ss), sc[3] = lds16(ss + s_second);
+        }
+        if (has_a) mma_slab(c, d, w[0], w[1], sc[0], sc[1], b[s]);
+        if (has_b) mma_slab(c, d, w[2], w[3], sc[2], sc[3], b[s + 1]);
       }
-      if (has_b) {
-        const uint32_t ss = at + s_off + (s + 1) * g.KG * 128;
-        w[2] = lds128(at + w_off[s + 1]), w[3] = lds128(at + w_off[s + 1] + second);
-        sc[2] = lds16(ss), sc[3] = lds16(ss + s_second);
-      }
-      if (has_a) mma_slab(c, d, w[0], w[1], sc[0], sc[1], b[s]);
-      if (has_b) mma_slab(c, d, w[2], w[3], sc[2], sc[3], b[s + 1]);
+      // alpha first: neither factor leaves FP32's range
+      sts128(part + (i ? buf2 : buf) * (kWarps * 512), (c[0] + d[0]) * alpha * i0, (c[1] + d[1]) * alpha * i1,
+             (c[2] + d[2]) * alpha * i0, (c[3] + d[3]) * alpha * i1);
+      __syncwarp();
+      arrive_if(lane == 0, L.empty + 8 * (i ? stage2 : stage));
+      arrive_if(lane == 0, L.part_full + 8 * (i ? buf2 : buf));
     }
-    // alpha first: neither factor leaves FP32's range
-    sts128(part + buf * (kWarps * 512), (c[0] + d[0]) * alpha * i0, (c[1] + d[1]) * alpha * i1,
-           (c[2] + d[2]) * alpha * i0, (c[3] + d[3]) * alpha * i1);
-    __syncwarp();
-    arrive_if(lane == 0, L.empty + 8 * stage);
-    arrive_if(lane == 0, L.part_full + 8 * buf);
-    if (++stage == (uint32_t)g.stages) {
-      stage = 0;
-      phase ^= 1u;
-    }
-    if (++buf == kPartBufs) {
-      buf = 0;
-      buf_phase ^= 1u;
-    }
-    fresh = ++t.tile == g.tiles;
+    u += n;
+    t.tile += n;
+    fresh = t.tile == g.tiles;
     if (fresh) {
       t.tile = 0;
       ++t.v;
+    }
+    stage += n;
+    if (stage >= (uint32_t)g.stages) {
+      stage -= g.stages;
+      phase ^= 1u;
+    }
+    buf += n;
+    if (buf >= kPartBufs) {
+      buf -= kPartBufs;
+      buf_phase ^= 1u;
     }
   }
 }
@@ -583,7 +600,7 @@ __device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, cons
     }
 #pragma unroll
     for (int sub = 0; sub < R; ++sub) {
-      const int row = tile_row<PHASE>(t.tile * R + sub, copied_row(gr, g.wide));
+      const int row = tile_row<PHASE>(t.tile * R + sub, gr);
       if (PHASE == 0) {
         if (a0 >= 0) p.h[(int64_t)a0 * p.I + row] = swiglu(c[sub][0], c[sub][2], p.gate_limit, p.up_limit);
         if (a1 >= 0) p.h[(int64_t)a1 * p.I + row] = swiglu(c[sub][1], c[sub][3], p.gate_limit, p.up_limit);
@@ -710,7 +727,7 @@ Phase phase_of(int K, int m16_tiles, int blocks, size_t smem) {
   g.KG = kWarps / g.R;
   g.tiles = m16_tiles / g.R;  // 16 or more m16 tiles, in sixteens
   g.blocks = blocks;
-  g.wide = K % 256 == 0;
+  g.piece = few_piece(K);
   g.stage_bytes = (9 * K * g.R + 1023) / 1024 * 1024;
   const int n = (int)((smem - 1024 - kPartBufs * kWarps * 512) / g.stage_bytes);
   g.stages = n < kMaxStages ? n : kMaxStages;
