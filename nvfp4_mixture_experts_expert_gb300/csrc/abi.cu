@@ -116,18 +116,20 @@ int make_byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
 }
 
 // Packed FP4 matrices [rows][K/2] as the few-token layer copies them
-// (moe_few.cu): `lines` rows r, r+1, .. and r+32, r+64, r+96 on, few_piece(K)
-// bytes of each.
+// (moe_few.cu): `lines` rows r, r+1, .. and r+32, r+64, r+96 on, over all of K in
+// pieces of 128 bytes where they fit a row, else of 64, swizzled in that width.
 int make_few_map(CUtensorMap* m, const void* w, int64_t rows, int64_t K, int lines) {
   auto fn = encode_fn();
   if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const cuuint32_t piece = K % 256 ? 64 : 128;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const cuuint64_t row = (cuuint64_t)(K / 2);
-  const cuuint64_t dims[4] = {row / 8, 32, 4, (cuuint64_t)(rows / 128)};
-  const cuuint64_t strides[3] = {row, 32 * row, 128 * row};
-  const cuuint32_t box[4] = {(cuuint32_t)(few_piece(K) / 8), (cuuint32_t)lines, 4, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, const_cast<void*>(w), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+  const cuuint64_t dims[5] = {piece, 32, 4, row / piece, (cuuint64_t)(rows / 128)};
+  const cuuint64_t strides[4] = {row, 32 * row, piece, 128 * row};
+  const cuuint32_t box[5] = {piece, (cuuint32_t)lines, 4, (cuuint32_t)(row / piece), 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(w), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        piece == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return NVFP4_OK;

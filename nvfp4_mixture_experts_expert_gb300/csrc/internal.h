@@ -289,9 +289,6 @@ struct FewArgs {
 };
 // Tensor maps of one product's weights (the box of an m16 tile, see moe_few.cu)
 // and of the next product's.
-// Bytes of a weight row that one copy takes (a box has 256 elements of 8 bytes at
-// most; K <= 8192, and half of a longer row is a multiple of 64 bytes).
-inline int few_piece(int64_t K) { return (int)(K / 2 <= 2048 ? K / 2 : K / 4); }
 struct FewMaps {
   CUtensorMap w, next_w;
 };

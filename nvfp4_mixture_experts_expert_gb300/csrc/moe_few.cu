@@ -22,12 +22,14 @@
 // line, so the rows of an m16 tile are taken as whole lines: W13, 2 lines of
 // gate rows and the same 2 of up rows (8 features; gate in accumulator rows
 // 0-7, up in rows 8-15, so a lane holds both of its feature); W2, 4 lines.
-// A tensor map with the dimensions (8 bytes of a row, line, row of the line,
-// 128-row block) then brings all of a tile's rows in one or two copies, row by
-// row: pieces of up to 2 KB, as HBM likes them.  (Slab by slab over the rows,
-// in the order that a swizzle wants, the same copies ran at 4.4 TB/s.)  The rows
-// lie in the same banks and two of them share each cycle of a consumers' read, at
-// a quarter of the shared memory's rate.
+// A tensor map with the dimensions (64 or 128 bytes of a row, line, row of the
+// line, piece of the row, 128-row block) then brings all of a tile's rows, piece
+// by piece, in one or two copies; row by row, a warp's issue of the copies took
+// longer than their arrival.  The copy engine takes about as long for 64 bytes
+// of a row as for 128, so the pieces are 128 bytes where K % 256 == 0.  The
+// swizzle of the piece's width makes the consumers' reads conflict-free (whole
+// rows come in as fast, but two rows then share the banks of each read: 870
+// cycles of shared memory a tile instead of 375, of the 1,600 a tile may take).
 //
 // Two launches of one kernel, h between them, and a sum; one CTA per SM, which takes an
 // equal share of the (list entry, tile) pairs in order, so that it changes
@@ -35,11 +37,11 @@
 // over all of K.  Its warps:
 //   16 consumers     KG = 16 / R of them share an m16 tile and split K by slabs;
 //                    their activations stay in registers while the entry lasts
-//   warp 16          joins the KG sums in a fixed order; SwiGLU, or the weighted
-//                    row of W2 h
-//   warp 17          the weights' copies into the ring
-//   warp 18          the scales', 16 bytes a line: as 32-byte pieces they would
+//   warp 16          the weights' copies into the ring
+//   warp 17          the scales', 16 bytes a line: as 32-byte pieces they would
 //                    be a third of the copy engine's work
+//   warps 18, 19     tile by tile in turn: join the KG sums in a fixed order;
+//                    SwiGLU, or the weighted row of W2 h
 // Every CTA routes for itself (a microsecond, no launch in between).  The second
 // launch starts as CTAs of the first leave (programmatic dependent launch) and
 // fills its rings before it waits for h, and the first asks for the second's
@@ -59,10 +61,11 @@ namespace {
 constexpr int kWarps = 16;  // consumers
 constexpr int kThreads = 32 * (kWarps + 4);
 constexpr int kRegsLaunch = 96;    // per thread; 61,440 of the SM's 65,536 registers
-constexpr int kRegsConsumer = 104; // with four slabs a warp: 64 of them activations
+constexpr int kRegsConsumer = 104; // 32 of them activations, with four slabs a warp 64
 constexpr int kRegsOther = 64;
 static_assert(128 * (4 * kRegsConsumer + kRegsOther) <= kThreads * kRegsLaunch, "the register split must fit");
 constexpr int kMaxStages = 16;
+constexpr int kJoinWarps = 2;
 constexpr int kPartBufs = 4;       // tiles whose sums wait to be joined
 constexpr int kPrefetch = 6;       // W2 tiles a CTA of the first launch brings into L2
 constexpr int kGroup = 8;  // tokens of one list entry
@@ -222,22 +225,33 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The lane's 32 weights of two rows (words in K order, the rows' two scales)
-// times its 32 activations of one token, over the quad: 128 of K.  Two sums, so
-// that a product does not wait for the one before it.
-__device__ __forceinline__ void mma_slab(float (&c)[4], float (&d)[4], const uint4& w0, const uint4& w1, uint32_t sc0, uint32_t sc1,
-                                         const uint32_t (&b)[16]) {
-  uint32_t s[2][2];
-  scale_pairs(sc0, s[0][0], s[0][1]);
-  scale_pairs(sc1, s[1][0], s[1][1]);
-  const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+// The lane's 32 weights of two rows of two tiles (words in K order, the rows' two
+// scales) times its 32 activations of one token, over the quad: 128 of K.  Two
+// sums a tile, so that a product does not wait for the one before it.
+// Decoding is what the consumers do: a pair of weights takes a conversion (2
+// cycles of the ALU pipe) and a multiplication (2 of the FP16 pipe), 3 together.
+__device__ __forceinline__ void mma_slab(float (&c)[2][4], float (&d)[2][4], const uint4 (&w)[2][2],
+                                         const uint32_t (&sc)[2][2], const uint32_t (&b)[16]) {
+  uint32_t s[2][2][2], x[2][2][4];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      scale_pairs(sc[t][r], s[t][r][0], s[t][r][1]);
+      x[t][r][0] = w[t][r].x, x[t][r][1] = w[t][r].y, x[t][r][2] = w[t][r].z, x[t][r][3] = w[t][r].w;
+    }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t r0[4], r1[4];
-    decode8(x0[i], s[0][i >> 1], r0);
-    decode8(x1[i], s[1][i >> 1], r1);
-    mma_f16(c, r0[0], r1[0], r0[1], r1[1], b[4 * i], b[4 * i + 1]);
-    mma_f16(d, r0[2], r1[2], r0[3], r1[3], b[4 * i + 2], b[4 * i + 3]);
+    uint32_t f[2][2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) decode8(x[t][r][i], s[t][r][i >> 1], f[t][r]);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) mma_f16(c[t], f[t][0][0], f[t][1][0], f[t][0][1], f[t][1][1], b[4 * i], b[4 * i + 1]);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      mma_f16(d[t], f[t][0][2], f[t][1][2], f[t][0][3], f[t][1][3], b[4 * i + 2], b[4 * i + 3]);
   }
 }
 
@@ -254,10 +268,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// 2 ulp in the quotient; a denominator past 2^126 gives 0 for a gate below -87.
 __device__ __forceinline__ float swiglu(float gate, float up, float gate_limit, float up_limit) {
   gate = clamp_up(gate, gate_limit);
   up = -clamp_up(-clamp_up(up, up_limit), up_limit);
-  return gate / (1.f + expf(-gate)) * up;
+  return __fdividef(gate, 1.f + expf(-gate)) * up;
 }
 
 // Where row r of m16 tile `st` lies in the order of its copy (line fastest):
@@ -268,13 +283,17 @@ __device__ __forceinline__ int tile_row(int st, int r) {
   return PHASE == 0 ? (st >> 4) * 128 + (st & 15) * 2 + (r & 1) + 32 * (r >> 1)
                     : (st >> 3) * 128 + (st & 7) * 4 + (r & 3) + 32 * (r >> 2);
 }
+// The copied row that accumulator row g (0-7) takes.  With 128-byte pieces, two
+// rows that eight lanes read together have to differ in bit 2 to miss each
+// other's banks under the swizzle.
+__device__ __forceinline__ int copied_row(int g, int wide) { return wide ? (g & 1) << 2 | g >> 1 : g; }
 
 // What a launch needs to know of its product (0: W13 x, 1: W2 h).
 struct Phase {
   int K, R, KG;       // R m16 tiles a tile, KG = 16 / R warps along K
   int tiles;          // per list entry
   int blocks;         // 128-row blocks of an expert's matrix
-  int piece;          // bytes of a row that one copy takes: K / 2, or half of it
+  int wide;           // 128-byte pieces of a row, else 64
   int stage_bytes, stages;
 };
 
@@ -288,6 +307,13 @@ struct Ring {
 // The list entry and tile of unit u.
 struct Unit {
   int v, tile;
+  __device__ __forceinline__ void advance(int n, int tiles) {  // n <= tiles
+    tile += n;
+    if (tile >= tiles) {
+      tile -= tiles;
+      ++v;
+    }
+  }
 };
 __device__ __forceinline__ Unit unit_at(int u, int tiles) {
   const int v = u / tiles;
@@ -321,23 +347,22 @@ struct TileAt {
       : line(PHASE == 0 ? (st & 15) * 2 : (st & 7) * 4), block(e * g.blocks + (PHASE == 0 ? st >> 4 : st >> 3)) {}
 };
 
-// All rows of a box, piece by piece: [piece][row of the line][line][bytes].
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, const Phase& g, int rows, int line,
-                                          int block, uint32_t bar) {
-  for (int x = 0; x < g.K / 2; x += g.piece, dst += rows * g.piece)
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x / 8), "r"(line), "r"(0), "r"(block), "r"(bar)
-        : "memory");
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, int line, int block, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %2, "
+      "%4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(block), "r"(bar)
+      : "memory");
 }
+
 template <int PHASE>
 __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, const Ring& L, const Route* r, int u0,
                           int u1) {
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
-  for (int u = u0; u < u1; ++u) {
+  Unit t = unit_at(u0, g.tiles);
+  for (int u = u0; u < u1; ++u, t.advance(1, g.tiles)) {
     if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) {
       // copies in flight land before the CTA leaves its shared memory
       for (int s = 0; s < g.stages; ++s)
@@ -348,15 +373,14 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
       __syncwarp();
       return;
     }
-    const Unit t = unit_at(u, g.tiles);
     const int e = r->expert[t.v];
     if (leader) {
       const uint32_t w = L.slots + stage * g.stage_bytes, bar = L.full + 8 * stage;
       mbar_arrive_expect_tx(bar, 8 * g.K * g.R);
       for (int i = 0; i < g.R; ++i) {
         const TileAt<PHASE> at(g, e, t.tile * g.R + i);
-        load_rows(w + i * 8 * g.K, &m.w, g, PHASE == 0 ? 8 : 16, at.line, at.block, bar);
-        if (PHASE == 0) load_rows(w + i * 8 * g.K + 4 * g.K, &m.w, g, 8, at.line, at.block + g.blocks / 2, bar);
+        load_5d(w + i * 8 * g.K, &m.w, at.line, at.block, bar);
+        if (PHASE == 0) load_5d(w + i * 8 * g.K + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar);
       }
     }
     __syncwarp();
@@ -377,7 +401,7 @@ __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, cons
   const uint8_t* all = PHASE == 0 ? p.sf13 : p.sf2;
   uint32_t stage = 0, phase = 0;
   Unit t = unit_at(u0, g.tiles);
-  for (int u = u0; u < u1; ++u) {
+  for (int u = u0; u < u1; ++u, t.advance(1, g.tiles)) {
     if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) break;
     const int e = r->expert[t.v];
     uint32_t to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + lane * 16;
@@ -396,10 +420,6 @@ __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, cons
       stage = 0;
       phase ^= 1u;
     }
-    if (++t.tile == g.tiles) {
-      t.tile = 0;
-      ++t.v;
-    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -413,11 +433,10 @@ __device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
     const Unit t = unit_at(u, g.tiles);
     for (int i = 0; i < g.R; ++i) {
       const TileAt<1> at(g, r->expert[t.v], t.tile * g.R + i);
-      for (int x = 0; x < g.K / 2; x += g.piece)
-        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                         reinterpret_cast<uint64_t>(&m.next_w)),
-                     "r"(x / 8), "r"(at.line), "r"(0), "r"(at.block)
-                     : "memory");
+      asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %1, %1, %3}];" ::"l"(
+                       reinterpret_cast<uint64_t>(&m.next_w)),
+                   "r"(0), "r"(at.line), "r"(at.block)
+                   : "memory");
     }
   }
 }
@@ -481,17 +500,19 @@ template <int PHASE, int SPW>
 __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
   const int kg = warp % g.KG, sub = warp / g.KG, slabs = g.K / 128;
-  // this lane's two rows (gr of the first copy and of the second, or gr and
-  // gr + 8 of the one), slab by slab, and their scales
+  // this lane's two rows, slab by slab, and their scales
+  const int row = copied_row(gr, g.wide);
   uint32_t w_off[SPW];
 #pragma unroll
   for (int s = 0; s < SPW; ++s) {
-    const int x = (kg + s * g.KG) * 64, piece = x / g.piece;
-    w_off[s] = sub * 8 * g.K + (piece * (PHASE == 0 ? 8 : 16) + gr) * g.piece + (x - piece * g.piece) + q * 16;
+    const int slab = kg + s * g.KG;
+    w_off[s] = sub * 8 * g.K + (g.wide ? (slab >> 1) * (PHASE == 0 ? 1024 : 2048) + row * 128 +
+                                             ((((slab & 1) * 4 + q) ^ row) << 4)
+                                       : slab * (PHASE == 0 ? 512 : 1024) + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
   }
-  const uint32_t second = PHASE == 0 ? 4 * g.K : 8 * g.piece;
+  const uint32_t second = PHASE == 0 ? 4 * g.K : g.wide ? 1024 : 512;
   const uint32_t s_off = 8 * g.K * g.R + sub * g.K + kg * 128 + (q >> 1) * 64 + (q & 1) * 2 +
-                         (PHASE == 0 ? (gr & 1) * 16 + (gr >> 1) * 4 : (gr & 3) * 16 + (gr >> 2) * 4);
+                         (PHASE == 0 ? (row & 1) * 16 + (row >> 1) * 4 : (row & 3) * 16 + (row >> 2) * 4);
   constexpr uint32_t s_second = PHASE == 0 ? 32 : 8;
   const uint32_t part = L.part + warp * 512 + lane * 16;
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
@@ -520,44 +541,33 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
       const uint32_t parity = kind < 2 ? (second ? phase2 : phase) : (second ? buf_phase2 : buf_phase);
       if (!warp_wait_lanes(3 * n, bar, parity, L.abort, p.status)) return;
     }
+    // both tiles' products side by side: each alone is a chain of waits
+    float c[2][4] = {}, d[2][4] = {};
+    const uint32_t at0 = L.slots + stage * g.stage_bytes, at1 = n == 2 ? L.slots + stage2 * g.stage_bytes : at0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (i == n) break;
-      const uint32_t at = L.slots + (i ? stage2 : stage) * g.stage_bytes;
-      float c[4] = {}, d[4] = {};
-#pragma unroll
-      for (int s = 0; s < SPW; s += 2) {  // two slabs' weights on their way at a time
-        const int sa = kg + s * g.KG, sb = sa + g.KG;
-        const bool has_a = sa < slabs, has_b = sb < slabs;
-        uint4 w[4];
-        uint32_t sc[4];
-        if (has_a) {
-          const uint32_t ss = at + s_off + s * g.KG * 128;
-          w[0] = lds128(at + w_off[s]), w[1] = lds128(at + w_off[s] + second);
-          sc[0] = lds16(ss), sc[1] = lds16(ss + s_second);
-        }
-        if (has_b) {
-          const uint32_t ss = at + s_off + (s + 1) * g.KG * 128;
-          w[2] = lds128(at + w_off[s + 1]), w[3] = lds128(at + w_off[s + 1] + second);
-          sc[2] = lds16(ss), sc[3] = lds16(ss + s_second);
-        }
-        if (has_a) mma_slab(c, d, w[0], w[1], sc[0], sc[1], b[s]);
-        if (has_b) mma_slab(c, d, w[2], w[3], sc[2], sc[3], b[s + 1]);
+    for (int s = 0; s < SPW; ++s) {
+      if (kg + s * g.KG < slabs) {
+        const uint32_t ss = s_off + s * g.KG * 128;
+        const uint4 w[2][2] = {{lds128(at0 + w_off[s]), lds128(at0 + w_off[s] + second)},
+                               {lds128(at1 + w_off[s]), lds128(at1 + w_off[s] + second)}};
+        const uint32_t sc[2][2] = {{lds16(at0 + ss), lds16(at0 + ss + s_second)},
+                                   {lds16(at1 + ss), lds16(at1 + ss + s_second)}};
+        mma_slab(c, d, w, sc, b[s]);
       }
-      // alpha first: neither factor leaves FP32's range
-      sts128(part + (i ? buf2 : buf) * (kWarps * 512), (c[0] + d[0]) * alpha * i0, (c[1] + d[1]) * alpha * i1,
-             (c[2] + d[2]) * alpha * i0, (c[3] + d[3]) * alpha * i1);
-      __syncwarp();
-      arrive_if(lane == 0, L.empty + 8 * (i ? stage2 : stage));
-      arrive_if(lane == 0, L.part_full + 8 * (i ? buf2 : buf));
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i < n)  // alpha first: neither factor leaves FP32's range
+        sts128(part + (i ? buf2 : buf) * (kWarps * 512), (c[i][0] + d[i][0]) * alpha * i0,
+               (c[i][1] + d[i][1]) * alpha * i1, (c[i][2] + d[i][2]) * alpha * i0, (c[i][3] + d[i][3]) * alpha * i1);
+    __syncwarp();
+    arrive_if(lane == 0, L.empty + 8 * stage);
+    arrive_if(lane == 0, L.part_full + 8 * buf);
+    arrive_if(lane == 0 && n == 2, L.empty + 8 * stage2);
+    arrive_if(lane == 0 && n == 2, L.part_full + 8 * buf2);
     u += n;
-    t.tile += n;
-    fresh = t.tile == g.tiles;
-    if (fresh) {
-      t.tile = 0;
-      ++t.v;
-    }
+    fresh = t.tile + n == g.tiles;
+    t.advance(n, g.tiles);
     stage += n;
     if (stage >= (uint32_t)g.stages) {
       stage -= g.stages;
@@ -573,61 +583,58 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
 
 // ------------------------------------------------------------------ join
 template <int PHASE, int R>
-__device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0,
-                                          int u1) {
+__device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int which,
+                                          int u0, int u1) {
   constexpr int KG = kWarps / R;
+  const int n = PHASE == 0 ? p.I : p.H;
   const int lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
-  uint32_t buf = 0, phase = 0;
-  for (int u = u0; u < u1; ++u) {
-    const Unit t = unit_at(u, g.tiles);
+  uint32_t buf = which, phase = 0;
+  Unit t = unit_at(u0 + which, g.tiles);
+  for (int u = u0 + which; u < u1; u += kJoinWarps, t.advance(kJoinWarps, g.tiles)) {
     const int a0 = r->member[t.v][2 * q], a1 = r->member[t.v][2 * q + 1];
     const float p0 = PHASE == 1 && a0 >= 0 ? r->weight[a0] : 0.f, p1 = PHASE == 1 && a1 >= 0 ? r->weight[a1] : 0.f;
     if (!warp_wait(L.part_full + 8 * buf, phase, L.abort, p.status)) return;
     const uint32_t from = L.part + buf * (kWarps * 512) + lane * 16;
-    float c[R][4];
+    float* to0 = (PHASE == 0 ? p.h : p.y) + (int64_t)a0 * n;
+    float* to1 = (PHASE == 0 ? p.h : p.y) + (int64_t)a1 * n;
+#pragma unroll 2
+    for (int sub = 0; sub < R; ++sub) {
+      float c[4];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const uint4 v = lds128(from + i * 512);
-      const float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+      for (int i = 0; i < KG; ++i) {
+        const uint4 v = lds128(from + (sub * KG + i) * 512);
+        const float f[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
 #pragma unroll
-      for (int n = 0; n < 4; ++n) c[i / KG][n] = i % KG ? c[i / KG][n] + f[n] : f[n];
+        for (int k = 0; k < 4; ++k) c[k] = i ? c[k] + f[k] : f[k];
+      }
+      const int row = tile_row<PHASE>(t.tile * R + sub, copied_row(gr, g.wide));
+      if (PHASE == 0) {
+        const float h0 = swiglu(c[0], c[2], p.gate_limit, p.up_limit);
+        const float h1 = swiglu(c[1], c[3], p.gate_limit, p.up_limit);
+        if (a0 >= 0) to0[row] = h0;
+        if (a1 >= 0) to1[row] = h1;
+      } else {  // accumulator row gr + 8 is output column row + 64
+        if (a0 >= 0) to0[row] = c[0] * p0, to0[row + 64] = c[2] * p0;
+        if (a1 >= 0) to1[row] = c[1] * p1, to1[row + 64] = c[3] * p1;
+      }
     }
     __syncwarp();
     arrive_if(lane == 0, L.part_empty + 8 * buf);
-    if (++buf == kPartBufs) {
-      buf = 0;
+    if ((buf += kJoinWarps) >= kPartBufs) {
+      buf -= kPartBufs;
       phase ^= 1u;
-    }
-#pragma unroll
-    for (int sub = 0; sub < R; ++sub) {
-      const int row = tile_row<PHASE>(t.tile * R + sub, gr);
-      if (PHASE == 0) {
-        if (a0 >= 0) p.h[(int64_t)a0 * p.I + row] = swiglu(c[sub][0], c[sub][2], p.gate_limit, p.up_limit);
-        if (a1 >= 0) p.h[(int64_t)a1 * p.I + row] = swiglu(c[sub][1], c[sub][3], p.gate_limit, p.up_limit);
-      } else {  // accumulator row gr + 8 is output column row + 64
-        if (a0 >= 0) {
-          float* y = p.y + (int64_t)a0 * p.H + row;
-          y[0] = c[sub][0] * p0;
-          y[64] = c[sub][2] * p0;
-        }
-        if (a1 >= 0) {
-          float* y = p.y + (int64_t)a1 * p.H + row;
-          y[0] = c[sub][1] * p1;
-          y[64] = c[sub][3] * p1;
-        }
-      }
     }
   }
 }
 
 template <int PHASE>
-__device__ void join_tiles(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
+__device__ void join_tiles(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int which, int u0, int u1) {
   switch (g.R) {
-    case 1: return join_loop<PHASE, 1>(p, g, L, r, u0, u1);
-    case 2: return join_loop<PHASE, 2>(p, g, L, r, u0, u1);
-    case 4: return join_loop<PHASE, 4>(p, g, L, r, u0, u1);
-    case 8: return join_loop<PHASE, 8>(p, g, L, r, u0, u1);
-    default: return join_loop<PHASE, 16>(p, g, L, r, u0, u1);
+    case 1: return join_loop<PHASE, 1>(p, g, L, r, which, u0, u1);
+    case 2: return join_loop<PHASE, 2>(p, g, L, r, which, u0, u1);
+    case 4: return join_loop<PHASE, 4>(p, g, L, r, which, u0, u1);
+    case 8: return join_loop<PHASE, 8>(p, g, L, r, which, u0, u1);
+    default: return join_loop<PHASE, 16>(p, g, L, r, which, u0, u1);
   }
 }
 
@@ -701,19 +708,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   const int64_t units = (int64_t)route.n_list * g.tiles;
   const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
   if (warp < kWarps) {
-    if constexpr (SPW > 2) regs_inc<kRegsConsumer>();
+    regs_inc<kRegsConsumer>();
     if (PHASE == 1) pdl_wait();
     consume_loop<PHASE, SPW>(p, g, L, &route, u0, u1);
   } else {
-    if constexpr (SPW > 2) regs_dec<kRegsOther>();
+    regs_dec<kRegsOther>();
     if (warp == kWarps) {
-      if (PHASE == 1) pdl_wait();
-      join_tiles<PHASE>(p, g, L, &route, u0, u1);
-    } else if (warp == kWarps + 1) {
       copy_loop<PHASE>(p, m, g, L, &route, u0, u1);
       if (PHASE == 0) prefetch_w2(m, next, &route);
-    } else if (warp == kWarps + 2) {
+    } else if (warp == kWarps + 1) {
       scale_loop<PHASE>(p, g, L, &route, u0, u1);
+    } else {
+      if (PHASE == 1) pdl_wait();
+      join_tiles<PHASE>(p, g, L, &route, warp - (kWarps + 2), u0, u1);
     }
   }
   __syncthreads();  // no warp's copies outlive the CTA
@@ -727,7 +734,7 @@ Phase phase_of(int K, int m16_tiles, int blocks, size_t smem) {
   g.KG = kWarps / g.R;
   g.tiles = m16_tiles / g.R;  // 16 or more m16 tiles, in sixteens
   g.blocks = blocks;
-  g.piece = few_piece(K);
+  g.wide = K % 256 == 0;
   g.stage_bytes = (9 * K * g.R + 1023) / 1024 * 1024;
   const int n = (int)((smem - 1024 - kPartBufs * kWarps * 512) / g.stage_bytes);
   g.stages = n < kMaxStages ? n : kMaxStages;
@@ -745,7 +752,7 @@ cudaError_t launch(const FewArgs& a, const FewMaps& m, int num_sms, cudaStream_t
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, few_kernel<PHASE, SPW>)) != cudaSuccess) return e;
     // setmaxnreg.inc waits for what the other warps give back: launch only with the allocation it is sized for
-    if (SPW > 2 && fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     dynamic = 232448 - 1024 - fa.sharedSizeBytes;
     e = cudaFuncSetAttribute(few_kernel<PHASE, SPW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dynamic);
     if (e != cudaSuccess) return e;

@@ -147,7 +147,7 @@ __device__ __forceinline__ bool wait_bounded_spin(uint32_t bar, uint32_t parity,
 // and multiply-adds took 860 with such a loop in front, although the barrier
 // was ready.  After kTries the role gives up.
 constexpr uint64_t kDrainNs = 2000000000ull;  // for what is in flight when a role gives up
-constexpr uint32_t kTries = 1u << 26;
+constexpr uint32_t kTries = 1u << 24;  // about a second
 __device__ __forceinline__ uint32_t lane0_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
