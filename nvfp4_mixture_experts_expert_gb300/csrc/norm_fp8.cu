@@ -8,6 +8,17 @@
 // s and y stay in FP32 registers; every output is rounded once.  The floor of
 // 2^-40 keeps the scale of an all-zero block finite (its codes are 0).  A NaN
 // in a row makes the whole row NaN (scales included).
+//
+// Bound: HBM.  A row is read once and its outputs written once, 9 bytes an
+// element with every output.  What made the difference (8192 x 4096, 302 MB,
+// 44.5 us at the 6.79 TB/s of a copy): the norm weight is loaded beside x and
+// the residual instead of behind the row's sum (53.7 -> 49 us: a block's loads
+// are one trip to memory, not two), and launches are chained (pdl_wait at the
+// start; the blocks of the next kernel take a SM's place as this one's leave
+// it): 45.1 us in a row of calls, 1 x 4096 2.1 instead of 4.2 us, 1001 x 3584
+// with FP32 weights 5.1 instead of 8.3.  Tried and dropped: blocks that loop
+// over rows with the next row's loads in flight (56 us: fewer threads a SM),
+// one vector a thread (50 us), streaming cache hints (50 us).
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -19,7 +30,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr float kMinAmax = 9.094947017729282e-13f;  // 2^-40
-constexpr int kMaxVec = 4;                          // 8-element vectors per thread
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -36,30 +46,58 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// Eight columns of the norm weight, as loaded.
+template <bool F32>
+struct Weight {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* w, int at) { v = __ldg(static_cast<const uint4*>(w) + at); }
+  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
+};
+template <>
+struct Weight<true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* w, int at) {
+    a = __ldg(static_cast<const float4*>(w) + 2 * at), b = __ldg(static_cast<const float4*>(w) + 2 * at + 1);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+
 // One row per block; thread i holds vectors i, i + blockDim, ... (8 columns
 // each), so 16 consecutive lanes hold one 128-column block.
-template <int V>
-__global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const NormArgs p) {
+template <int V, int MAX_THREADS, int MIN_BLOCKS, bool F32>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_BLOCKS) add_rmsnorm_fp8_kernel(const NormArgs p) {
   const int64_t row = blockIdx.x;
   const int nvec = p.H / 8, nt = blockDim.x, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   __shared__ float s_sum[32];
-  float s[V][8];
-  float sum = 0.f;
+  pdl_wait();
+  uint4 x[V] = {}, r[V] = {};
+  Weight<F32> w[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int at = v * nt + tid;
     if (at < nvec) {
-      unpack8(*reinterpret_cast<const uint4*>(p.x + row * p.ld_x + at * 8), s[v]);
-      if (p.residual) {
-        float r[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.residual + row * p.ld_residual + at * 8), r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[v][i] += r[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(s[v][i], s[v][i], sum);
+      x[v] = *reinterpret_cast<const uint4*>(p.x + row * p.ld_x + at * 8);
+      if (p.residual) r[v] = *reinterpret_cast<const uint4*>(p.residual + row * p.ld_residual + at * 8);
     }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (v * nt + tid < nvec) w[v].load(p.weight, v * nt + tid);
+  float s[V][8], sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    unpack8(x[v], s[v]);
+    if (p.residual) {
+      float f[8];
+      unpack8(r[v], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[v][i] += f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(s[v][i], s[v][i], sum);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -76,18 +114,12 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const NormArgs p)
     const bool in = at < nvec;
     float y[8], amax = 0.f;
     if (in) {
-      float w[8];
-      if (p.weight_f32) {
-        const float4* wp = reinterpret_cast<const float4*>(static_cast<const float*>(p.weight) + at * 8);
-        const float4 a = __ldg(wp), b = __ldg(wp + 1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-      } else {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + at * 8)), w);
-      }
+      float f[8];
+      w[v].get(f);
       if (p.residual_out) *reinterpret_cast<uint4*>(p.residual_out + row * p.ld_residual_out + at * 8) = pack8(s[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        y[i] = s[v][i] * rstd * w[i];
+        y[i] = s[v][i] * rstd * f[i];
         amax = max_nan(amax, fabsf(y[i]));
       }
       if (p.normed) *reinterpret_cast<uint4*>(p.normed + row * p.H + at * 8) = pack8(y);
@@ -112,13 +144,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const NormArgs p)
 
 cudaError_t launch_add_rmsnorm_fp8(const NormArgs& a, cudaStream_t s) {
   const int nvec = a.H / 8;
-  // two vectors a thread up to H = 4096, four above (1024 threads reach H = 32768)
-  const int v = nvec <= 512 ? 2 : kMaxVec;
-  const int nt = ((nvec + v - 1) / v + 31) / 32 * 32;
   const dim3 grid((unsigned)a.T);
-  if (v == 2)
-    return launch_kernel(add_rmsnorm_fp8_kernel<2>, grid, dim3(nt), 0, s, false, a);
-  return launch_kernel(add_rmsnorm_fp8_kernel<4>, grid, dim3(nt), 0, s, false, a);
+  auto go = [&](auto bf16, auto f32, int v) {
+    const dim3 block(((nvec + v - 1) / v + 31) / 32 * 32);
+    return launch_kernel(a.weight_f32 ? f32 : bf16, grid, block, 0, s, true, a);
+  };
+  // Two vectors a thread up to H = 4096, in the most blocks a SM whose
+  // registers do not spill; four above: 1024 threads reach H = 32768.
+  if (nvec <= 512) return go(add_rmsnorm_fp8_kernel<2, 256, 5, false>, add_rmsnorm_fp8_kernel<2, 256, 4, true>, 2);
+  if (nvec <= 2048) return go(add_rmsnorm_fp8_kernel<4, 512, 1, false>, add_rmsnorm_fp8_kernel<4, 512, 1, true>, 4);
+  return go(add_rmsnorm_fp8_kernel<4, 1024, 1, false>, add_rmsnorm_fp8_kernel<4, 1024, 1, true>, 4);
 }
 
 }  // namespace nvfp4

@@ -61,6 +61,30 @@ struct Where {
   }
 };
 
+// The outputs of one call.  An allocation costs 0.8 us of the host's time, so
+// small outputs (kShared bytes at most) are parts of one.
+class Outputs {
+ public:
+  static constexpr int64_t kShared = 256 << 10, kAlign = 256;
+  Outputs(const Where& at, int64_t bytes, int count) : at_(at) {
+    if (count > 1 && bytes + count * kAlign <= kShared) pool_ = at.empty({bytes + count * kAlign}, at::kByte);
+  }
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) {
+    if (!pool_) return at_.empty(shape, dtype);
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(pool_->storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(dtype));
+    t.unsafeGetTensorImpl()->set_storage_offset(used_ / (int64_t)t.itemsize());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    used_ += (t.numel() * (int64_t)t.itemsize() + kAlign - 1) / kAlign * kAlign;
+    return t;
+  }
+
+ private:
+  const Where& at_;
+  std::optional<at::Tensor> pool_;
+  int64_t used_ = 0;
+};
+
 void need_cuda(const at::Tensor& t, const char* name) {
   TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA tensor, not on ", t.device());
 }
@@ -110,14 +134,19 @@ PyObject* add_rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[6] != Py_None) {
     s = tensor(a[6], "residual_out");
     ld_o = rows(*s, "residual_out", at::kBFloat16, T, H, at.dev);
-  } else if (r || a[1] != Py_None) {
-    s = at.empty({T, H}, at::kBFloat16);
+  }
+  const bool sum = a[1] != Py_None && !s;
+  const int64_t cols = (H + 127) / 128;
+  Outputs out_of(at, T * (H * (2 * sum + 2 * normed + quantized) + 4 * cols * quantized),
+                 sum + normed + 2 * quantized);
+  if (sum) {
+    s = out_of.empty({T, H}, at::kBFloat16);
     ld_o = H;
   }
-  if (normed) y = at.empty({T, H}, at::kBFloat16);
+  if (normed) y = out_of.empty({T, H}, at::kBFloat16);
   if (quantized) {
-    q = at.empty({T, H}, at::kFloat8_e4m3fn);
-    scales = at.empty({T, (H + 127) / 128}, at::kFloat);
+    q = out_of.empty({T, H}, at::kFloat8_e4m3fn);
+    scales = out_of.empty({T, cols}, at::kFloat);
   }
   const int rc = nvfp4_add_rmsnorm_fp8(
       x.data_ptr(), ld_x, r, ld_r, w.data_ptr(), f32, T, H, (float)eps, s ? s->data_ptr() : nullptr, ld_o,

@@ -125,6 +125,35 @@ def test_norm_no_rows_own_stream_and_graph():
                                                                                     c.view(torch.uint8))
 
 
+@pytest.mark.parametrize("T,H", [(1, 128), (3, 144), (1001, 512)])  # one allocation for all outputs, and one each
+def test_outputs_do_not_overlap(T, H):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    outs = api.add_rms_norm_fp8(*_inputs(T, H))
+    spans = []
+    for i, t in enumerate(outs):
+        assert t.is_contiguous() and t.data_ptr() % 16 == 0
+        t.view(torch.uint8).fill_(i + 1)
+        spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+    assert all((t.view(torch.uint8) == i + 1).all() for i, t in enumerate(outs))
+    spans.sort()
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+
+
+def test_calls_that_follow_each_other_see_the_sums_before():
+    """Launches may overlap; each call reads what the one before wrote."""
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, res, w = _inputs(2000, 4096)
+    s = res.clone()
+    for _ in range(20):
+        api.add_rms_norm_fp8(x, s, w, normed=False, quantized=False, residual_out=s)
+    want = res
+    for _ in range(20):
+        want = (want.float() + x.float()).bfloat16()
+    assert torch.equal(s, want)
+
+
 def test_norm_refuses_wrong_tensors():
     import torch
     from nvfp4_mixture_experts_expert_gb300 import api, binding
