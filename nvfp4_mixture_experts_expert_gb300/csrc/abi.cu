@@ -1012,6 +1012,22 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
     return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (scales 4)");
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
+  if (M > kFp8SmallRows && M <= kFp8SplitRows) {
+    Fp8SplitArgs t;
+    memset(&t, 0, sizeof(t));
+    if (int rc = make_byte_map(&t.map_a, a, M, K, ld_a, fp8_split_nb(M))) return rc;
+    if (int rc = make_byte_map(&t.map_w, w, N, K, K, 128)) return rc;
+    t.a_scale = a_scale;
+    t.w_scale = w_scale;
+    t.out = out;
+    t.status = dev->status;
+    t.ld_out = ld_out;
+    t.M = (int)M;
+    t.N = (int)N;
+    t.kbs = (int)((K + 127) / 128);
+    cudaError_t e = launch_fp8_split(t, out_is_f32 != 0, dev->sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
+  }
   if (M > kFp8SmallRows) {
     Fp8GemmArgs t;
     memset(&t, 0, sizeof(t));

@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "fp8_mma.cuh"
 #include "nvfp4_format.cuh"
 #include "ptx.cuh"
 
@@ -71,32 +72,6 @@ struct Cfg {
   static_assert(STAGES >= BUFS, "a stage's barrier may not complete twice before the epilogue has seen it once");
 };
 
-// E4M3 x E4M3 -> FP32, K-major operands, M = 128.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-}
-
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&a)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
-        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
-        "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
-        "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
-      : "r"(taddr)
-      : "memory");
-}
-
 // Shared-memory addresses: the ring, the output buffers, the barriers (full[STAGES]: a block's
 // operands have landed; done[STAGES]: its product is complete, which frees the
 // ring slot and hands the accumulator to the epilogue; acc_empty[BUFS]: the
@@ -137,15 +112,6 @@ __device__ __forceinline__ Tile tile_at(const Fp8GemmArgs& p, int it) {
   return {(it - nt * p.m_tiles) * kBM, nt * BN};
 }
 
-__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&a)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
-        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
-      : "r"(taddr)
-      : "memory");
-}
-
 template <int BN>
 __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
   using C = Cfg<BN>;
@@ -182,12 +148,6 @@ __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
       }
   }
   __syncwarp();
-}
-
-__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
 }
 
 // Slot by slot: 128 rows x kScaleKb blocks, four rows of eight to a copy, up to
@@ -423,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *L.tmem_slot;
+  pdl_wait();
   if (warp < kEpiWarp0) {
     regs_dec<kRegsSmall>();
     if (warp == 0) load_loop<BN>(p, L);
@@ -460,7 +421,7 @@ cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
   p.m_tiles = (int)((p.M + kBM - 1) / kBM);
   p.tiles = p.m_tiles * ((p.N + BN - 1) / BN);
   return launch_kernel(fp8_gemm_kernel<BN, F32>, dim3(p.tiles < num_sms ? p.tiles : num_sms), dim3(kThreads),
-                       Cfg<BN>::SMEM, s, false, p);
+                       Cfg<BN>::SMEM, s, true, p);
 }
 template <int BN>
 cudaError_t launch_out(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s) {

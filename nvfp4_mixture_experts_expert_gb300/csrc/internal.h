@@ -242,7 +242,7 @@ struct NormArgs {
 cudaError_t launch_add_rmsnorm_fp8(const NormArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- fp8_small.cu
-constexpr int64_t kFp8SmallRows = 32;  // rows of a up to which this kernel is used
+constexpr int64_t kFp8SmallRows = 8;  // rows of a up to which this kernel is used
 struct Fp8Args {
   const uint8_t* a;      // E4M3 [M][K], row stride ld_a
   const float* a_scale;  // [M][ceil(K / 128)]
@@ -253,6 +253,22 @@ struct Fp8Args {
   int N, K, out_f32;
 };
 cudaError_t launch_fp8_small(const Fp8Args& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- fp8_split.cu
+constexpr int64_t kFp8SplitRows = 32;  // rows of a up to which this kernel is used
+struct Fp8SplitArgs {
+  CUtensorMap map_a;  // a: [M][K] bytes, box 128 x fp8_split_nb(M) rows, 128-byte swizzle
+  CUtensorMap map_w;  // w: [N][K] bytes, box 128 x 128
+  const float* a_scale;
+  const float* w_scale;
+  void* out;
+  int* status;
+  int64_t ld_out;
+  int M, N, kbs;
+  int split;  // CTAs of a cluster, set by the launch
+};
+int fp8_split_nb(int64_t M);
+cudaError_t launch_fp8_split(Fp8SplitArgs& p, bool f32, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- fp8_gemm.cu
 struct Fp8GemmArgs {

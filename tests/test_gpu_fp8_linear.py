@@ -55,6 +55,59 @@ def test_linear_larger(M, N, K):
     _check(a, sa, w, sw, api.fp8_linear(a, sa, w, sw, out_dtype=torch.float32))
 
 
+# K in ranges longer than the scales held at a time (9 to 32 rows), more tiles of w than SMs, uneven K ranges
+@pytest.mark.parametrize("M,N,K", [(20, 136, 66000), (9, 72, 132224), (12, 19464, 400), (32, 6144, 3600),
+                                   (10, 2560, 1168)])
+def test_linear_few_rows_over_a_split_k(M, N, K):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    a, sa, w, sw = _inputs(M, N, K, seed=M)
+    out = api.fp8_linear(a, sa, w, sw, out_dtype=torch.float32)
+    _check(a, sa, w, sw, out)
+    assert torch.equal(out, api.fp8_linear(a, sa, w, sw, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("M", [20, 32])
+def test_linear_split_k_strided_and_non_finite(M):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    a, sa, w, sw = _inputs(M, 520, 1040, seed=3, pad=48)
+    buf = torch.full((M + 2, 544), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = buf[1:M + 1, 8:528]
+    api.fp8_linear(a, sa, w, sw, out=out)
+    _check(a, sa, w, sw, out)
+    want = out.clone()
+    buf[1:M + 1, 8:528] = float("nan")
+    assert torch.isnan(buf).all()  # nothing else was written
+    a.view(torch.uint8)[1, 77] = 0x7F  # NaN
+    sa[2, 3] = float("inf")
+    w.view(torch.uint8)[130, 5] = 0xFF
+    got = api.fp8_linear(a, sa, w, sw)
+    assert torch.isnan(got[1]).all() and not torch.isfinite(got[2]).any() and torch.isnan(got[:, 130]).all()
+    rows = [m for m in range(M) if m not in (1, 2)]
+    cols = [n for n in range(520) if n != 130]
+    assert torch.equal(got[rows][:, cols], want[rows][:, cols])
+
+
+@pytest.mark.parametrize("M", [4, 16, 64])
+def test_calls_that_follow_each_other(M):
+    """Launches may overlap; each call reads what the one before wrote."""
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    a, sa, w, sw = _inputs(M, 1024, 1024, seed=9)
+    x = api.fp8_linear(a, sa, w, sw)
+    norm = torch.ones(1024, device="cuda")
+    for _ in range(10):
+        q, s, _, _ = api.add_rms_norm_fp8(x, None, norm, normed=False)
+        x = api.fp8_linear(q, s, w, sw)
+        torch.cuda.synchronize()
+    y = api.fp8_linear(a, sa, w, sw)
+    for _ in range(10):
+        q, s, _, _ = api.add_rms_norm_fp8(y, None, norm, normed=False)
+        y = api.fp8_linear(q, s, w, sw)
+    assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("M", [6, 200, 700])
 def test_linear_strided_rows_and_a_slice_of_a_wider_output(M):
     import torch
