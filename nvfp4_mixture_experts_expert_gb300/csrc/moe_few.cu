@@ -35,12 +35,12 @@
 // equal share of the (list entry, tile) pairs in order, so that it changes
 // expert once or twice.  A tile is R m16 tiles (about 32 KB of packed weights)
 // over all of K.  Its warps:
-//   16 consumers     KG = 16 / R of them share an m16 tile and split K by slabs;
+//   8 consumers      KG = 8 / R of them share an m16 tile and split K by slabs;
 //                    their activations stay in registers while the entry lasts
-//   warp 16          the weights' copies into the ring
-//   warp 17          the scales', 16 bytes a line: as 32-byte pieces they would
+//   warp 8           the weights' copies into the ring
+//   warp 9           the scales', 16 bytes a line: as 32-byte pieces they would
 //                    be a third of the copy engine's work
-//   warps 18, 19     tile by tile in turn: join the KG sums in a fixed order;
+//   warps 10, 11     tile by tile in turn: join the KG sums in a fixed order;
 //                    SwiGLU, or the weighted row of W2 h
 // Every CTA routes for itself (a microsecond, no launch in between).  The second
 // launch starts as CTAs of the first leave (programmatic dependent launch) and
@@ -58,16 +58,16 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWarps = 16;  // consumers
+constexpr int kWarps = 8;  // consumers
 constexpr int kThreads = 32 * (kWarps + 4);
-constexpr int kRegsLaunch = 96;    // per thread; 61,440 of the SM's 65,536 registers
-constexpr int kRegsConsumer = 104; // 32 of them activations, with four slabs a warp 64
-constexpr int kRegsOther = 64;
-static_assert(128 * (4 * kRegsConsumer + kRegsOther) <= kThreads * kRegsLaunch, "the register split must fit");
+constexpr int kRegsLaunch = 168;   // per thread; 64,512 of the SM's 65,536 registers
+constexpr int kRegsConsumer = 216; // 64 of them activations
+constexpr int kRegsOther = 72;
+static_assert(128 * (2 * kRegsConsumer + kRegsOther) <= kThreads * kRegsLaunch, "the register split must fit");
 constexpr int kMaxStages = 16;
 constexpr int kJoinWarps = 2;
 constexpr int kPartBufs = 4;       // tiles whose sums wait to be joined
-constexpr int kPrefetch = 6;       // W2 tiles a CTA of the first launch brings into L2
+constexpr int kPrefetch = 3;       // W2 tiles a CTA of the first launch brings into L2
 constexpr int kGroup = 8;  // tokens of one list entry
 
 // Routing tables: every (token, expert) assignment a = t * k + j, and the list
@@ -213,10 +213,10 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t s2, uint32_t (&r)[4
 }
 // Two E4M3 scales -> each as an f16 pair of itself.
 __device__ __forceinline__ void scale_pairs(uint32_t codes, uint32_t& s0, uint32_t& s1) {
-  uint32_t h;
-  asm("{\n.reg .b16 t;\ncvt.u16.u32 t, %1;\ncvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(h) : "r"(codes));
-  s0 = __byte_perm(h, h, 0x1010);
-  s1 = __byte_perm(h, h, 0x3232);
+  asm("{\n.reg .b16 t, lo, hi;\n.reg .b32 h;\ncvt.u16.u32 t, %2;\ncvt.rn.f16x2.e4m3x2 h, t;\n"
+      "mov.b32 {lo, hi}, h;\nmov.b32 %0, {lo, lo};\nmov.b32 %1, {hi, hi};\n}"
+      : "=r"(s0), "=r"(s1)
+      : "r"(codes));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -290,7 +290,7 @@ __device__ __forceinline__ int copied_row(int g, int wide) { return wide ? (g & 
 
 // What a launch needs to know of its product (0: W13 x, 1: W2 h).
 struct Phase {
-  int K, R, KG;       // R m16 tiles a tile, KG = 16 / R warps along K
+  int K, R, KG;       // R m16 tiles a tile, KG = kWarps / R warps along K
   int tiles;          // per list entry
   int blocks;         // 128-row blocks of an expert's matrix
   int wide;           // 128-byte pieces of a row, else 64
@@ -347,11 +347,12 @@ struct TileAt {
       : line(PHASE == 0 ? (st & 15) * 2 : (st & 7) * 4), block(e * g.blocks + (PHASE == 0 ? st >> 4 : st >> 3)) {}
 };
 
-__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, int line, int block, uint32_t bar) {
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, int line, int block, uint32_t bar,
+                                        uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %2, "
-      "%4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(block), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+      "%3, %2, %2, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(block), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -360,10 +361,11 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
                           int u1) {
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
+  const uint64_t policy = evict_first_policy();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   Unit t = unit_at(u0, g.tiles);
   for (int u = u0; u < u1; ++u, t.advance(1, g.tiles)) {
-    if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) {
+    if (!warp_wait_asleep(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) {
       // copies in flight land before the CTA leaves its shared memory
       for (int s = 0; s < g.stages; ++s)
         if (lane == 0 && (issued >> s & 1u)) {
@@ -379,8 +381,8 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
       mbar_arrive_expect_tx(bar, 8 * g.K * g.R);
       for (int i = 0; i < g.R; ++i) {
         const TileAt<PHASE> at(g, e, t.tile * g.R + i);
-        load_5d(w + i * 8 * g.K, &m.w, at.line, at.block, bar);
-        if (PHASE == 0) load_5d(w + i * 8 * g.K + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar);
+        load_5d(w + i * 8 * g.K, &m.w, at.line, at.block, bar, policy);
+        if (PHASE == 0) load_5d(w + i * 8 * g.K + 4 * g.K, &m.w, at.line, at.block + g.blocks / 2, bar, policy);
       }
     }
     __syncwarp();
@@ -399,10 +401,11 @@ template <int PHASE>
 __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
   const int lane = threadIdx.x & 31, line = lane & 3, cts = g.K / 64;
   const uint8_t* all = PHASE == 0 ? p.sf13 : p.sf2;
+  const uint64_t policy = evict_first_policy();
   uint32_t stage = 0, phase = 0;
   Unit t = unit_at(u0, g.tiles);
   for (int u = u0; u < u1; ++u, t.advance(1, g.tiles)) {
-    if (!warp_wait(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) break;
+    if (!warp_wait_asleep(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) break;
     const int e = r->expert[t.v];
     uint32_t to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + lane * 16;
     for (int i = 0; i < g.R; ++i) {
@@ -411,7 +414,9 @@ __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, cons
       const uint8_t* from = all + ((int64_t)block * cts + (lane >> 2)) * 512 +
                             (at.line + (PHASE == 0 ? line & 1 : line)) * 16;
       for (int ct = lane >> 2; ct < cts; ct += 8, from += 8 * 512, to += 512)
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+                     "l"(policy)
+                     : "memory");
       // K = 64 * cts: the lanes past an odd end have made one copy less
       to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + (i + 1) * g.K + lane * 16;
     }
@@ -593,7 +598,7 @@ __device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, cons
   for (int u = u0 + which; u < u1; u += kJoinWarps, t.advance(kJoinWarps, g.tiles)) {
     const int a0 = r->member[t.v][2 * q], a1 = r->member[t.v][2 * q + 1];
     const float p0 = PHASE == 1 && a0 >= 0 ? r->weight[a0] : 0.f, p1 = PHASE == 1 && a1 >= 0 ? r->weight[a1] : 0.f;
-    if (!warp_wait(L.part_full + 8 * buf, phase, L.abort, p.status)) return;
+    if (!warp_wait_asleep(L.part_full + 8 * buf, phase, L.abort, p.status)) return;
     const uint32_t from = L.part + buf * (kWarps * 512) + lane * 16;
     float* to0 = (PHASE == 0 ? p.h : p.y) + (int64_t)a0 * n;
     float* to1 = (PHASE == 0 ? p.h : p.y) + (int64_t)a1 * n;
@@ -633,8 +638,7 @@ __device__ void join_tiles(const FewArgs& p, const Phase& g, const Ring& L, cons
     case 1: return join_loop<PHASE, 1>(p, g, L, r, which, u0, u1);
     case 2: return join_loop<PHASE, 2>(p, g, L, r, which, u0, u1);
     case 4: return join_loop<PHASE, 4>(p, g, L, r, which, u0, u1);
-    case 8: return join_loop<PHASE, 8>(p, g, L, r, which, u0, u1);
-    default: return join_loop<PHASE, 16>(p, g, L, r, which, u0, u1);
+    default: return join_loop<PHASE, 8>(p, g, L, r, which, u0, u1);
   }
 }
 
@@ -726,11 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   __syncthreads();  // no warp's copies outlive the CTA
 }
 
-Phase phase_of(int K, int m16_tiles, int blocks, size_t smem) {
+// `entries`: the most entries the list can have.  R doubles up to 32 KB of
+// weights a tile as long as a CTA keeps eight tiles: with fewer, one more or less
+// is a large part of its time (5 tokens, H 1792, I 640: 21.6 us instead of 26.1).
+Phase phase_of(int K, int m16_tiles, int blocks, size_t smem, int64_t entries, int num_sms) {
   Phase g = {};
   g.K = K;
   g.R = 1;
-  while (g.R < kWarps && 2 * g.R * K <= 4096) g.R *= 2;
+  while (g.R < kWarps && 2 * g.R * K <= 4096 && entries * m16_tiles >= 2 * g.R * 8 * (int64_t)num_sms) g.R *= 2;
   g.KG = kWarps / g.R;
   g.tiles = m16_tiles / g.R;  // 16 or more m16 tiles, in sixteens
   g.blocks = blocks;
@@ -758,8 +765,8 @@ cudaError_t launch(const FewArgs& a, const FewMaps& m, int num_sms, cudaStream_t
     if (e != cudaSuccess) return e;
     configured = dev;
   }
-  const Phase first = phase_of(a.H, a.I / 8, 2 * a.I / 128, dynamic);
-  const Phase second = phase_of(a.I, a.H / 16, a.H / 128, dynamic);
+  const Phase first = phase_of(a.H, a.I / 8, 2 * a.I / 128, dynamic, a.T * a.k, num_sms);
+  const Phase second = phase_of(a.I, a.H / 16, a.H / 128, dynamic, a.T * a.k, num_sms);
   const Phase& g = PHASE == 0 ? first : second;
   const size_t smem = 1024 + (size_t)g.stages * g.stage_bytes + kPartBufs * kWarps * 512;
   return launch_kernel(few_kernel<PHASE, SPW>, dim3(num_sms), dim3(kThreads), smem, s, true, m, a, g, second);
@@ -767,7 +774,7 @@ cudaError_t launch(const FewArgs& a, const FewMaps& m, int num_sms, cudaStream_t
 
 template <int PHASE>
 cudaError_t launch_phase(const FewArgs& a, const FewMaps& m, int K, int num_sms, cudaStream_t s) {
-  return K > 4096 ? launch<PHASE, 4>(a, m, num_sms, s) : launch<PHASE, 2>(a, m, num_sms, s);
+  return K > 4096 ? launch<PHASE, 8>(a, m, num_sms, s) : launch<PHASE, 4>(a, m, num_sms, s);
 }
 
 }  // namespace

@@ -168,6 +168,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return true;
 }
 
+// warp_wait for a warp beside ones that compute: it sleeps in the barrier
+// instead of taking issue slots from them.
+__device__ __forceinline__ bool warp_wait_asleep(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  for (uint32_t n = 1; !__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 2000u)); ++n)
+    if (n % 256 == 0 && __any_sync(0xffffffffu, n >= kTries / 64 || *abort)) {
+      *abort = 1;
+      atomicExch(status, 6 /* NVFP4_ERR_DEVICE_TIMEOUT */);
+      return false;
+    }
+  return true;
+}
+
 // Waits for `count` barriers at once: lane i < count tests its own.
 __device__ __forceinline__ bool warp_wait_lanes(uint32_t count, uint32_t bar, uint32_t parity, volatile int* abort,
                                                 int* status) {
@@ -242,6 +254,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+// L2 policy of data that is read once: first to be replaced.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
 }
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
