@@ -1060,12 +1060,15 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
 }
 
-// Workspace of the few-token layer: status word, ids, h, y.
-static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* ids, size_t* h, size_t* y) {
+// Workspace of the few-token layer: status word, ids, routing tables, h, y.
+static size_t few_tokens_layout(int64_t T, int64_t H, int64_t I, int top_k, size_t* ids, size_t* table, size_t* h,
+                                size_t* y) {
   const int64_t A = T * top_k;
   size_t off = 256;
   *ids = off;
   off += kFewAssignments * 4;
+  *table = off;
+  off += kFewTableBytes;
   *h = off;
   off += (size_t)round_up(A * I * 4, 256);
   *y = off;
@@ -1079,8 +1082,8 @@ static bool few_tokens_sizes(int64_t T, int64_t H, int64_t I, int E, int top_k) 
 }
 
 size_t nvfp4_moe_few_tokens_workspace_size(int64_t T, int64_t H, int64_t I, int E, int top_k) {
-  size_t r, h, y;
-  return few_tokens_sizes(T, H, I, E, top_k) ? few_tokens_layout(T, H, I, top_k, &r, &h, &y) : 0;
+  size_t ids, table, h, y;
+  return few_tokens_sizes(T, H, I, E, top_k) ? few_tokens_layout(T, H, I, top_k, &ids, &table, &h, &y) : 0;
 }
 
 static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt, int64_t T, int64_t H, int64_t I,
@@ -1105,8 +1108,8 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
       !aligned16(out) || !aligned4(rt.logits) || !aligned4(rt.topk_ids) || !aligned4(rt.topk_w) ||
       !aligned4(w13_gs) || !aligned4(w2_gs))
     return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (f32 and i32 vectors 4)");
-  size_t ids, h, y;
-  const size_t need = few_tokens_layout(T, H, I, top_k, &ids, &h, &y);
+  size_t ids, table, h, y;
+  const size_t need = few_tokens_layout(T, H, I, top_k, &ids, &table, &h, &y);
   if (!workspace || workspace_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes needed", need);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -1129,6 +1132,7 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
   a.out = (uint16_t*)out;
   a.status = (int*)ws;
   a.ids = (int32_t*)(ws + ids);
+  a.table = ws + table;
   a.h = (float*)(ws + h);
   a.y = (float*)(ws + y);
   a.T = (int)T;

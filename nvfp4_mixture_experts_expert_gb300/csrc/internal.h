@@ -287,6 +287,7 @@ cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, bool f32, int num_sms, cudaS
 // ---------------------------------------------------------------- moe_few.cu
 constexpr int kFewTokens = 32;        // tokens of one call at most
 constexpr int kFewAssignments = 256;  // kFewTokens * 8
+constexpr int kFewTableBytes = 7424;   // a multiple of 256
 struct FewArgs {
   const uint16_t* x;      // bf16 [T][H], row stride ld_x
   const float* logits;    // [T][E], or null: ext_ids / ext_w
@@ -296,6 +297,7 @@ struct FewArgs {
   const float *gs13, *gs2;
   uint16_t* out;          // bf16 [T][H]
   int* status;            // workspace byte 0
+  void* table;            // [kFewTableBytes] routing tables between the launches
   int32_t* ids;           // [kFewAssignments] local expert of an assignment, -1: not computed
   float* h;               // [T * k][I]
   float* y;               // [T * k][H]

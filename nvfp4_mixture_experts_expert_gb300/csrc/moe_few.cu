@@ -17,7 +17,6 @@
 // that puts its largest value at 2^14..2^15 (exact for bf16; 11 bits are kept
 // of the FP32 h) and the sum is scaled back in FP32.
 //
-//
 // The 128 x 4 scale tiles keep rows r, r + 32, r + 64, r + 96 in one 16-byte
 // line, so the rows of an m16 tile are taken as whole lines: W13, 2 lines of
 // gate rows and the same 2 of up rows (8 features; gate in accumulator rows
@@ -29,12 +28,11 @@
 // of a row as for 128, so the pieces are 128 bytes where K % 256 == 0.  The
 // swizzle of the piece's width makes the consumers' reads conflict-free (whole
 // rows come in as fast, but two rows then share the banks of each read: 870
-// cycles of shared memory a tile instead of 375, of the 1,600 a tile may take).
+// cycles of shared memory a tile instead of 375, of the 1,570 that HBM takes).
 //
-// Two launches of one kernel, h between them, and a sum; one CTA per SM, which takes an
-// equal share of the (list entry, tile) pairs in order, so that it changes
-// expert once or twice.  A tile is R m16 tiles (about 32 KB of packed weights)
-// over all of K.  Its warps:
+// Two launches of one kernel, h between them, and a sum; one CTA per SM, which
+// takes a range of the (list entry, tile) pairs.  A tile is R m16 tiles (up to 32
+// KB of packed weights) over all of K.  Its warps:
 //   8 consumers      KG = 8 / R of them share an m16 tile and split K by slabs;
 //                    their activations stay in registers while the entry lasts
 //   warp 8           the weights' copies into the ring
@@ -42,10 +40,23 @@
 //                    be a third of the copy engine's work
 //   warps 10, 11     tile by tile in turn: join the KG sums in a fixed order;
 //                    SwiGLU, or the weighted row of W2 h
-// Every CTA routes for itself (a microsecond, no launch in between).  The second
-// launch starts as CTAs of the first leave (programmatic dependent launch) and
-// fills its rings before it waits for h, and the first asks for the second's
-// first weights to be brought into L2, so HBM does not idle between the two.
+// Every CTA of the first launch routes for itself (3 to 5 us; a launch of its own
+// would take as long); the second finds the tables in the workspace.  It starts
+// as CTAs of the first leave (programmatic dependent launch) and fills its rings
+// before it waits for h, and the first asks for the second's first weights to be
+// brought into L2, so HBM idles little between the two.
+//
+// Bound: reading the chosen experts' weights, at 32 tokens (48 experts of H 4096,
+// I 2048, top 6: 680 MB) 100 us at the rate of a copy; the layer takes 134, of
+// which the first launch's stream runs at 6.5 TB/s.  The rest is what comes
+// before a launch's first tile (routing, activations, the ring's first copies),
+// the way from one launch to the next and the sum: ~20 us of one token's 31,
+// whose weights take 12.5.  Measured beside what was kept (warm, 8 / 32 tokens):
+// sixteen consumer warps 84 / 155 us where eight took 83 / 156 and then less
+// with every step that shortened the waits; weights not marked for early eviction
+// 90 / 165 instead of 83 / 156 (they push scales, activations and the next
+// launch's weights out of L2); waiting warps that poll instead of sleeping 2 %;
+// the consumers' products with the next tiles' reads in front of them 102 / 187.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -74,7 +85,7 @@ constexpr int kGroup = 8;  // tokens of one list entry
 
 // Routing tables: every (token, expert) assignment a = t * k + j, and the list
 // of (expert, up to 8 of its assignments).
-struct Route {
+struct alignas(16) Route {
   int32_t n_list;
   int32_t pad[3];
   int32_t id[kFewAssignments];  // local expert, -1: not computed
@@ -201,6 +212,36 @@ __device__ void route_all(const FewArgs& p, Route* r) {
     r->expert[v] = e;
     r->member[v][rank % kGroup] = (int16_t)a;
   }
+}
+
+// The first launch's first CTA leaves the tables for the second, whose CTAs then
+// need not route again: complete once `ready` holds kRouteReady, until the sum
+// takes it back.  The second launch starts after that CTA has triggered it; a CTA
+// that finds the tables missing all the same routes for itself.
+struct alignas(16) RouteTable {
+  uint64_t ready, pad;
+  Route route;
+};
+static_assert(sizeof(RouteTable) <= kFewTableBytes, "the workspace's share");
+constexpr uint64_t kRouteReady = 0x6f75746564214d4bull;
+constexpr int kRouteWords = sizeof(Route) / 16;
+
+__device__ __forceinline__ void leave_route(const FewArgs& p, const Route& r) {
+  RouteTable* t = static_cast<RouteTable*>(p.table);
+  for (int i = threadIdx.x; i < kRouteWords; i += kThreads)
+    reinterpret_cast<uint4*>(&t->route)[i] = reinterpret_cast<const uint4*>(&r)[i];
+  __syncthreads();
+  if (threadIdx.x == 0)
+    asm volatile("fence.acq_rel.gpu;\nst.release.gpu.global.b64 [%0], %1;" ::"l"(&t->ready), "l"(kRouteReady) : "memory");
+}
+__device__ __forceinline__ bool take_route(const FewArgs& p, Route* r) {
+  const RouteTable* t = static_cast<const RouteTable*>(p.table);
+  uint64_t ready;
+  asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(ready) : "l"(&t->ready) : "memory");
+  if (ready == kRouteReady)
+    for (int i = threadIdx.x; i < kRouteWords; i += kThreads)
+      reinterpret_cast<uint4*>(r)[i] = __ldcg(reinterpret_cast<const uint4*>(&t->route) + i);
+  return __syncthreads_and(ready == kRouteReady);
 }
 
 // Eight E2M1 codes (one word) times a block scale: four f16 pairs, in order.
@@ -713,6 +754,7 @@ __device__ void join_tiles(const FewArgs& p, const Phase& g, const Ring& L, cons
 // out[t] = bf16(the sum of the token's weighted rows, j ascending).
 __global__ void __launch_bounds__(256) few_sum_kernel(const FewArgs p) {
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) static_cast<RouteTable*>(p.table)->ready = 0;
   const int i = blockIdx.x * 256 + threadIdx.x, per = p.H / 4;  // four columns a thread
   if (i >= p.T * per) return;
   const int t = i / per, n = i - t * per;
@@ -761,7 +803,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   }
   if (PHASE == 0) {
     pdl_wait();  // logits and activations may come from the kernel just before, and its caller may still use h
-    pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     // on their way to L2 while the tokens are routed
     for (int i = threadIdx.x * 32; p.logits && i < p.T * p.E; i += kThreads * 32) prefetch_l2(p.logits + i);
@@ -773,11 +814,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       prefetch_l2(p.gs2 + threadIdx.x);
     }
   }
-  // The second launch reads the router's output before it waits for the first:
-  // that started only when whatever wrote it was complete.
-  route_all(p, &route);
-  __syncthreads();
-  if (PHASE == 0 && blockIdx.x == 0 && threadIdx.x < p.T * p.k) p.ids[threadIdx.x] = route.id[threadIdx.x];
+  if (PHASE == 0 || !take_route(p, &route)) {
+    // also the second launch may read the router's output before it waits for the
+    // first: that started only when whatever wrote it was complete
+    route_all(p, &route);
+    __syncthreads();
+  }
+  if (PHASE == 0) {
+    if (blockIdx.x == 0) {
+      if (threadIdx.x < p.T * p.k) p.ids[threadIdx.x] = route.id[threadIdx.x];
+      leave_route(p, route);
+    }
+    pdl_trigger();
+  }
   int u0, u1;
   share_of(route.n_list, g.tiles, u0, u1);
   if (warp < kWarps) {

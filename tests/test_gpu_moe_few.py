@@ -49,7 +49,7 @@ SIZES = [  # T, H, I, E, k
     (1, 256, 128, 8, 2), (1, 256, 128, 1, 1), (2, 512, 384, 3, 3), (3, 1792, 640, 12, 4), (5, 768, 1152, 16, 8),
     (8, 1024, 256, 64, 6), (9, 256, 512, 256, 8), (16, 512, 128, 5, 2), (17, 1280, 896, 31, 5), (31, 256, 128, 40, 8),
     (32, 1024, 512, 48, 6), (32, 256, 256, 4, 4), (1, 4096, 2048, 8, 6), (4, 8192, 128, 4, 2), (4, 256, 8192, 4, 2),
-    (2, 7168, 2176, 3, 2),
+    (2, 7168, 2176, 3, 2), (32, 256, 2048, 64, 8), (32, 2048, 128, 200, 8), (20, 512, 256, 38, 1),
 ]
 
 
@@ -219,6 +219,34 @@ def test_own_stream_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(want, kept)
     assert torch.equal(want, got) and layer.status() == 0
+
+
+def test_routes_of_earlier_calls_are_not_used():
+    """The second launch takes the first's routing tables; those of a call before
+    are still in the workspace."""
+    import torch
+    H, I, E, k, T = 512, 256, 24, 4, 12
+    w, x, layer = _weights(E, H, I), _x(T, H, 14), _layer(T, H, I, E, k)
+    every = [_logits(T, E, seed) for seed in range(6)]
+    want = []
+    for logits in every:
+        ids, p = R.route(logits, k)
+        want.append(R.moe(x, ids, p, w, E, H, I))
+        _check(layer(x, logits, w), *want[-1])
+    ids, p = R.route(every[0], k)
+    ids, p = ids.int().contiguous(), p.float().contiguous()
+    _check(layer.routed(x, ids, p, 0, w), *want[0])
+    static = every[5].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x, static, w)
+    outs = []
+    for logits in every:  # replays back to back
+        static.copy_(logits)
+        graph.replay()
+        outs.append(out.clone())
+    for got, ref in zip(outs, want):
+        _check(got, *ref)
 
 
 def test_nearer_to_the_weights_layer_than_the_quantized_forward():
