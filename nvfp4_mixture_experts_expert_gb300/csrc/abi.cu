@@ -1031,17 +1031,20 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
   if (M > kFp8SmallRows) {
     Fp8GemmArgs t;
     memset(&t, 0, sizeof(t));
-    const int bn = fp8_gemm_bn(M, N, dev->sms);
-    if (int rc = make_byte_map(&t.map_a, a, M, K, ld_a, 128)) return rc;
-    if (int rc = make_byte_map(&t.map_w, w, N, K, K, bn)) return rc;
-    if (int rc = make_store_map(&t.map_out, out, M, N, ld_out, out_is_f32 != 0, 64)) return rc;
     t.a_scale = a_scale;
     t.w_scale = w_scale;
+    t.out = out;
     t.status = dev->status;
+    t.ld_out = ld_out;
     t.M = (int)M;
     t.N = (int)N;
     t.kbs = (int)((K + 127) / 128);
-    cudaError_t e = launch_fp8_gemm(t, bn, out_is_f32 != 0, dev->sms, (cudaStream_t)stream);
+    cudaError_t e = fp8_gemm_plan(t, dev->sms);
+    if (e != cudaSuccess) return cuda_fail(e, "fp8_linear plan");
+    if (int rc = make_byte_map(&t.map_a, a, M, K, ld_a, 128)) return rc;
+    if (int rc = make_byte_map(&t.map_w, w, N, K, K, t.bn)) return rc;
+    if (int rc = make_store_map(&t.map_out, out, M, N, ld_out, out_is_f32 != 0, 64)) return rc;
+    e = launch_fp8_gemm(t, out_is_f32 != 0, dev->sms, (cudaStream_t)stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
   }
   Fp8Args g = {};

@@ -11,7 +11,9 @@
 // TMEM lane and thread; a warp's columns lie in one 128-block of w, so a
 // thread multiplies a whole block by one number.
 //
-// Persistent, one CTA per SM, tiles of 128 x BN, 12 warps:
+// Persistent, one CTA per SM, tiles of 128 x BN; where a problem has few tiles, K
+// is split over the CTAs of a cluster, which add their sums through shared memory
+// (fp8_gemm_plan).  12 warps:
 //   warp 0      TMA: per K-block a 128 x 128 box of a and a BN x 128 box of w
 //               (SWIZZLE_128B) into a ring; rows and columns past the matrices
 //               read as zero
@@ -112,17 +114,31 @@ __device__ __forceinline__ Tile tile_at(const Fp8GemmArgs& p, int it) {
   return {(it - nt * p.m_tiles) * kBM, nt * BN};
 }
 
-template <int BN>
+// This CTA's tiles (first, step) and K-blocks: all of them, or with SPLIT one
+// range of one tile, whose other ranges the cluster's other CTAs have.
+struct Work {
+  int tile, step, kb0, kb1;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Work work_of(const Fp8GemmArgs& p) {
+  if (!SPLIT) return {(int)blockIdx.x, (int)gridDim.x, 0, p.kbs};
+  const int rank = blockIdx.x % p.split;
+  return {(int)blockIdx.x / p.split, p.tiles, (int)((int64_t)p.kbs * rank / p.split),
+          (int)((int64_t)p.kbs * (rank + 1) / p.split)};
+}
+
+template <int BN, bool SPLIT>
 __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
+  const Work g = work_of<SPLIT>(p);
   using C = Cfg<BN>;
   volatile int* abort = L.abort_flag;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;
-  for (int it = blockIdx.x; it < p.tiles && ok && !*abort; it += gridDim.x) {
+  for (int it = g.tile; it < p.tiles && ok && !*abort; it += g.step) {
     const Tile t = tile_at<BN>(p, it);
-    for (int kb = 0; kb < p.kbs; ++kb) {
+    for (int kb = g.kb0; kb < g.kb1; ++kb) {
       ok = warp_wait(L.done + 8 * stage, phase ^ 1u, abort, p.status);
       if (!ok) break;
       if (leader) {
@@ -153,15 +169,16 @@ __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
 // Slot by slot: 128 rows x kScaleKb blocks, four rows of eight to a copy, up to
 // kScaleSlots ahead.  Asynchronous, because behind the operand copies that the
 // ring keeps in flight a load takes microseconds.
-template <int BN>
+template <int BN, bool SPLIT>
 __device__ void scale_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
+  const Work g = work_of<SPLIT>(p);
   volatile int* abort = L.abort_flag;
   const int lane = threadIdx.x & 31, r0 = lane >> 3, k = lane & 7;
   uint32_t slot = 0, phase = 0;
   bool ok = true;
-  for (int it = blockIdx.x; it < p.tiles && ok; it += gridDim.x) {
+  for (int it = g.tile; it < p.tiles && ok; it += g.step) {
     const Tile t = tile_at<BN>(p, it);
-    for (int c0 = 0; c0 < p.kbs; c0 += kScaleKb) {
+    for (int c0 = g.kb0; c0 < g.kb1; c0 += kScaleKb) {
       ok = warp_wait(L.sc_empty + 8 * slot, phase ^ 1u, abort, p.status);
       if (!ok) break;
       const uint32_t to = L.scales + slot * kScaleSlotBytes + (k * kScalePitch + r0) * 4;
@@ -187,8 +204,9 @@ __device__ void scale_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
 // four MMAs takes a warp ~400 cycles, the MMAs of a 128 x 128 block 256.  One
 // elected lane issues; the loop runs on the whole warp so that descriptors,
 // addresses and phases are warp-uniform.
-template <int BN>
+template <int BN, bool SPLIT>
 __device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem, int which) {
+  const Work g = work_of<SPLIT>(p);
   using C = Cfg<BN>;
   volatile int* abort = L.abort_flag;
   const int lane = threadIdx.x & 31;
@@ -197,7 +215,7 @@ __device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem,
   const uint64_t a0 = smem_desc(L.stages, 16, 1024, 2);
   const uint64_t b0 = smem_desc(L.stages + C::A_BYTES, 16, 1024, 2);
   uint32_t stage = which, phase = 0, buf = which, buf_phase = 1;
-  const int blocks = p.kbs * ((p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int blocks = (g.kb1 - g.kb0) * ((p.tiles - g.tile + g.step - 1) / g.step);
   bool issued = false;
   for (int b = which; b < blocks; b += kMmaWarps) {
     if (!warp_wait(L.full + 8 * stage, phase, abort, p.status) ||
@@ -253,8 +271,9 @@ __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&d)[W]
 // 512 that the block's MMAs take.  The rows' scales are loaded by warp 3; the
 // columns' (one number a warp) one block ahead, and multiplied when used: a
 // product any earlier would wait for the load.
-template <int BN, bool F32>
+template <int BN, bool F32, bool SPLIT>
 __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem) {
+  const Work g = work_of<SPLIT>(p);
   using C = Cfg<BN>;
   constexpr int W = BN == 256 ? 16 : 32, CHUNKS = C::COLS / W;  // measured: 112 / 142 us at 256, 130 / 122 at 128
   volatile int* abort = L.abort_flag;
@@ -265,21 +284,22 @@ __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t 
   const uint32_t my_scales = L.scales + (quarter * 32 + lane) * 4;
   uint32_t stage = 0, phase = 0, buf = 0, sc = 0, sc_phase = 0;
   bool ok = true;
-  for (int it = blockIdx.x; it < p.tiles && ok; it += gridDim.x) {
+  for (int it = g.tile; it < p.tiles && ok; it += g.step) {
     const Tile t = tile_at<BN>(p, it);
     const int n0 = t.n0 + half * C::COLS;
     const float* sw = p.w_scale + (int64_t)(n0 < p.N ? n0 / 128 : 0) * p.kbs;
-    float sw0 = __ldg(sw);
+    float sw0 = __ldg(sw + g.kb0);
     uint64_t acc[C::COLS / 2];
 #pragma unroll
     for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0ull;
-    for (int kb = 0; kb < p.kbs; ++kb) {
-      const float sw1 = kb + 1 < p.kbs ? __ldg(sw + kb + 1) : 0.f;
-      if (kb % kScaleKb == 0) {
+    for (int kb = g.kb0; kb < g.kb1; ++kb) {
+      const float sw1 = kb + 1 < g.kb1 ? __ldg(sw + kb + 1) : 0.f;
+      const int sk = (kb - g.kb0) % kScaleKb;
+      if (sk == 0) {
         ok = warp_wait(L.sc_full + 8 * sc, sc_phase, abort, p.status);
         if (!ok) break;
       }
-      const float sa0 = ld_shared_f32(my_scales + sc * kScaleSlotBytes + kb % kScaleKb * (kScalePitch * 4));
+      const float sa0 = ld_shared_f32(my_scales + sc * kScaleSlotBytes + sk * (kScalePitch * 4));
       ok = warp_wait(L.done + 8 * stage, phase, abort, p.status);
       if (!ok) break;
       tc_fence_after();
@@ -301,7 +321,7 @@ __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t 
         add_scaled(acc + W / 2 * c, d, ss);
       }
       sw0 = sw1;
-      if (kb % kScaleKb == kScaleKb - 1 || kb + 1 == p.kbs) {
+      if (sk == kScaleKb - 1 || kb + 1 == g.kb1) {
         __syncwarp();
         arrive_if(lane == 0, L.sc_empty + 8 * sc);
         if (++sc == kScaleSlots) {
@@ -316,6 +336,17 @@ __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t 
       if (++buf == C::BUFS) buf = 0;
     }
     if (!ok) break;
+    if constexpr (SPLIT) {  // the range's sums, a row of the tile per thread, for the join
+      const uint32_t to = L.stages + ((quarter * 32 + lane) * (BN + 4) + half * C::COLS) * 4;
+#pragma unroll
+      for (int i = 0; i < C::COLS / 4; ++i) {
+        float v[4];
+        f2_unpack(acc[2 * i], v[0], v[1]);
+        f2_unpack(acc[2 * i + 1], v[2], v[3]);
+        st_shared_v4(to + 16 * i, {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+      }
+      continue;
+    }
     // 32 rows x 64 bytes at a time through the warp's staging buffer
     constexpr int PIECE = F32 ? 16 : 32;  // columns
 #pragma unroll
@@ -352,7 +383,49 @@ __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t 
   __syncwarp();
 }
 
+// The cluster's CTAs add up the ranges' sums in K order, each its share of the
+// tile's rows: four columns a lane, two rows' loads in flight.
 template <int BN, bool F32>
+__device__ void join_ranges(const Fp8GemmArgs& p, const Smem<BN>& L) {
+  constexpr int PER = BN / 4, ROWS = 32 / PER;  // lanes a row, rows a warp
+  static_assert(PER <= 32 && 32 % PER == 0, "a warp reads whole rows");
+  const Tile t = tile_at<BN>(p, work_of<true>(p).tile);
+  const int warp = (threadIdx.x >> 5) - kEpiWarp0, lane = threadIdx.x & 31, rank = blockIdx.x % p.split;
+  const int col = lane % PER * 4, n = t.n0 + col;
+  const int r0 = kBM * rank / p.split, r1 = min(kBM * (rank + 1) / p.split, p.M - t.m0);
+  for (int r = r0 + warp * ROWS + lane / PER; r < r1; r += 2 * kEpiWarps * ROWS) {
+    uint4 v[2][kMaxSplit];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = r + j * kEpiWarps * ROWS;
+#pragma unroll
+      for (int i = 0; i < kMaxSplit; ++i)
+        if (i < p.split && row < r1) v[j][i] = ld_shared_cluster_v4(mapa_shared(L.stages + (row * (BN + 4) + col) * 4, i));
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = r + j * kEpiWarps * ROWS;
+      if (row >= r1 || n >= p.N) continue;
+      float s[4] = {};
+#pragma unroll
+      for (int i = 0; i < kMaxSplit; ++i)
+        if (i < p.split) {
+          s[0] += __uint_as_float(v[j][i].x);
+          s[1] += __uint_as_float(v[j][i].y);
+          s[2] += __uint_as_float(v[j][i].z);
+          s[3] += __uint_as_float(v[j][i].w);
+        }
+      const int64_t at = (int64_t)(t.m0 + row) * p.ld_out + n;
+      if (F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(s[0], s[1], s[2], s[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+            make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    }
+  }
+}
+
+template <int BN, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmArgs p) {
   using C = Cfg<BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -386,12 +459,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   pdl_wait();
   if (warp < kEpiWarp0) {
     regs_dec<kRegsSmall>();
-    if (warp == 0) load_loop<BN>(p, L);
-    if (warp == 1 || warp == 2) mma_loop<BN>(p, L, tmem, warp - 1);
-    if (warp == 3) scale_loop<BN>(p, L);
+    if (warp == 0) load_loop<BN, SPLIT>(p, L);
+    if (warp == 1 || warp == 2) mma_loop<BN, SPLIT>(p, L, tmem, warp - 1);
+    if (warp == 3) scale_loop<BN, SPLIT>(p, L);
+    if constexpr (SPLIT) {  // the two meetings of the join
+      __syncwarp();
+      cluster_sync_all();
+      cluster_arrive_relaxed();
+      cluster_wait();
+    }
   } else {
     regs_inc<kRegsEpi>();
-    epilogue_loop<BN, F32>(p, L, tmem);
+    epilogue_loop<BN, F32, SPLIT>(p, L, tmem);
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync_all();
+      join_ranges<BN, F32>(p, L);
+      __syncwarp();
+      cluster_arrive_relaxed();  // the other CTAs' reads of this one's shared memory
+      cluster_wait();
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -402,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
 }
 
-template <int BN, bool F32>
-cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
+template <int BN, bool F32, bool SPLIT>
+cudaError_t configure() {
   static int configured = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -411,16 +498,29 @@ cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
   if (configured != dev) {
     // setmaxnreg.inc waits for what the other warps give back: launch only with the allocation it is sized for
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN, F32>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN, F32, SPLIT>)) != cudaSuccess) return e;
     if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<BN, F32, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Cfg<BN>::SMEM);
     if (e != cudaSuccess) return e;
     configured = dev;
   }
+  return cudaSuccess;
+}
+template <int BN, bool F32>
+cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
   p.m_tiles = (int)((p.M + kBM - 1) / kBM);
   p.tiles = p.m_tiles * ((p.N + BN - 1) / BN);
-  return launch_kernel(fp8_gemm_kernel<BN, F32>, dim3(p.tiles < num_sms ? p.tiles : num_sms), dim3(kThreads),
+  cudaError_t e;
+  if constexpr (BN < 256) {
+    if (p.split > 1) {
+      if ((e = configure<BN, F32, true>()) != cudaSuccess) return e;
+      return launch_split<const Fp8GemmArgs>(fp8_gemm_kernel<BN, F32, true>, p.tiles * p.split, kThreads,
+                                             Cfg<BN>::SMEM, p.split, s, p);
+    }
+  }
+  if ((e = configure<BN, F32, false>()) != cudaSuccess) return e;
+  return launch_kernel(fp8_gemm_kernel<BN, F32, false>, dim3(p.tiles < num_sms ? p.tiles : num_sms), dim3(kThreads),
                        Cfg<BN>::SMEM, s, true, p);
 }
 template <int BN>
@@ -430,21 +530,43 @@ cudaError_t launch_out(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// Columns of a tile: those whose rounds of tiles over the SMs take least.  A
-// K-block of a tile measured 503, 279 and 199 ns at 256, 128 and 64 columns
-// (8192 x 4096 x 4096: 113, 125 and 172 us), so 64 pays when 256 leaves most SMs
-// without a tile (128 x 4096 x 4096: 10.4 against 18.5 us).
-int fp8_gemm_bn(int64_t M, int64_t N, int num_sms) {
-  const int64_t mt = (M + kBM - 1) / kBM;
-  auto time = [&](int64_t bn, int64_t ns) { return (mt * ((N + bn - 1) / bn) + num_sms - 1) / num_sms * ns; };
-  const int64_t t256 = time(256, 503), t128 = time(128, 279), t64 = time(64, 199);
-  return t256 <= t128 && t256 <= t64 ? 256 : t128 <= t64 ? 128 : 64;
+// The plan whose K-blocks take least time: columns of a tile, by its rounds of
+// tiles over the SMs, and where there is one round with SMs to spare, CTAs that
+// share a tile's K.  A K-block of a tile measured 503, 279 and 199 ns at 256, 128
+// and 64 columns (8192 x 4096 x 4096: 113, 125 and 172 us), so 64 pays when 256
+// leaves most SMs without a tile (128 x 4096 x 4096: 8.5 against 16.2 us), and the
+// join of a split K 3 and 2 us (300 x 1000 x 3600: 8.4 us with 128 columns and five
+// CTAs a tile against 10.7 with 64 and one; 100 x 512 x 4096 5.7 against 8.4; 256 x
+// 1000 x 1024, eight K-blocks, would lose: 5.3 against 4.3).
+cudaError_t fp8_gemm_plan(Fp8GemmArgs& p, int num_sms) {
+  static int configured = -1, clusters[kMaxSplit + 1];  // one CTA a SM in all forms
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured != dev) {
+    if ((e = configure<64, false, true>()) != cudaSuccess) return e;
+    e = max_clusters(fp8_gemm_kernel<64, false, true>, kThreads, Cfg<64>::SMEM, clusters);
+    if (e != cudaSuccess) return e;
+    configured = dev;
+  }
+  constexpr int kBns[3] = {256, 128, 64}, kNs[3] = {503, 279, 199}, kJoinNs[3] = {0, 3000, 2000};
+  const int64_t mt = (p.M + kBM - 1) / kBM;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t tiles = mt * ((p.N + kBns[i] - 1) / kBns[i]);
+    for (int c = 1; c <= (kBns[i] < 256 ? kMaxSplit : 1) && c <= p.kbs; ++c) {
+      if (c > 1 && (tiles * c > num_sms || tiles > clusters[c])) continue;
+      const int64_t ns = (tiles * c + num_sms - 1) / num_sms * ((p.kbs + c - 1) / c) * kNs[i] + (c > 1 ? kJoinNs[i] : 0);
+      if (ns < least) least = ns, p.bn = kBns[i], p.split = c;
+    }
+  }
+  return cudaSuccess;
 }
 
-cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, bool f32, int num_sms, cudaStream_t s) {
-  return bn == 256   ? launch_out<256>(p, f32, num_sms, s)
-         : bn == 128 ? launch_out<128>(p, f32, num_sms, s)
-                     : launch_out<64>(p, f32, num_sms, s);
+cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s) {
+  return p.bn == 256   ? launch_out<256>(p, f32, num_sms, s)
+         : p.bn == 128 ? launch_out<128>(p, f32, num_sms, s)
+                       : launch_out<64>(p, f32, num_sms, s);
 }
 
 }  // namespace nvfp4

@@ -1,7 +1,11 @@
-// FP8 products on tcgen05 (kind::f8f6f4) and their accumulators' way out of TMEM,
-// shared by the FP8 linear kernels.
+// FP8 products on tcgen05 (kind::f8f6f4), their accumulators' way out of TMEM,
+// and K split over a cluster: shared by the FP8 linear kernels.
 #pragma once
 #include <cstdint>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
 
 namespace nvfp4 {
 
@@ -44,6 +48,48 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t at) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
+}
+
+constexpr int kMaxSplit = 8;  // portable cluster size
+
+// How many clusters of 1 to kMaxSplit CTAs the GPU holds at a time.
+template <typename... KArgs>
+cudaError_t max_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int (&clusters)[kMaxSplit + 1]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  for (int c = 1; c <= kMaxSplit; ++c) {
+    cfg.gridDim = dim3(c);
+    at[0].val.clusterDim.x = c;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[c], kernel, &cfg);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// A chained launch (see pdl_wait) in clusters of `split` CTAs.
+template <typename Arg>
+cudaError_t launch_split(void (*kernel)(Arg), int blocks, int threads, size_t smem, int split, cudaStream_t s,
+                         const Arg& arg) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 
 }  // namespace nvfp4

@@ -41,7 +41,6 @@ constexpr int kEpiWarp0 = 2;
 constexpr int kThreads = 32 * (kEpiWarp0 + 4);
 constexpr int kBufs = 4;               // TMEM accumulators
 constexpr int kScaleBytes = 8192;      // scale products of up to kScaleBytes / (4 NB) K-blocks
-constexpr int kMaxSplit = 8;           // portable cluster size
 
 template <int NB>
 struct SplitCfg {
@@ -65,14 +64,6 @@ __device__ __forceinline__ void st_shared_f32(uint32_t at, float v) {
 }
 __device__ __forceinline__ void ld_shared_2x64(uint32_t at, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_cluster_v4(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
 }
 // The four warps of the sums.
 __device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -334,44 +325,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_split_kernel(const __grid_con
 
 template <int NB, bool F32>
 cudaError_t launch(Fp8SplitArgs& p, int num_sms, cudaStream_t s) {
-  using C = SplitCfg<NB>;
-  static int configured = -1, clusters[kMaxSplit + 1];  // that fit the GPU at a time, by size
+  constexpr size_t SMEM = SplitCfg<NB>::SMEM;
+  static int configured = -1, clusters[kMaxSplit + 1];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
   if (configured != dev) {
-    e = cudaFuncSetAttribute(fp8_split_kernel<NB, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    e = cudaFuncSetAttribute(fp8_split_kernel<NB, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
-    cfg.numAttrs = 1;
-    for (int c = 1; c <= kMaxSplit; ++c) {
-      cfg.gridDim = dim3(c);
-      at[0].val.clusterDim.x = c;
-      if ((e = cudaOccupancyMaxActiveClusters(&clusters[c], fp8_split_kernel<NB, F32>, &cfg)) != cudaSuccess) return e;
-    }
+    if ((e = max_clusters(fp8_split_kernel<NB, F32>, kThreads, SMEM, clusters)) != cudaSuccess) return e;
     configured = dev;
   }
   const int tiles = (p.N + kTileN - 1) / kTileN;
   p.split = 1;  // the most CTAs that run at once, one a SM
   for (int c = 2; c <= kMaxSplit && c <= p.kbs; ++c)
     if (tiles * c <= num_sms && tiles <= clusters[c]) p.split = c;
-  cfg.gridDim = dim3(tiles * p.split);
-  at[0].val.clusterDim.x = p.split;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fp8_split_kernel<NB, F32>, static_cast<const Fp8SplitArgs>(p));
-}
-template <int NB>
-cudaError_t launch_out(Fp8SplitArgs& p, bool f32, int num_sms, cudaStream_t s) {
-  return f32 ? launch<NB, true>(p, num_sms, s) : launch<NB, false>(p, num_sms, s);
+  return launch_split<const Fp8SplitArgs>(fp8_split_kernel<NB, F32>, tiles * p.split, kThreads, SMEM, p.split, s, p);
 }
 
 }  // namespace
@@ -379,7 +348,8 @@ cudaError_t launch_out(Fp8SplitArgs& p, bool f32, int num_sms, cudaStream_t s) {
 int fp8_split_nb(int64_t M) { return M <= 16 ? 16 : 32; }
 
 cudaError_t launch_fp8_split(Fp8SplitArgs& p, bool f32, int num_sms, cudaStream_t s) {
-  return fp8_split_nb(p.M) == 16 ? launch_out<16>(p, f32, num_sms, s) : launch_out<32>(p, f32, num_sms, s);
+  if (fp8_split_nb(p.M) == 16) return f32 ? launch<16, true>(p, num_sms, s) : launch<16, false>(p, num_sms, s);
+  return f32 ? launch<32, true>(p, num_sms, s) : launch<32, false>(p, num_sms, s);
 }
 
 }  // namespace nvfp4

@@ -273,16 +273,19 @@ cudaError_t launch_fp8_split(Fp8SplitArgs& p, bool f32, int num_sms, cudaStream_
 // ---------------------------------------------------------------- fp8_gemm.cu
 struct Fp8GemmArgs {
   CUtensorMap map_a;  // a: [M][K] bytes, box 128 x 128, 128-byte swizzle
-  CUtensorMap map_w;  // w: [N][K] bytes, box 128 x BN rows
+  CUtensorMap map_w;  // w: [N][K] bytes, box 128 x bn rows
   CUtensorMap map_out;  // out: [M][N], box 64 bytes x 32 rows, 64-byte swizzle
   const float* a_scale;
   const float* w_scale;
+  void* out;
   int* status;
+  int64_t ld_out;
   int M, N, kbs;
+  int bn, split;       // columns of a tile and CTAs that share its K, set by fp8_gemm_plan
   int m_tiles, tiles;  // set by the launch
 };
-int fp8_gemm_bn(int64_t M, int64_t N, int num_sms);
-cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, int bn, bool f32, int num_sms, cudaStream_t s);
+cudaError_t fp8_gemm_plan(Fp8GemmArgs& p, int num_sms);  // from M, N and kbs
+cudaError_t launch_fp8_gemm(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- moe_few.cu
 constexpr int kFewTokens = 32;        // tokens of one call at most
