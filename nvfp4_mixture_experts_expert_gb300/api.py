@@ -261,6 +261,38 @@ class MoEFewTokens:
         return B.nvfp4_read_device_status(self.workspace, stream, reset)
 
 
+def quantize_fp8_weight(w):
+    """float8_e4m3fn codes [N, K] and f32 scales [ceil(N/128), ceil(K/128)] of a weight
+    matrix, as fp8_linear takes them (once, when a model is loaded; torch operations)."""
+    N, K = w.shape
+    nb, kb = -(-N // 128), -(-K // 128)
+    blocks = torch.nn.functional.pad(w.float(), (0, kb * 128 - K, 0, nb * 128 - N)).view(nb, 128, kb, 128)
+    scale = blocks.abs().amax((1, 3)).clamp_min(2.0 ** -40) / 448
+    codes = (blocks / scale[:, None, :, None]).clamp(-448, 448).view(nb * 128, kb * 128)[:N, :K]
+    return codes.to(torch.float8_e4m3fn).contiguous(), scale.contiguous()
+
+
+class FFNBlock:
+    """The FFN half of a decoder layer for up to T <= 32 tokens: residual addition and
+    norm, FP8 router with FP32 logits, MoE layer.  Owns the layer's workspace: one
+    call at a time.  norm_weight bf16 or f32 [H]; router = quantize_fp8_weight of
+    the router's [E, H] matrix (E a multiple of 8)."""
+
+    def __init__(self, T, H, I, E, top_k, norm_weight, router, weights: MoEWeights, eps=1e-6, gate_limit=10.0,
+                 up_limit=10.0, device="cuda"):
+        self.layer = MoEFewTokens(T, H, I, E, top_k, device)
+        self.norm_weight, self.router, self.weights = norm_weight, router, weights
+        self.eps, self.limits = eps, (gate_limit, up_limit)
+
+    def __call__(self, x, residual, stream=None):
+        """x, residual bf16 [t, H], t <= T: the attention's output and the hidden states
+        before it.  Returns the block's output and the hidden states x + residual,
+        which the next layer's norm adds up."""
+        q, scales, y, s = add_rms_norm_fp8(x, residual, self.norm_weight, self.eps, stream=stream)
+        logits = fp8_linear(q, scales, *self.router, out_dtype=torch.float32, stream=stream)
+        return self.layer(y, logits, self.weights, *self.limits, stream=stream), s
+
+
 class HostPipeline:
     """Streams batches from pinned host memory through one MoEForward.
 

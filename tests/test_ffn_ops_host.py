@@ -87,3 +87,20 @@ def test_no_work_is_not_an_error(B):
     B.nvfp4_add_rmsnorm_fp8(**{**NORM, "T": 0, "x": None}, stream=0)
     B.nvfp4_fp8_linear(**{**LINEAR, "M": 0, "a": None}, stream=0)
     B.nvfp4_moe_few_tokens(**{**FEW, "T": 0, "hidden": None}, stream=0)
+
+
+def test_quantize_fp8_weight():
+    torch = pytest.importorskip("torch")
+    from nvfp4_mixture_experts_expert_gb300 import api
+    w = torch.randn(200, 272, generator=torch.Generator().manual_seed(0))
+    w[:128, :128] = 0
+    codes, scale = api.quantize_fp8_weight(w)
+    assert codes.shape == w.shape and codes.dtype is torch.float8_e4m3fn and scale.shape == (2, 3)
+    for i in range(2):
+        for j in range(3):
+            part = w[128 * i:128 * i + 128, 128 * j:128 * j + 128]
+            top = max(float(part.abs().max()), 2.0 ** -40)
+            assert abs(float(scale[i, j]) * 448 / top - 1) < 1e-6
+            err = (codes[128 * i:128 * i + 128, 128 * j:128 * j + 128].float() * scale[i, j] - part).abs()
+            # half a unit of three mantissa bits, or of the subnormals 2^-9 apart
+            assert (err <= torch.maximum(part.abs() / 16, scale[i, j] * 2.0 ** -10) * (1 + 1e-5)).all()
