@@ -215,7 +215,7 @@ def add_rms_norm_fp8(x, residual, weight, eps=1e-6, normed=True, quantized=True,
     Returns (q, scales, y, s): float8_e4m3fn [T, H] and f32 [T, ceil(H/128)]
     (None with quantized=False), bf16 y (None with normed=False), bf16 s (None
     without a residual).  residual_out: where s goes; x or residual for in place.
-    Outputs of up to 256 KB together are parts of one allocation."""
+    Outputs of up to 16 MB together are parts of one allocation."""
     return C.add_rms_norm_fp8(x, residual, weight, eps, normed, quantized, residual_out, _handle(stream))
 
 

@@ -62,10 +62,11 @@ struct Where {
 };
 
 // The outputs of one call.  An allocation costs 0.8 us of the host's time, so
-// small outputs (kShared bytes at most) are parts of one.
+// outputs of up to kShared bytes together, whose kernel takes no longer than that, are
+// parts of one.
 class Outputs {
  public:
-  static constexpr int64_t kShared = 256 << 10, kAlign = 256;
+  static constexpr int64_t kShared = 16 << 20, kAlign = 256;
   Outputs(const Where& at, int64_t bytes, int count) : at_(at) {
     if (count > 1 && bytes + count * kAlign <= kShared) pool_ = at.empty({bytes + count * kAlign}, at::kByte);
   }

@@ -125,7 +125,7 @@ def test_norm_no_rows_own_stream_and_graph():
                                                                                     c.view(torch.uint8))
 
 
-@pytest.mark.parametrize("T,H", [(1, 128), (3, 144), (1001, 512)])  # one allocation for all outputs, and one each
+@pytest.mark.parametrize("T,H", [(1, 128), (3, 144), (1001, 512), (9000, 272)])  # one allocation for all outputs, and one each
 def test_outputs_do_not_overlap(T, H):
     import torch
     from nvfp4_mixture_experts_expert_gb300 import api
