@@ -22,10 +22,17 @@
 //   warps 4-11  epilogue: a TMEM lane quarter and half of the columns each
 // Every wait is bounded and reports in the library's status word.
 //
-// Measured (8192 x 4096 x 4096, bf16 out): 113 us, 2.44 PFLOP/s, 0.63 of twice
-// the measured bf16 rate.  The tile's operands are 48 KB a block and SM, 15 TB/s
-// out of L2 over the SMs at this rate; without the copies (operands stale,
-// timing only) the kernel took a tenth less.
+// Measured (8192 x 4096 x 4096, bf16 out): 109 us in a row of launches, 2.5 PFLOP/s,
+// 0.66 of twice the measured bf16 rate (117 us over seconds, under the power
+// cap).  A K-block of a 128 x 256 tile takes ~900 cycles where its MMAs take 512:
+// the issuers wait for accumulators, of which TMEM holds two, and an accumulator's
+// way round (MMA, commit, the epilogue's wait of ~120 cycles and read of ~400,
+// arrival, issue ~200) is 1,700.  Built and not faster: CTA pairs with 256 x 256
+// tiles, which copy a third less a block (115 us), also with accumulators by column
+// halves (115); w's scales through shared memory as a's are (109 to 112); an
+// epilogue that enters the next block before it adds up the last columns of this
+// one (129); column counts between (224, 192, 160, 96: two scales a warp; 2048 x
+// 6144 x 3584 51 us with 224 against 49).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -306,19 +313,25 @@ __device__ void epilogue_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t 
       const uint32_t at = t0 + buf * BN;
       const float s0 = sa0 * sw0;
       const uint64_t ss = f2_pack(s0, s0);
-      uint32_t d[W];
+      // 256 columns: the next 16 on their way while these are added (2048 x 6144 x 3584 in 46.0 us instead of
+      // 48.4; at 128 and 64 columns it costs up to 3 %)
+      constexpr int AHEAD = BN == 256 ? 2 : 1;
+      uint32_t d[AHEAD][W];
+      tmem_load_cols(at, d[0]);
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c) {
-        tmem_load_cols(at + W * c, d);
+        uint32_t(&now)[W] = d[c % AHEAD];
+        if (AHEAD == 1 && c > 0) tmem_load_cols(at + W * c, now);
         tmem_load_wait();
 #pragma unroll
-        for (int i = 0; i < W; ++i) asm volatile("" : "+r"(d[i]));  // no use of d moves above the wait
+        for (int i = 0; i < W; ++i) asm volatile("" : "+r"(now[i]));  // no use of it moves above the wait
+        if (AHEAD == 2 && c + 1 < CHUNKS) tmem_load_cols(at + W * (c + 1), d[(c + 1) % AHEAD]);
         if (c + 1 == CHUNKS) {  // everything is in registers: the accumulator is free
           tc_fence_before();
           __syncwarp();
           arrive_if(lane == 0, L.acc_empty + 8 * buf);
         }
-        add_scaled(acc + W / 2 * c, d, ss);
+        add_scaled(acc + W / 2 * c, now, ss);
       }
       sw0 = sw1;
       if (sk == kScaleKb - 1 || kb + 1 == g.kb1) {
