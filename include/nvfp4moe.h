@@ -527,7 +527,8 @@ int nvfp4_add_rmsnorm_fp8(const void* x, int64_t ld_x, const void* residual, int
  *   out      device bf16 [M][N], or f32 with out_is_f32 != 0, row stride ld_out
  * N % 8 == 0, K % 16 == 0, ld_a >= K and a multiple of 16, ld_out >= N and a
  * multiple of 8, 0 <= M <= 1048576 (0: no work), N, K <= 1048576.  Pointers
- * 16-byte aligned, scales 4-byte aligned.
+ * 16-byte aligned, scales 4-byte aligned.  A device-side timeout is reported in
+ * the library's status word (nvfp4_device_status).
  */
 int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const void* w, const float* w_scale, int64_t M,
                      int64_t N, int64_t K, void* out, int64_t ld_out, int out_is_f32, void* stream);
@@ -542,7 +543,7 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
  * silu(min(g, gate_limit)) * clamp(u, +-up_limit) is kept to 11 bits or more,
  * sums are FP32, and each output is rounded to bf16 once.  So no activation
  * scales are needed, and the result is nearer to the weights' exact layer than
- * nvfp4_moe_forward's (which is the faster one for more tokens).
+ * nvfp4_moe_forward's (which is the faster one from about 24 tokens on).
  *   hidden   device bf16 [T][H], row stride ld_hidden (elements, a multiple of 8)
  *   router_logits  device f32 [T][E]
  *   w13 .. w2_gs   as nvfp4_moe_forward

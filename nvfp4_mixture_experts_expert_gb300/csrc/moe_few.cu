@@ -50,13 +50,13 @@
 // I 2048, top 6: 680 MB) 100 us at the rate of a copy; the layer takes 134, of
 // which the first launch's stream runs at 6.5 TB/s.  The rest is what comes
 // before a launch's first tile (routing, activations, the ring's first copies),
-// the way from one launch to the next and the sum: ~20 us of one token's 31,
-// whose weights take 12.5.  Measured beside what was kept (warm, 8 / 32 tokens):
-// sixteen consumer warps 84 / 155 us where eight took 83 / 156 and then less
-// with every step that shortened the waits; weights not marked for early eviction
-// 90 / 165 instead of 83 / 156 (they push scales, activations and the next
-// launch's weights out of L2); waiting warps that poll instead of sleeping 2 %;
-// the consumers' products with the next tiles' reads in front of them 102 / 187.
+// the way from one launch to the next and the sum: ~18 us of one token's 31,
+// whose weights take 12.5.  Measured beside what was kept, at the time (8 / 32
+// tokens, us in a row of calls): sixteen consumer warps 85 / 161 where eight took
+// 83 / 156; weights not marked for early eviction 90 / 165 instead of 83 / 156
+// (they push scales, activations and the next launch's weights out of L2); warps
+// that wait by polling 94 / 172 instead of 92 / 169; consumers that read the next
+// tiles before they finish the last products 103 / 187 instead of 92 / 169.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

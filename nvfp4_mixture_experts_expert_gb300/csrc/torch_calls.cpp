@@ -1,7 +1,7 @@
 // Host side of the operators that take a few microseconds on the GPU: argument
 // checks, outputs and the C-ABI call in one extension function, on torch's C++
 // tensors.  The same in Python (checks, torch.empty, ctypes) takes 12 us for
-// one output and 19 us for four, longer than the kernels; this takes 4 and 6.
+// one output and 19 us for four, longer than the kernels; this takes 3 to 4 us.
 // api.py documents the calls and is their public form.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -61,9 +61,9 @@ struct Where {
   }
 };
 
-// The outputs of one call.  An allocation costs 0.8 us of the host's time, so
-// outputs of up to kShared bytes together, whose kernel takes no longer than that, are
-// parts of one.
+// The outputs of one call.  Each allocation costs 0.8 us of the host's time, and
+// up to about kShared bytes the kernel takes less than four of them with the
+// launch (5.7 us), so smaller outputs are parts of one (4.2 us).
 class Outputs {
  public:
   static constexpr int64_t kShared = 16 << 20, kAlign = 256;
