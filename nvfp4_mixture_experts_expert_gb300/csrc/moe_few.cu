@@ -47,16 +47,21 @@
 // brought into L2, so HBM idles little between the two.
 //
 // Bound: reading the chosen experts' weights, at 32 tokens (48 experts of H 4096,
-// I 2048, top 6: 680 MB) 100 us at the rate of a copy; the layer takes 134, of
+// I 2048, top 6: 680 MB) 100 us at the rate of a copy; the layer takes 127, of
 // which the first launch's stream runs at 6.5 TB/s.  The rest is what comes
 // before a launch's first tile (routing, activations, the ring's first copies),
-// the way from one launch to the next and the sum: ~18 us of one token's 31,
+// the way from one launch to the next and the sum: ~18 us of one token's 30,
 // whose weights take 12.5.  Measured beside what was kept, at the time (8 / 32
 // tokens, us in a row of calls): sixteen consumer warps 85 / 161 where eight took
 // 83 / 156; weights not marked for early eviction 90 / 165 instead of 83 / 156
 // (they push scales, activations and the next launch's weights out of L2); warps
 // that wait by polling 94 / 172 instead of 92 / 169; consumers that read the next
 // tiles before they finish the last products 103 / 187 instead of 92 / 169.
+//
+// Size counts too: most of the code runs once a launch, behind misses of the
+// instruction cache, so loops off the stream are kept rolled.  127 and 105 KB of
+// code in the two launches took 0.6 to 1.1 us more than 91 and 74 (3 % at one
+// token, 4 % at 5 tokens of a small layer), 147 and 125 KB another 5.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -113,6 +118,7 @@ __device__ __forceinline__ void route_one(const FewArgs& p, int t, int lane, int
       key[i] = e < p.E ? route_key(__ldg(p.logits + (int64_t)t * p.E + e), e) : 0ull;
     }
     uint64_t mine = 0ull;
+#pragma unroll 1
     for (int j = 0; j < p.k; ++j) {
       uint64_t best = key[0];
 #pragma unroll
@@ -146,6 +152,7 @@ __device__ __forceinline__ void route_one(const FewArgs& p, int t, int lane, int
     }
     float all = 0.f;
     int first = lane;
+#pragma unroll 1
     for (int j = p.k - 1; j >= 0; --j) {
       const int oid = __shfl_sync(0xffffffffu, id, j);
       const float ow = __shfl_sync(0xffffffffu, w, j);
@@ -171,8 +178,10 @@ __device__ void route_all(const FewArgs& p, Route* r) {
   __shared__ int32_t s_first[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int e = tid; e < 256; e += kThreads) s_mask[e] = 0u;
-  for (int i = tid; i < kFewAssignments * kGroup; i += kThreads) (&r->member[0][0])[i] = -1;
+#pragma unroll 1
+  for (int i = tid; i < kFewAssignments * kGroup / 8; i += kThreads) reinterpret_cast<uint4*>(r->member)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
   __syncthreads();
+#pragma unroll 1
   for (int t = warp; t < p.T; t += kThreads / 32) {
     if (p.E <= 32)
       route_one<1>(p, t, lane, r->id, r->weight, s_mask);
@@ -204,6 +213,7 @@ __device__ void route_all(const FewArgs& p, Route* r) {
     if (lane == 31) r->n_list = incl;
   }
   __syncthreads();
+#pragma unroll 1
   for (int a = tid; a < p.T * p.k; a += kThreads) {
     const int e = r->id[a], t = a / p.k;
     if (e < 0) continue;
@@ -445,6 +455,7 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
     if (leader) {
       const uint32_t w = L.slots + stage * g.stage_bytes, bar = L.full + 8 * stage;
       mbar_arrive_expect_tx(bar, 8 * g.K * g.R);
+#pragma unroll 1
       for (int i = 0; i < g.R; ++i) {
         const TileAt<PHASE> at(g, e, t.tile * g.R + i);
         load_5d(w + i * 8 * g.K, &m.w, at.line, at.block, bar, policy);
@@ -474,11 +485,13 @@ __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, cons
     if (!warp_wait_asleep(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status)) break;
     const int e = r->expert[t.v];
     uint32_t to = L.slots + stage * g.stage_bytes + 8 * g.K * g.R + lane * 16;
+#pragma unroll 1
     for (int i = 0; i < g.R; ++i) {
       const TileAt<PHASE> at(g, e, t.tile * g.R + i);
       const int block = at.block + (PHASE == 0 ? (line >> 1) * (g.blocks / 2) : 0);
       const uint8_t* from = all + ((int64_t)block * cts + (lane >> 2)) * 512 +
                             (at.line + (PHASE == 0 ? line & 1 : line)) * 16;
+#pragma unroll 4
       for (int ct = lane >> 2; ct < cts; ct += 8, from += 8 * 512, to += 512)
         asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
                      "l"(policy)
@@ -500,8 +513,10 @@ __device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
   int u0, u1;
   share_of(r->n_list, g.tiles, u0, u1);
   if (!elect_one()) return;
+#pragma unroll 1
   for (int u = u0; u < min(u1, u0 + kPrefetch); ++u) {
     const Unit t = unit_at(u, g.tiles);
+#pragma unroll 1
     for (int i = 0; i < g.R; ++i) {
       const TileAt<1> at(g, r->expert[t.v], t.tile * g.R + i);
       asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %1, %1, %3}];" ::"l"(
@@ -567,30 +582,40 @@ __device__ __forceinline__ float load_activations(const FewArgs& p, const Phase&
   return inverse;
 }
 
+// 32 bytes (a whole sector), past L1.
+__device__ __forceinline__ void load_sector(const float* p, float (&v)[8]) {
+  asm volatile("ld.relaxed.gpu.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p)
+               : "memory");
+}
 // The same for h with four slabs a warp at most: the FP32 values stay in
 // registers between their maximum and their rounding, so that all loads are in
 // flight together, once (32 tokens: 142 us instead of 155; all SMs read h at the
-// same time).
+// same time), by whole sectors (128 instead of 134: 16 bytes a lane would take
+// each sector twice).
 template <int SPW>
 __device__ __forceinline__ float load_h(const FewArgs& p, const Phase& g, int a, int kg, int q, uint32_t (&b)[SPW][16]) {
   const float* h = p.h + (int64_t)(a < 0 ? 0 : a) * p.I + q * 32;
-  float4 v[SPW][8];
+  float v[SPW][4][8];
 #pragma unroll
   for (int s = 0; s < SPW; ++s) {
     const int slab = kg + s * g.KG;
     const bool in = slab < g.K / 128 && a >= 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[s][i] = in ? __ldcg(reinterpret_cast<const float4*>(h + slab * 128) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[s][i][j] = 0.f;
+      if (in) load_sector(h + slab * 128 + 8 * i, v[s][i]);
+    }
   }
   float amax = 0.f;
 #pragma unroll
   for (int s = 0; s < SPW; ++s)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 u = v[s][i];
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[s][i][j]));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   float inverse;
@@ -598,11 +623,10 @@ __device__ __forceinline__ float load_h(const FewArgs& p, const Phase& g, int a,
 #pragma unroll
   for (int s = 0; s < SPW; ++s)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 u = v[s][i];
-      b[s][2 * i] = pack_f16x2(u.x * scale, u.y * scale);
-      b[s][2 * i + 1] = pack_f16x2(u.z * scale, u.w * scale);
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        b[s][4 * i + j] = pack_f16x2(v[s][i][2 * j] * scale, v[s][i][2 * j + 1] * scale);
   return inverse;
 }
 
@@ -711,7 +735,7 @@ __device__ __forceinline__ void join_loop(const FewArgs& p, const Phase& g, cons
     const uint32_t from = L.part + buf * (kWarps * 512) + lane * 16;
     float* to0 = (PHASE == 0 ? p.h : p.y) + (int64_t)a0 * n;
     float* to1 = (PHASE == 0 ? p.h : p.y) + (int64_t)a1 * n;
-#pragma unroll 2
+#pragma unroll 1
     for (int sub = 0; sub < R; ++sub) {
       float c[4];
 #pragma unroll
