@@ -369,7 +369,7 @@ struct Unit {
   }
 };
 __device__ __forceinline__ Unit unit_at(int u, int tiles) {
-  const int v = u / tiles;
+  const int v = (int)((uint32_t)u / (uint32_t)tiles);
   return {v, u - v * tiles};
 }
 
@@ -378,13 +378,13 @@ __device__ __forceinline__ Unit unit_at(int u, int tiles) {
 // the entries first where that leaves none with more than kEntryTiles over its
 // even share of all units (8 tokens: 74.7 us instead of 77.7; 32: 138 instead of 141).
 __device__ __forceinline__ void share_of(int n, int tiles, int& u0, int& u1) {
-  const int G = gridDim.x, c = blockIdx.x;
-  const int64_t units = (int64_t)n * tiles;
-  const int even = (int)((units + G - 1) / G);
-  if (n > 0 && n <= G && (tiles + G / n - 1) / (G / n) <= even + kEntryTiles) {
-    const int v = ((c + 1) * n - 1) / G, c0 = v * G / n, count = (v + 1) * G / n - c0;
-    u0 = v * tiles + tiles * (c - c0) / count;
-    u1 = v * tiles + tiles * (c - c0 + 1) / count;
+  const uint32_t G = gridDim.x, c = blockIdx.x;
+  const uint32_t units = (uint32_t)n * tiles;  // at most 256 * 1024: times G within 32 bits
+  const uint32_t even = (units + G - 1) / G;
+  if (n > 0 && (uint32_t)n <= G && (tiles + G / n - 1) / (G / n) <= even + kEntryTiles) {
+    const uint32_t v = ((c + 1) * n - 1) / G, c0 = v * G / n, count = (v + 1) * G / n - c0;
+    u0 = (int)(v * tiles + tiles * (c - c0) / count);
+    u1 = (int)(v * tiles + tiles * (c - c0 + 1) / count);
   } else {
     u0 = (int)(units * c / G);
     u1 = (int)(units * (c + 1) / G);
