@@ -3,7 +3,8 @@
 // tensors.  The same in Python (checks, torch.empty, ctypes) takes 12 us for
 // one output and 19 us for four, longer than the kernels; this takes 3 to 4 us.
 // api.py documents the calls and is their public form.
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -56,33 +57,44 @@ struct Where {
       guard.reset_stream(c10::cuda::getStreamFromExternal(stream, dev.index()));
     }
   }
+  // From the caching allocator, on this stream.
+  c10::Storage storage(int64_t bytes) const {
+    c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
+    return c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                              from->allocate(bytes), from, /*resizable=*/true));
+  }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) const {
-    return at::Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
+    return part(storage(c10::multiply_integers(shape) * (int64_t)c10::elementSize(dtype)), 0, shape, dtype);
+  }
+  // A contiguous tensor `offset` bytes into a storage.
+  static at::Tensor part(c10::Storage s, int64_t offset, at::IntArrayRef shape, at::ScalarType dtype) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        std::move(s), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(dtype));
+    if (offset) t.unsafeGetTensorImpl()->set_storage_offset(offset / (int64_t)c10::elementSize(dtype));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return t;
   }
 };
 
-// The outputs of one call.  Each allocation costs 0.8 us of the host's time, and
-// up to about kShared bytes the kernel takes less than four of them with the
-// launch (5.7 us), so smaller outputs are parts of one (4.2 us).
+// The outputs of one call, parts of one allocation where they are small: up to
+// about kShared bytes the kernel takes no longer than the host does with an
+// allocation for each (5.0 us with four, 3.7 with one for all).
 class Outputs {
  public:
   static constexpr int64_t kShared = 16 << 20, kAlign = 256;
   Outputs(const Where& at, int64_t bytes, int count) : at_(at) {
-    if (count > 1 && bytes + count * kAlign <= kShared) pool_ = at.empty({bytes + count * kAlign}, at::kByte);
+    if (count > 1 && bytes + count * kAlign <= kShared) pool_ = at.storage(bytes + count * kAlign);
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) {
     if (!pool_) return at_.empty(shape, dtype);
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-        c10::Storage(pool_->storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(dtype));
-    t.unsafeGetTensorImpl()->set_storage_offset(used_ / (int64_t)t.itemsize());
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    used_ += (t.numel() * (int64_t)t.itemsize() + kAlign - 1) / kAlign * kAlign;
-    return t;
+    const int64_t at = used_, bytes = c10::multiply_integers(shape) * (int64_t)c10::elementSize(dtype);
+    used_ += (bytes + kAlign - 1) / kAlign * kAlign;
+    return Where::part(pool_, at, shape, dtype);
   }
 
  private:
   const Where& at_;
-  std::optional<at::Tensor> pool_;
+  c10::Storage pool_;
   int64_t used_ = 0;
 };
 
