@@ -494,7 +494,8 @@ int nvfp4_moe_set_stage_events(void* const* events, int n_events);
  *   s = x + residual (FP32; x alone with residual NULL)
  *   y = s * rsqrt(mean over the row of s^2 + eps) * weight (FP32)
  *   scales[t][c] = max(max |y| over columns 128c..128c+127, 2^-40) / 448
- *   q[t][i] = E4M3(y / scale of its block), round to nearest even
+ *   q[t][i] = E4M3(y / scale of its block), round to nearest even (the quotient by
+ *   the scale as stored, in FP32)
  * Every output is rounded once, from the FP32 value.  A NaN or an infinity in
  * a row makes the row's y NaN where 32-bit arithmetic gives NaN, scales included.
  *   x, residual   device bf16 [T][H], row strides ld_x, ld_residual (elements)

@@ -3,7 +3,7 @@
 //   s = x + residual                       (FP32; bf16(s) is the next residual)
 //   y = s * rsqrt(mean(s^2) + eps) * w     (FP32; bf16(y) is the normed output)
 //   per block of 128 columns of a row:
-//     scale = max(max|y|, 2^-40) / 448,  q = E4M3(y * (448 / max(max|y|, 2^-40)))
+//     scale = max(max|y|, 2^-40) / 448,  q = E4M3(y / scale)       (both quotients in FP32)
 //
 // s and y stay in FP32 registers; every output is rounded once.  The floor of
 // 2^-40 keeps the scale of an all-zero block finite (its codes are 0).  A NaN
@@ -35,6 +35,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// a / b in FP32 from the rounded reciprocal of b: the product's remainder is exact in a fused multiply-add and
+// corrects it (Markstein, IBM J. Res. Dev. 34, 1990).  An infinite b (reciprocal 0) gives a * 0.  The product
+// alone lies an ulp or two off, and beside a tie takes the neighbouring code; eight divisions a vector would take
+// 47.9 us instead of 44.9 at 8192 x 4096, 27.1 instead of 22.5 at 2048 x 7168.
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+  const float q = a * inv;
+  return inv == 0.f ? q : fmaf(fmaf(-q, b, a), inv, q);
 }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -128,13 +137,15 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_BLOCKS) add_rmsnorm_fp8_kerne
 #pragma unroll
       for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       amax = max_nan(amax, kMinAmax);
-      const float inv = 448.f / amax;
+      const float scale = quotient(amax, 448.f, 1.f / 448.f), inv = 1.f / scale;
       if (in) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = quotient(y[i], scale, inv);
         uint2 c;
-        c.x = e4m3x2_code(y[0] * inv, y[1] * inv) | (e4m3x2_code(y[2] * inv, y[3] * inv) << 16);
-        c.y = e4m3x2_code(y[4] * inv, y[5] * inv) | (e4m3x2_code(y[6] * inv, y[7] * inv) << 16);
+        c.x = e4m3x2_code(y[0], y[1]) | (e4m3x2_code(y[2], y[3]) << 16);
+        c.y = e4m3x2_code(y[4], y[5]) | (e4m3x2_code(y[6], y[7]) << 16);
         *reinterpret_cast<uint2*>(p.q + row * p.H + at * 8) = c;
-        if ((lane & 15) == 0) p.scales[row * cols + at / 16] = amax / 448.f;
+        if ((lane & 15) == 0) p.scales[row * cols + at / 16] = scale;
       }
     }
   }
