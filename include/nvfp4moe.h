@@ -497,7 +497,8 @@ int nvfp4_moe_set_stage_events(void* const* events, int n_events);
  *   q[t][i] = E4M3(y / scale of its block), round to nearest even (the quotient by
  *   the scale as stored, in FP32)
  * Every output is rounded once, from the FP32 value.  A NaN or an infinity in
- * a row makes the row's y NaN where 32-bit arithmetic gives NaN, scales included.
+ * a row makes the row's y NaN where 32-bit arithmetic gives NaN, scales included;
+ * so does a zero row with eps = 0 (0 * rsqrt(0)).
  *   x, residual   device bf16 [T][H], row strides ld_x, ld_residual (elements)
  *   weight        device bf16 [H], or f32 [H] with weight_is_f32 != 0
  *   residual_out  device bf16 [T][H] (bf16(s)), row stride ld_residual_out, or

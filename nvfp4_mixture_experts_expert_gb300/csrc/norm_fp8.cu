@@ -7,7 +7,8 @@
 //
 // s and y stay in FP32 registers; every output is rounded once.  The floor of
 // 2^-40 keeps the scale of an all-zero block finite (its codes are 0).  A NaN
-// in a row makes the whole row NaN (scales included).
+// in a row makes the whole row NaN (scales included), and so does a mean square
+// of 0 without eps.
 //
 // Bound: HBM.  A row is read once and its outputs written once, 9 bytes an
 // element with every output.  What made the difference (8192 x 4096, 302 MB,

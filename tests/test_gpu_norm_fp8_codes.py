@@ -1,4 +1,4 @@
-"""The FP8 codes of the norm beside ties.
+"""The FP8 codes of the norm beside ties, and its zero rows with and without eps.
 
 With rows of +-1 the mean square is 1 and, at eps = 0, y is the FP32 weight with
 the row's signs, exactly: the codes have one right value."""
@@ -53,3 +53,19 @@ def test_codes_are_the_quotients_by_the_stored_scale(blocks):
     want_q, want_scale = quotient_codes(x * w)
     assert torch.equal(y.cpu(), (x * w).bfloat16()) and torch.equal(scale.cpu(), want_scale)
     assert torch.equal(q.view(torch.uint8).cpu(), want_q.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_zero_rows_without_eps_are_nan_and_with_it_zero():
+    """As 32-bit arithmetic has it: 0 * rsqrt(0) = 0 * inf."""
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x = torch.randn(3, 640, device="cuda").bfloat16()
+    x[1] = 0
+    w = torch.ones(640, device="cuda")
+    q, scale, y, _ = api.add_rms_norm_fp8(x, None, w, 0.0)
+    assert torch.isnan(y[1]).all() and torch.isnan(scale[1]).all() and torch.isnan(q[1].float()).all()
+    for t in (0, 2):
+        assert torch.isfinite(y[t]).all() and torch.isfinite(scale[t]).all() and torch.isfinite(q[t].float()).all()
+    q, scale, y, _ = api.add_rms_norm_fp8(x, None, w, 1e-20)
+    assert (y[1] == 0).all() and (q[1].float() == 0).all() and (scale[1] == 2.0 ** -40 / 448).all()
