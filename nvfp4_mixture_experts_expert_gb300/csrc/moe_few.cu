@@ -13,9 +13,15 @@
 // long as both operands use the same one, so a lane takes 32 consecutive
 // weights (16 bytes, two scale blocks) of its rows.  The tokens are the N
 // operand, eight at a time: an expert with more of them is listed again for
-// the next eight.  A slab of a token's activations is scaled by a power of two
-// that puts its largest value at 2^14..2^15 (exact for bf16; 11 bits are kept
-// of the FP32 h) and the sum is scaled back in FP32.
+// the next eight.
+//
+// A token's activations are scaled by a power of two, one for a warp's share of
+// K, that puts their largest at 2^14..2^15, and the sum is scaled back in FP32.
+// bf16 values down to 2^-31 of the largest are then exact in f16; what the rounding
+// of smaller ones leaves is added in passes of its own (add_rest), so x is used
+// exactly.  The FP32 h is rounded to 11 bits, and to 2^-39 of the share's largest
+// below 2^-28 of it: an eighth of what the output's rounding to bf16 does, where
+// a second f16 term for its other bits would double the products.
 //
 // The 128 x 4 scale tiles keep rows r, r + 32, r + 64, r + 96 in one 16-byte
 // line, so the rows of an m16 tile are taken as whole lines: W13, 2 lines of
@@ -316,9 +322,15 @@ __device__ __forceinline__ float slab_scale(float amax, float& inverse) {
   inverse = pow2f(-s);
   return pow2f(s);
 }
+__device__ __forceinline__ int exponent_of(float pow2) { return (int)(__float_as_uint(pow2) >> 23) - 127; }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float rounded_f16(float v) {
+  float r;
+  asm("{\n.reg .b16 h;\ncvt.rn.f16.f32 h, %1;\ncvt.f32.f16 %0, h;\n}" : "=f"(r) : "f"(v));
   return r;
 }
 // 2 ulp in the quotient; a denominator past 2^126 gives 0 for a gate below -87.
@@ -397,6 +409,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t at) {
@@ -528,29 +545,70 @@ __device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
 }
 
 // ------------------------------------------------------------------ consumers
-// This lane's activations of its token (assignment a, -1: none) for the warp's
-// slabs, as f16 pairs scaled by one power of two; returns its inverse.
-template <int PHASE, int SPW>
-__device__ __forceinline__ float load_activations(const FewArgs& p, const Phase& g, int a, int kg, int q,
-                                                  uint32_t (&b)[SPW][16]) {
+// This lane's activations of its token for the warp's slabs, as f16 pairs scaled
+// by one power of two, whose inverse is returned.  x (of assignment a, -1: none):
+// `rest` is the number of passes that its values too small for f16 beside the
+// largest need (the warp's tokens' most; 0 but for rows whose values span more
+// than 2^31).  Magnitudes are compared as bf16 bits, two at a time.
+template <int SPW>
+__device__ __forceinline__ float load_x(const FewArgs& p, const Phase& g, int a, int kg, int q, uint32_t (&b)[SPW][16],
+                                        int& rest) {
   const int slabs = g.K / 128;
-  float amax = 0.f;
-  const uint16_t* x = PHASE == 0 ? p.x + (int64_t)(a < 0 ? 0 : a / p.k) * p.ld_x + q * 32 : nullptr;
-  const float* h = PHASE == 1 ? p.h + (int64_t)(a < 0 ? 0 : a) * p.I + q * 32 : nullptr;
+  const uint16_t* x = p.x + (int64_t)(a < 0 ? 0 : a / p.k) * p.ld_x + q * 32;
+  uint32_t most = 0u, least = 0x7fff7fffu;  // of two columns; least of |x| + 0x7fff, signed: 0 comes last
 #pragma unroll
   for (int s = 0; s < SPW; ++s) {
     const int slab = kg + s * g.KG;
     if (slab >= slabs || a < 0) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) b[s][i] = 0u;
-    } else if (PHASE == 0) {
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + slab * 128) + i);
         b[s][4 * i] = u.x, b[s][4 * i + 1] = u.y, b[s][4 * i + 2] = u.z, b[s][4 * i + 3] = u.w;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(b[s][i])), fabsf(bf16_hi(b[s][i]))));
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t mag = b[s][i] & 0x7fff7fffu;
+        most = __vmaxs2(most, mag);
+        least = __vmins2(least, mag + 0x7fff7fffu);
+      }
+    }
+  }
+  most = __vmaxs2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = __vmaxs2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  least = __vmins2(least, __shfl_xor_sync(0xffffffffu, least, 1));
+  least = __vmins2(least, __shfl_xor_sync(0xffffffffu, least, 2));
+  const uint32_t top = max(most & 0xffffu, most >> 16);
+  const uint32_t low = min((least & 0xffffu) ^ 0x8000u, (least >> 16) ^ 0x8000u);  // the smallest above 0, less 1
+  float inverse;
+  const float scale = slab_scale(__uint_as_float(top << 16), inverse);
+  const int exponent = exponent_of(scale), field = max((int)(low + 1) >> 7, 1), left = 78 - field - exponent;
+  // 8 bits are exact in f16 from 2^-17 on; what is left down to the smallest value's last bit, 2^(field - 134), is
+  // exact by add_rest's passes, of which the first adds 39 to the exponent and each other 32.  Beside an infinity
+  // or a NaN nothing is missed.
+  rest = top >= 0x7f80u || (int)(low + 1) >> 7 >= 110 - exponent ? 0 : left <= 0 ? 1 : 1 + (left + 31) / 32;
+  rest = (int)__reduce_max_sync(0xffffffffu, (uint32_t)rest);
+#pragma unroll
+  for (int s = 0; s < SPW; ++s)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[s][i] = pack_f16x2(bf16_lo(b[s][i]) * scale, bf16_hi(b[s][i]) * scale);
+  return inverse;
+}
+// h with more than four slabs a warp.
+template <int SPW>
+__device__ __forceinline__ float load_long_h(const FewArgs& p, const Phase& g, int a, int kg, int q,
+                                             uint32_t (&b)[SPW][16]) {
+  const int slabs = g.K / 128;
+  float amax = 0.f;
+  const float* h = p.h + (int64_t)(a < 0 ? 0 : a) * p.I + q * 32;
+#pragma unroll
+  for (int s = 0; s < SPW; ++s) {
+    const int slab = kg + s * g.KG;
+    if (slab >= slabs || a < 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) b[s][i] = 0u;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -567,16 +625,11 @@ __device__ __forceinline__ float load_activations(const FewArgs& p, const Phase&
   for (int s = 0; s < SPW; ++s) {
     const int slab = kg + s * g.KG;
     if (slab >= slabs || a < 0) continue;
-    if (PHASE == 0) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) b[s][i] = pack_f16x2(bf16_lo(b[s][i]) * scale, bf16_hi(b[s][i]) * scale);
-    } else {  // read again (from L2) rather than held: 32 FP32 values a slab
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(h + slab * 128) + i);
-        b[s][2 * i] = pack_f16x2(u.x * scale, u.y * scale);
-        b[s][2 * i + 1] = pack_f16x2(u.z * scale, u.w * scale);
-      }
+    for (int i = 0; i < 8; ++i) {  // read again (from L2) rather than held: 32 FP32 values a slab
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(h + slab * 128) + i);
+      b[s][2 * i] = pack_f16x2(u.x * scale, u.y * scale);
+      b[s][2 * i + 1] = pack_f16x2(u.z * scale, u.w * scale);
     }
   }
   return inverse;
@@ -630,20 +683,73 @@ __device__ __forceinline__ float load_h(const FewArgs& p, const Phase& g, int a,
   return inverse;
 }
 
+// v += the products of what load_x's rounding to f16 left of the smallest values.
+// Those remainders have 8 bits at most and lie below 2^-25 as scaled there; pass by
+// pass the ones of 32 powers of two are taken, from memory again, and go the way
+// of the others.  Slow, so its code is kept small, and off the way of any row
+// whose values lie within 2^31 of its largest.  `at`, `second`, `s_off`, `s_second`:
+// the tile, and in it the lane's second row and the scales of its two; `weight_at`:
+// its first row's weights of a slab.
+template <typename WeightAt>
+__device__ __forceinline__ void add_rest(const FewArgs& p, const Phase& g, int a, int kg, int q, float inverse, int rest,
+                                         float alpha, uint32_t at, uint32_t second, uint32_t s_off, uint32_t s_second,
+                                         const WeightAt& weight_at, float (&v)[4]) {
+  const uint16_t* x = p.x + (int64_t)(a < 0 ? 0 : a / p.k) * p.ld_x + q * 32;
+  const int first = -exponent_of(inverse);
+#pragma unroll 1
+  for (int pass = 0; pass < rest; ++pass) {
+    const int exponent = min(first + 39 + 32 * pass, 157);  // past 148 nothing is left
+    float c[4] = {};
+#pragma unroll 1
+    for (int i = kg * 4; i < g.K / 32; i = i % 4 == 3 ? i + 4 * g.KG - 3 : i + 1) {  // a quarter of a slab's 32 columns
+      const int slab = i / 4, part = i % 4;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (a >= 0) u = __ldg(reinterpret_cast<const uint4*>(x + slab * 128) + part);
+      const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float r[2] = {bf16_lo(in[j]), bf16_hi(in[j])};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          r[n] = fmaf(-rounded_f16(r[n] * pow2f(first)), inverse, r[n]) * pow2f(exponent / 2) *
+                 pow2f(exponent - exponent / 2);
+          if (!(fabsf(r[n]) >= 0x1p-17f && fabsf(r[n]) < 0x1p15f)) r[n] = 0.f;
+        }
+        b[j] = pack_f16x2(r[0], r[1]);
+      }
+      uint32_t f[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t s[2];
+        scale_pairs(lds16(at + s_off + (slab - kg) * 128 + n * s_second), s[0], s[1]);
+        decode8(lds32(at + weight_at(slab) + n * second + part * 4), part < 2 ? s[0] : s[1], f[n]);
+      }
+      mma_f16(c, f[0][0], f[1][0], f[0][1], f[1][1], b[0], b[1]);
+      mma_f16(c, f[0][2], f[1][2], f[0][3], f[1][3], b[2], b[3]);
+    }
+    const float down0 = pow2f(-(exponent / 2)), down1 = pow2f(exponent / 2 - exponent);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] += c[j] * alpha * __shfl_sync(0xffffffffu, down0, q * 8 + (j & 1) * 4) *
+              __shfl_sync(0xffffffffu, down1, q * 8 + (j & 1) * 4);
+  }
+}
+
 template <int PHASE, int SPW>
 __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, const Route* r, int u0, int u1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, q = lane & 3;
   const int kg = warp % g.KG, sub = warp / g.KG, slabs = g.K / 128;
   // this lane's two rows, slab by slab, and their scales
   const int row = copied_row(gr, g.wide);
+  const auto weight_at = [&](int slab) -> uint32_t {
+    return sub * 8 * g.K + (g.wide ? (slab >> 1) * (PHASE == 0 ? 1024 : 2048) + row * 128 +
+                                         ((((slab & 1) * 4 + q) ^ row) << 4)
+                                   : slab * (PHASE == 0 ? 512 : 1024) + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
+  };
   uint32_t w_off[SPW];
 #pragma unroll
-  for (int s = 0; s < SPW; ++s) {
-    const int slab = kg + s * g.KG;
-    w_off[s] = sub * 8 * g.K + (g.wide ? (slab >> 1) * (PHASE == 0 ? 1024 : 2048) + row * 128 +
-                                             ((((slab & 1) * 4 + q) ^ row) << 4)
-                                       : slab * (PHASE == 0 ? 512 : 1024) + row * 64 + ((q ^ (row >> 1 & 3)) << 4));
-  }
+  for (int s = 0; s < SPW; ++s) w_off[s] = weight_at(kg + s * g.KG);
   const uint32_t second = PHASE == 0 ? 4 * g.K : g.wide ? 1024 : 512;
   const uint32_t s_off = 8 * g.K * g.R + sub * g.K + kg * 128 + (q >> 1) * 64 + (q & 1) * 2 +
                          (PHASE == 0 ? (row & 1) * 16 + (row >> 1) * 4 : (row & 3) * 16 + (row >> 2) * 4);
@@ -651,17 +757,19 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
   const uint32_t part = L.part + warp * 512 + lane * 16;
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
   uint32_t b[SPW][16];
-  float i0 = 0.f, i1 = 0.f, alpha = 0.f;
+  float inv = 0.f, i0 = 0.f, i1 = 0.f, alpha = 0.f;
+  int rest = 0;
   Unit t = unit_at(u0, g.tiles);
   bool fresh = true;
   for (int u = u0; u < u1;) {
     if (fresh) {
       alpha = 1.f / __ldg((PHASE == 0 ? p.gs13 : p.gs2) + r->expert[t.v]);
-      float inv;
-      if constexpr (PHASE == 1 && SPW <= 4)
+      if constexpr (PHASE == 0)
+        inv = load_x<SPW>(p, g, r->member[t.v][gr], kg, q, b, rest);
+      else if constexpr (SPW <= 4)
         inv = load_h<SPW>(p, g, r->member[t.v][gr], kg, q, b);
       else
-        inv = load_activations<PHASE, SPW>(p, g, r->member[t.v][gr], kg, q, b);
+        inv = load_long_h<SPW>(p, g, r->member[t.v][gr], kg, q, b);
       i0 = __shfl_sync(0xffffffffu, inv, q * 8);
       i1 = __shfl_sync(0xffffffffu, inv, q * 8 + 4);
     }
@@ -698,6 +806,16 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
       if (i < n)  // alpha first: neither factor leaves FP32's range
         sts128(part + (i ? buf2 : buf) * (kWarps * 512), (c[i][0] + d[i][0]) * alpha * i0,
                (c[i][1] + d[i][1]) * alpha * i1, (c[i][2] + d[i][2]) * alpha * i0, (c[i][3] + d[i][3]) * alpha * i1);
+    if constexpr (PHASE == 0)
+      if (rest)
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const uint32_t to = part + (i ? buf2 : buf) * (kWarps * 512);
+          const uint4 sum = lds128(to);
+          float v[4] = {__uint_as_float(sum.x), __uint_as_float(sum.y), __uint_as_float(sum.z), __uint_as_float(sum.w)};
+          add_rest(p, g, r->member[t.v][gr], kg, q, inv, rest, alpha, i ? at1 : at0, second, s_off, s_second, weight_at, v);
+          sts128(to, v[0], v[1], v[2], v[3]);
+        }
     __syncwarp();
     arrive_if(lane == 0, L.empty + 8 * stage);
     arrive_if(lane == 0, L.part_full + 8 * buf);
