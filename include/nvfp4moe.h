@@ -541,9 +541,11 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
  *
  * Routing, SwiGLU and combine as nvfp4_moe_forward (top-k of the FP32 logits,
  * ties -> lower expert; softmax over the k chosen); the weights are the same
- * NVFP4 tensors.  The activations stay as they are: x is used exactly, h =
- * silu(min(g, gate_limit)) * clamp(u, +-up_limit) is kept to 11 bits or more,
- * sums are FP32, and each output is rounded to bf16 once.  So no activation
+ * NVFP4 tensors.  The activations stay as they are: x is used exactly, whatever
+ * its range; h = silu(min(g, gate_limit)) * clamp(u, +-up_limit) is rounded to 11
+ * bits, or to a multiple of 2^-38 of the largest |h| of its row where that is
+ * coarser (values under 2^-28 of the largest); sums are FP32, and each output is
+ * rounded to bf16 once.  So no activation
  * scales are needed, and the result is nearer to the weights' exact layer than
  * nvfp4_moe_forward's (which is the faster one from about 24 tokens on).
  *   hidden   device bf16 [T][H], row stride ld_hidden (elements, a multiple of 8)
