@@ -553,7 +553,8 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
  *   w13 .. w2_gs   as nvfp4_moe_forward
  *   out      device bf16 [T][H]
  * An assignment whose weight is 0 (a -inf logit) is not computed; a token with
- * none left (all logits -inf) gets a zero row.
+ * none left (all logits -inf) gets a zero row.  A NaN or +inf among the chosen
+ * logits makes the token's row NaN, as in nvfp4_moe_forward.
  * 0 <= T <= NVFP4_MOE_FEW_TOKENS_MAX (0: no work), H % 256 == 0, I % 128 == 0,
  * H and I <= 8192, E <= 256, top_k <= min(8, E), limits > 0.  The workspace (256-byte aligned,
  * nvfp4_moe_few_tokens_workspace_size() bytes; 0 for sizes out of range) serves

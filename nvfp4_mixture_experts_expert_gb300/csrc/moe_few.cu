@@ -112,7 +112,7 @@ __device__ __forceinline__ float clamp_up(float v, float hi) { return v > hi ? h
 
 // One warp per token: lane j < k gets the j-th choice.  An assignment of weight
 // 0 (a -inf logit, a zero weight of the caller's) is not computed; a token with
-// none left gets a zero row.  An expert named twice is computed once, with the
+// none left gets a zero row.  A largest logit of +inf or NaN makes the weights NaN.  An expert named twice is computed once, with the
 // sum of the two weights.  NK: logits a lane.
 template <int NK>
 __device__ __forceinline__ void route_one(const FewArgs& p, int t, int lane, int32_t* s_id, float* s_w,
@@ -145,7 +145,7 @@ __device__ __forceinline__ void route_one(const FewArgs& p, int t, int lane, int
     if (lane < p.k) {
       const float l = key_value(mine);
       id = key_expert(mine);
-      z = l == -INFINITY ? 0.f : l == top ? 1.f : expf(l - top);
+      z = l == -INFINITY ? 0.f : expf(l - top);
     }
     float sum = z;
 #pragma unroll
