@@ -34,3 +34,30 @@ def test_infinite_and_nan_logits_route_as_in_the_whole_forward():
     bad = torch.tensor([False, True, True, False, True, True, False, False], device="cuda")
     for out in (layer(x, logits, w), fwd(x, logits, w, a1, a2)):
         assert torch.equal(torch.isnan(out).all(1), bad) and torch.equal(torch.isnan(out).any(1), bad)
+
+
+def test_gates_far_below_zero_keep_their_silu():
+    """Gates of -85 to -88.6, where 1 + exp(-gate) passes 2^126, under up values of 2^100."""
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    T, H, I = 32, 256, 128
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w13 = torch.zeros(1, 2 * I, H, device="cuda")
+    w13[:, :I, :128] = -0.7
+    w13[:, I:, 128] = torch.randn(I, generator=g, device="cuda")
+    w = api.quantize_moe_weights(w13.bfloat16(), torch.randn(1, H, I, generator=g, device="cuda").bfloat16())
+    w13 = R.decode_nvfp4(w.w13[0], w.w13_sf[0], w.w13_gs[0], 2 * I, H)
+    x = torch.zeros(T, H, device="cuda")
+    x[:, :128] = (torch.linspace(-85, -88.5, T, device="cuda") / w13[0].sum())[:, None]
+    x[:, 128] = 2.0 ** 100
+    x = x.bfloat16()
+    gate, up = (x.double() @ w13.T).chunk(2, 1)
+    assert gate.min() > -88.65 and gate.max() < -84 and (gate < -87.4).sum() >= 4 * I
+    out = api.MoEFewTokens(T, H, I, 1, 1)(x, torch.zeros(T, 1, device="cuda"), w, 3e38, 3e38)
+    w2 = R.decode_nvfp4(w.w2[0], w.w2_sf[0], w.w2_gs[0], H, I)
+    h = gate * torch.sigmoid(gate) * up
+    ref = h @ w2.T
+    # the gate's absolute error is its silu's relative one; then expf, the quotient and the products, h's 11 bits, the sum
+    rel = 1.1 * gate.abs() * ((H / 16 * 2 + 40) * R.U32) + 16 * R.U32 + 2.0 ** -11 + (I / 16 * 2 + 40) * R.U32
+    tol = (h.abs() * rel) @ w2.abs().T
+    assert ((out.double() - ref).abs() <= tol + (ref.abs() + tol) * R.BF16).all()
