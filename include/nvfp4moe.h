@@ -428,8 +428,10 @@ int nvfp4_debug_gemm_trace(void* buffer, int stages, int tiles, int kind);
  * its L1 GEMM with the operand loads switched off and that wait limit, so the
  * GEMM gives up, records NVFP4_ERR_DEVICE_TIMEOUT in that call's workspace
  * status word and returns; the rest of the forward runs on whatever the L2
- * input buffer held (its output is meaningless, nothing faults).  0 switches
- * it off.  Process-wide; 0 <= timeout_ms <= 10000.
+ * input buffer held (its output is meaningless, nothing faults).  While it is
+ * on, nvfp4_fp8_linear (above 8 rows) loads a tile's first K-block alone and the
+ * few-token MoE layer a CTA's first tile; their waits give up after their own
+ * limit (about a second).  0 switches it off.  Process-wide; 0 <= timeout_ms <= 10000.
  */
 int nvfp4_moe_set_debug_stall(int timeout_ms);
 

@@ -163,7 +163,7 @@ int64_t moe_capacity(int64_t T, int E, int k) {
 
 void* g_stage_events[8] = {};
 int g_n_stage_events = 0;
-int g_debug_stall_ms = 0;  // > 0: MoE forwards launch their L1 GEMM with no operand loads (failure-detection test)
+int g_debug_stall_ms = 0;  // > 0: failure-detection check (nvfp4_moe_set_debug_stall)
 int g_l1_l2_overlap = 1;   // the L2 GEMM takes the L1 output per m-tile (nvfp4_moe_set_overlap)
 int g_swap_l2 = 0;         // small batches: the L2 GEMM with swapped operands (nvfp4_moe_set_swap_l2)
 
@@ -1025,6 +1025,7 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
     t.M = (int)M;
     t.N = (int)N;
     t.kbs = (int)((K + 127) / 128);
+    t.stall = g_debug_stall_ms > 0;
     cudaError_t e = launch_fp8_split(t, out_is_f32 != 0, dev->sms, (cudaStream_t)stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fp8_linear launch");
   }
@@ -1039,6 +1040,7 @@ int nvfp4_fp8_linear(const void* a, int64_t ld_a, const float* a_scale, const vo
     t.M = (int)M;
     t.N = (int)N;
     t.kbs = (int)((K + 127) / 128);
+    t.stall = g_debug_stall_ms > 0;
     cudaError_t e = fp8_gemm_plan(t, dev->sms);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_linear plan");
     if (int rc = make_byte_map(&t.map_a, a, M, K, ld_a, 128)) return rc;
@@ -1143,6 +1145,7 @@ static int moe_few_impl(const void* hidden, int64_t ld_hidden, const Routing& rt
   a.I = (int)I;
   a.E = E;
   a.k = top_k;
+  a.stall = g_debug_stall_ms > 0;
   a.gate_limit = gate_limit;
   a.up_limit = up_limit;
   FewMaps m13 = {}, m2 = {};

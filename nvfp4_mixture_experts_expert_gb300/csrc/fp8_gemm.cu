@@ -75,7 +75,7 @@ struct Cfg {
   static constexpr int TMEM_COLS = BUFS * BN;
   static constexpr int COLS = BN / 2;             // columns of an epilogue warp
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kEpiWarps * kStagingBytes +
-                                 kScaleSlots * kScaleSlotBytes + 8 * (2 * STAGES + BUFS + kMmaWarps + 2 * kScaleSlots) + 16;
+                                 kScaleSlots * kScaleSlotBytes + 8 * (2 * STAGES + BUFS + 2 * kScaleSlots) + 16;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   static_assert(STAGES % kMmaWarps == 0 && BUFS % kMmaWarps == 0, "each MMA warp has slots of its own");
   static_assert(STAGES >= BUFS, "a stage's barrier may not complete twice before the epilogue has seen it once");
@@ -87,7 +87,7 @@ struct Cfg {
 // epilogue has read an accumulator; sc_full, sc_empty[kScaleSlots]).
 template <int BN>
 struct Smem {
-  uint32_t stages, staging, scales, full, done, acc_empty, drain, sc_full, sc_empty;
+  uint32_t stages, staging, scales, full, done, acc_empty, sc_full, sc_empty;
   uint32_t* tmem_slot;
   int* abort_flag;
 };
@@ -103,8 +103,7 @@ __device__ __forceinline__ Smem<BN> carve(uint8_t* raw) {
   s.full = s.scales + kScaleSlots * kScaleSlotBytes;
   s.done = s.full + 8 * C::STAGES;
   s.acc_empty = s.done + 8 * C::STAGES;
-  s.drain = s.acc_empty + 8 * C::BUFS;
-  s.sc_full = s.drain + 8 * kMmaWarps;
+  s.sc_full = s.acc_empty + 8 * C::BUFS;
   s.sc_empty = s.sc_full + 8 * kScaleSlots;
   s.tmem_slot = reinterpret_cast<uint32_t*>(base + (s.sc_empty + 8 * kScaleSlots - s.stages));
   s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
@@ -143,9 +142,10 @@ __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;
+  const int kb1 = p.stall ? g.kb0 + 1 : g.kb1;
   for (int it = g.tile; it < p.tiles && ok && !*abort; it += g.step) {
     const Tile t = tile_at<BN>(p, it);
-    for (int kb = g.kb0; kb < g.kb1; ++kb) {
+    for (int kb = g.kb0; kb < kb1; ++kb) {
       ok = warp_wait(L.done + 8 * stage, phase ^ 1u, abort, p.status);
       if (!ok) break;
       if (leader) {
@@ -163,7 +163,8 @@ __device__ void load_loop(const Fp8GemmArgs& p, const Smem<BN>& L) {
       }
     }
   }
-  if (lane == 0 && (*abort || !ok)) {  // copies in flight land before the CTA exits
+  // The copies land before the warp leaves, also where another role gives up later.
+  if (lane == 0) {
     for (int s = 0; s < C::STAGES; ++s)
       if (issued & (1u << s)) {
         volatile int no_abort = 0;
@@ -223,6 +224,7 @@ __device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem,
   const uint64_t b0 = smem_desc(L.stages + C::A_BYTES, 16, 1024, 2);
   uint32_t stage = which, phase = 0, buf = which, buf_phase = 1;
   const int blocks = (g.kb1 - g.kb0) * ((p.tiles - g.tile + g.step - 1) / g.step);
+  uint32_t last = 0, last_phase = 0;
   bool issued = false;
   for (int b = which; b < blocks; b += kMmaWarps) {
     if (!warp_wait(L.full + 8 * stage, phase, abort, p.status) ||
@@ -239,6 +241,8 @@ __device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem,
     }
     __syncwarp();
     issued = true;
+    last = stage;
+    last_phase = phase;
     if ((stage += kMmaWarps) >= C::STAGES) {
       stage -= C::STAGES;
       phase ^= 1u;
@@ -248,15 +252,12 @@ __device__ void mma_loop(const Fp8GemmArgs& p, const Smem<BN>& L, uint32_t tmem,
       buf_phase ^= 1u;
     }
   }
-  if (__any_sync(0xffffffffu, *abort) && issued) {  // every MMA issued finishes before TMEM is freed
-    if (leader) tc_commit(L.drain + 8 * which);
-    __syncwarp();
-    if (lane == 0) {
-      volatile int no_abort = 0;
-      wait_bounded(L.drain + 8 * which, 0, &no_abort, nullptr, kDrainNs);
-    }
-    __syncwarp();
+  // The products end before the warp leaves and TMEM is freed, also where another role gives up later.
+  if (lane == 0 && issued) {
+    volatile int no_abort = 0;
+    wait_bounded(L.done + 8 * last, last_phase, &no_abort, nullptr, kDrainNs);
   }
+  __syncwarp();
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t (&v)[4]) {
@@ -450,7 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       mbar_init(L.done + 8 * s, 1);
     }
     for (int b = 0; b < C::BUFS; ++b) mbar_init(L.acc_empty + 8 * b, kEpiWarps);
-    for (int w = 0; w < kMmaWarps; ++w) mbar_init(L.drain + 8 * w, 1);
     for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(L.sc_full + 8 * i, 32);
       mbar_init(L.sc_empty + 8 * i, kEpiWarps);

@@ -49,7 +49,7 @@ struct SplitCfg {
   static constexpr int STAGES = NB == 16 ? 6 : 5;
   static constexpr int TMEM_COLS = kBufs * NB;
   static constexpr int CHUNK = kScaleBytes / (4 * NB);  // K-blocks whose scales are held at a time
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kScaleBytes + 8 * (2 * STAGES + kBufs + 1) + 16;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kScaleBytes + 8 * (2 * STAGES + kBufs) + 16;
   static_assert(SMEM <= 232448 && NB * kTileN * 4 <= STAGES * STAGE_BYTES, "the partial sums reuse the ring");
   static_assert(STAGES >= kBufs, "a stage's barrier may not complete twice before it has been seen once");
 };
@@ -69,7 +69,7 @@ __device__ __forceinline__ void ld_shared_2x64(uint32_t at, uint64_t& a, uint64_
 __device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 struct SplitSmem {
-  uint32_t stages, scales, full, done, acc_empty, drain;
+  uint32_t stages, scales, full, done, acc_empty;
   uint32_t* tmem_slot;
   int* abort_flag;
 };
@@ -83,8 +83,7 @@ __device__ __forceinline__ SplitSmem carve(uint8_t* raw) {
   s.full = s.scales + kScaleBytes;
   s.done = s.full + 8 * C::STAGES;
   s.acc_empty = s.done + 8 * C::STAGES;
-  s.drain = s.acc_empty + 8 * kBufs;
-  s.tmem_slot = reinterpret_cast<uint32_t*>(base + (s.drain + 8 - s.stages));
+  s.tmem_slot = reinterpret_cast<uint32_t*>(base + (s.acc_empty + 8 * kBufs - s.stages));
   s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
   return s;
 }
@@ -97,10 +96,9 @@ __device__ void load_loop(const Fp8SplitArgs& p, const SplitSmem& L, int n0, int
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0;
   int issued = 0;
-  bool ok = true;
+  if (p.stall) kb1 = kb0 + 1;
   for (int kb = kb0; kb < kb1; ++kb) {
-    ok = warp_wait(L.done + 8 * stage, phase ^ 1u, abort, p.status);
-    if (!ok) break;
+    if (!warp_wait(L.done + 8 * stage, phase ^ 1u, abort, p.status)) break;
     if (leader) {
       const uint32_t at = L.stages + stage * C::STAGE_BYTES, bar = L.full + 8 * stage;
       mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
@@ -114,7 +112,8 @@ __device__ void load_loop(const Fp8SplitArgs& p, const SplitSmem& L, int n0, int
       phase ^= 1u;
     }
   }
-  if (lane == 0 && (*abort || !ok)) {  // copies in flight land before the CTA exits
+  // The copies land before the warp leaves, also where another role gives up later.
+  if (lane == 0) {
     for (int b = max(issued - C::STAGES, 0); b < issued; ++b) {
       volatile int no_abort = 0;
       wait_bounded(L.full + 8 * (b % C::STAGES), (b / C::STAGES) & 1, &no_abort, nullptr, kDrainNs);
@@ -152,15 +151,12 @@ __device__ void mma_loop(const Fp8SplitArgs& p, const SplitSmem& L, uint32_t tme
       phase ^= 1u;
     }
   }
-  if (__any_sync(0xffffffffu, *abort) && b > 0) {  // every MMA issued finishes before TMEM is freed
-    if (leader) tc_commit(L.drain);
-    __syncwarp();
-    if (lane == 0) {
-      volatile int no_abort = 0;
-      wait_bounded(L.drain, 0, &no_abort, nullptr, kDrainNs);
-    }
-    __syncwarp();
+  // The products end before the warp leaves and TMEM is freed, also where another role gives up later.
+  if (lane == 0 && b > 0) {
+    volatile int no_abort = 0;
+    wait_bounded(L.done + 8 * ((b - 1) % C::STAGES), ((b - 1) / C::STAGES) & 1, &no_abort, nullptr, kDrainNs);
   }
+  __syncwarp();
 }
 
 template <bool F32>
@@ -290,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_split_kernel(const __grid_con
       mbar_init(L.done + 8 * s, 1);
     }
     for (int b = 0; b < kBufs; ++b) mbar_init(L.acc_empty + 8 * b, 4);
-    mbar_init(L.drain, 1);
     *L.abort_flag = 0;
     fence_mbar_init();
   }

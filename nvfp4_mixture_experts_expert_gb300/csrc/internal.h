@@ -265,6 +265,7 @@ struct Fp8SplitArgs {
   int* status;
   int64_t ld_out;
   int M, N, kbs;
+  int stall;  // failure-detection check: only a tile's first K-block is loaded
   int split;  // CTAs of a cluster, set by the launch
 };
 int fp8_split_nb(int64_t M);
@@ -281,6 +282,7 @@ struct Fp8GemmArgs {
   int* status;
   int64_t ld_out;
   int M, N, kbs;
+  int stall;           // failure-detection check: only a tile's first K-block is loaded
   int bn, split;       // columns of a tile and CTAs that share its K, set by fp8_gemm_plan
   int m_tiles, tiles;  // set by the launch
 };
@@ -306,6 +308,7 @@ struct FewArgs {
   float* y;               // [T * k][H]
   int64_t ld_x;
   int T, H, I, E, k, start;
+  int stall;  // failure-detection check: only a CTA's first tile is loaded
   float gate_limit, up_limit;
 };
 // Tensor maps of one product's weights (the box of an m16 tile, see moe_few.cu)

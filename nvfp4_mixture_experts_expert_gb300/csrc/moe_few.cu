@@ -451,30 +451,41 @@ __device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
+// The first W2 tiles of this CTA's share of the second launch, into L2.
+__device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
+  int u0, u1;
+  share_of(r->n_list, g.tiles, u0, u1);
+  if (!elect_one()) return;
+#pragma unroll 1
+  for (int u = u0; u < min(u1, u0 + kPrefetch); ++u) {
+    const Unit t = unit_at(u, g.tiles);
+#pragma unroll 1
+    for (int i = 0; i < g.R; ++i) {
+      const TileAt<1> at(g, r->expert[t.v], t.tile * g.R + i);
+      asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %1, %1, %3}];" ::"l"(
+                       reinterpret_cast<uint64_t>(&m.next_w)),
+                   "r"(0), "r"(at.line), "r"(at.block)
+                   : "memory");
+    }
+  }
+}
+
 template <int PHASE>
-__device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, const Ring& L, const Route* r, int u0,
-                          int u1) {
+__device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, const Phase& next, const Ring& L,
+                          const Route* r, int u0, int u1) {
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   const uint64_t policy = evict_first_policy();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   Unit t = unit_at(u0, g.tiles);
+  if (p.stall) u1 = min(u1, u0 + 1);
   for (int u = u0; u < u1; ++u, t.advance(1, g.tiles)) {
     bool ok = warp_wait_asleep(L.empty + 8 * stage, phase ^ 1u, L.abort, p.status);
     // Two tiles under way until the first lands: they keep HBM busy, and the
     // consumers' first tile does not share its rate with all of the ring's.
     if (ok && u - u0 >= kFirstCopies && u - u0 < g.stages)
       ok = warp_wait_asleep(L.full + 8 * (stage - kFirstCopies), 0, L.abort, p.status);
-    if (!ok) {
-      // copies in flight land before the CTA leaves its shared memory
-      for (int s = 0; s < g.stages; ++s)
-        if (lane == 0 && (issued >> s & 1u)) {
-          volatile int no_abort = 0;
-          wait_bounded(L.full + 8 * s, issued_parity >> s & 1u, &no_abort, nullptr, kDrainNs);
-        }
-      __syncwarp();
-      return;
-    }
+    if (!ok) break;
     const int e = r->expert[t.v];
     if (leader) {
       const uint32_t w = L.slots + stage * g.stage_bytes, bar = L.full + 8 * stage;
@@ -494,6 +505,15 @@ __device__ void copy_loop(const FewArgs& p, const FewMaps& m, const Phase& g, co
       phase ^= 1u;
     }
   }
+  if (PHASE == 0) prefetch_w2(m, next, r);
+  // The copies land before the warp leaves, also where another role gives up later.
+  if (lane == 0) {
+    volatile int no_abort = 0;
+#pragma unroll 1
+    for (int s = 0; s < g.stages; ++s)
+      if (issued >> s & 1u) wait_bounded(L.full + 8 * s, issued_parity >> s & 1u, &no_abort, nullptr, kDrainNs);
+  }
+  __syncwarp();
 }
 
 // The tile's scale lines, 16 bytes (four rows by four columns) a copy: per m16
@@ -530,25 +550,6 @@ __device__ void scale_loop(const FewArgs& p, const Phase& g, const Ring& L, cons
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// The first W2 tiles of this CTA's share of the second launch, into L2.
-__device__ void prefetch_w2(const FewMaps& m, const Phase& g, const Route* r) {
-  int u0, u1;
-  share_of(r->n_list, g.tiles, u0, u1);
-  if (!elect_one()) return;
-#pragma unroll 1
-  for (int u = u0; u < min(u1, u0 + kPrefetch); ++u) {
-    const Unit t = unit_at(u, g.tiles);
-#pragma unroll 1
-    for (int i = 0; i < g.R; ++i) {
-      const TileAt<1> at(g, r->expert[t.v], t.tile * g.R + i);
-      asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %1, %1, %3}];" ::"l"(
-                       reinterpret_cast<uint64_t>(&m.next_w)),
-                   "r"(0), "r"(at.line), "r"(at.block)
-                   : "memory");
-    }
-  }
 }
 
 // ------------------------------------------------------------------ consumers
@@ -985,8 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   } else {
     regs_dec<kRegsOther>();
     if (warp == kWarps) {
-      copy_loop<PHASE>(p, m, g, L, &route, u0, u1);
-      if (PHASE == 0) prefetch_w2(m, next, &route);
+      copy_loop<PHASE>(p, m, g, next, L, &route, u0, u1);
     } else if (warp == kWarps + 1) {
       scale_loop<PHASE>(p, g, L, &route, u0, u1);
     } else {
