@@ -783,17 +783,17 @@ __device__ void consume_loop(const FewArgs& p, const Phase& g, const Ring& L, co
     }
     // Two tiles at a time while the list entry lasts: waiting, handing over the
     // sums and coming back cost about half of what one tile's products take.
-    // Both have landed and buffers for their sums are free: six lanes ask.
+    // Both have landed and buffers for their sums are free (of one tile, each is asked twice).
     const int n = min(2, min(u1 - u, g.tiles - t.tile));
     const uint32_t stage2 = stage + 1 == (uint32_t)g.stages ? 0u : stage + 1, phase2 = stage2 ? phase : phase ^ 1u;
     const uint32_t buf2 = buf + 1 == kPartBufs ? 0u : buf + 1, buf_phase2 = buf2 ? buf_phase : buf_phase ^ 1u;
     {
-      const bool second = lane >= 3;
-      const uint32_t kind = second ? lane - 3 : lane, slot = second ? stage2 : stage;
-      const uint32_t bar = kind == 0 ? L.full + 8 * slot : kind == 1 ? L.scales + 8 * slot
-                                                                     : L.part_empty + 8 * (second ? buf2 : buf);
-      const uint32_t parity = kind < 2 ? (second ? phase2 : phase) : (second ? buf_phase2 : buf_phase);
-      if (!warp_wait_lanes(3 * n, bar, parity, L.abort, p.status)) return;
+      const uint32_t s2 = n == 2 ? stage2 : stage, ph2 = n == 2 ? phase2 : phase;
+      const uint32_t b2 = n == 2 ? buf2 : buf, bp2 = n == 2 ? buf_phase2 : buf_phase;
+      const uint32_t bars[6] = {L.full + 8 * stage, L.scales + 8 * stage,   L.full + 8 * s2,
+                                L.scales + 8 * s2,  L.part_empty + 8 * buf, L.part_empty + 8 * b2};
+      const uint32_t parities[6] = {phase, phase, ph2, ph2, buf_phase, bp2};
+      if (!warp_wait_every(bars, parities, L.abort, p.status)) return;
     }
     // both tiles' products side by side: each alone is a chain of waits
     float c[2][4] = {}, d[2][4] = {};

@@ -165,6 +165,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
       atomicExch(status, 6 /* NVFP4_ERR_DEVICE_TIMEOUT */);
       return false;
     }
+  __syncwarp();  // the test's acquire for the lanes that did not make it: a vote orders no memory
   return true;
 }
 
@@ -180,17 +181,17 @@ __device__ __forceinline__ bool warp_wait_asleep(uint32_t bar, uint32_t parity, 
   return true;
 }
 
-// Waits for `count` barriers at once: lane i < count tests its own.
-__device__ __forceinline__ bool warp_wait_lanes(uint32_t count, uint32_t bar, uint32_t parity, volatile int* abort,
-                                                int* status) {
+// Waits for N barriers at once.  Every lane tests them all, and so has its own
+// acquire of each: lane i testing barrier i alone, with a __syncwarp() behind the
+// vote for the other lanes, takes the few-token layer 76.4 us instead of 73.8 (8
+// tokens; 129.5 instead of 126.1 with 32).
+template <int N>
+__device__ __forceinline__ bool warp_wait_every(const uint32_t (&bar)[N], const uint32_t (&parity)[N],
+                                                volatile int* abort, int* status) {
   for (uint32_t n = 1;; ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p, q;\nsetp.lt.u32 q, %3, %4;\nsetp.eq.b32 p, 0, 0;\n"
-        "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(threadIdx.x & 31), "r"(count)
-        : "memory");
+    uint32_t ok = 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ok &= mbar_test_wait(bar[i], parity[i]);
     if (__all_sync(0xffffffffu, ok)) return true;
     if (n % 256 == 0 && __any_sync(0xffffffffu, n >= kTries || *abort)) {
       *abort = 1;
