@@ -14,6 +14,7 @@
 
 #include "../../include/nvfp4moe.h"
 #include "internal.h"
+#include "per_device.h"
 
 using namespace nvfp4;
 
@@ -41,7 +42,6 @@ struct DeviceInfo {
   bool ok = false;
 };
 
-constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 

@@ -504,21 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 
 template <int BN, bool F32, bool SPLIT>
 cudaError_t configure() {
-  static int configured = -1;
+  static PerDevice<char, cudaError_t> done;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (configured != dev) {
+  if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+  const char* none = nullptr;
+  return done.get(dev, &none, [](char&) {
     // setmaxnreg.inc waits for what the other warps give back: launch only with the allocation it is sized for
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN, F32, SPLIT>)) != cudaSuccess) return e;
+    if (const cudaError_t e = cudaFuncGetAttributes(&fa, fp8_gemm_kernel<BN, F32, SPLIT>)) return e;
     if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<BN, F32, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Cfg<BN>::SMEM);
-    if (e != cudaSuccess) return e;
-    configured = dev;
-  }
-  return cudaSuccess;
+    return cudaFuncSetAttribute(fp8_gemm_kernel<BN, F32, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Cfg<BN>::SMEM);
+  });
 }
 template <int BN, bool F32>
 cudaError_t launch(Fp8GemmArgs& p, int num_sms, cudaStream_t s) {
@@ -552,23 +549,23 @@ cudaError_t launch_out(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s) {
 // CTAs a tile against 10.7 with 64 and one; 100 x 512 x 4096 5.7 against 8.4; 256 x
 // 1000 x 1024, eight K-blocks, would lose: 5.3 against 4.3).
 cudaError_t fp8_gemm_plan(Fp8GemmArgs& p, int num_sms) {
-  static int configured = -1, clusters[kMaxSplit + 1];  // one CTA a SM in all forms
+  static PerDevice<Clusters, cudaError_t> fit;  // one CTA a SM in all forms
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (configured != dev) {
-    if ((e = configure<64, false, true>()) != cudaSuccess) return e;
-    e = max_clusters(fp8_gemm_kernel<64, false, true>, kThreads, Cfg<64>::SMEM, clusters);
-    if (e != cudaSuccess) return e;
-    configured = dev;
-  }
+  const Clusters* clusters = nullptr;
+  e = fit.get(dev, &clusters, [](Clusters& c) {
+    if (const cudaError_t e = configure<64, false, true>()) return e;
+    return max_clusters(fp8_gemm_kernel<64, false, true>, kThreads, Cfg<64>::SMEM, c);
+  });
+  if (e != cudaSuccess) return e;
   constexpr int kBns[3] = {256, 128, 64}, kNs[3] = {503, 279, 199}, kJoinNs[3] = {0, 3000, 2000};
   const int64_t mt = (p.M + kBM - 1) / kBM;
   int64_t least = INT64_MAX;
   for (int i = 0; i < 3; ++i) {
     const int64_t tiles = mt * ((p.N + kBns[i] - 1) / kBns[i]);
     for (int c = 1; c <= (kBns[i] < 256 ? kMaxSplit : 1) && c <= p.kbs; ++c) {
-      if (c > 1 && (tiles * c > num_sms || tiles > clusters[c])) continue;
+      if (c > 1 && (tiles * c > num_sms || tiles > clusters->most[c])) continue;
       const int64_t ns = (tiles * c + num_sms - 1) / num_sms * ((p.kbs + c - 1) / c) * kNs[i] + (c > 1 ? kJoinNs[i] : 0);
       if (ns < least) least = ns, p.bn = kBns[i], p.split = c;
     }

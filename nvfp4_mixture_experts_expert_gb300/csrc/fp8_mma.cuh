@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "per_device.h"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -53,8 +54,11 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t at) {
 constexpr int kMaxSplit = 8;  // portable cluster size
 
 // How many clusters of 1 to kMaxSplit CTAs the GPU holds at a time.
+struct Clusters {
+  int most[kMaxSplit + 1];
+};
 template <typename... KArgs>
-cudaError_t max_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int (&clusters)[kMaxSplit + 1]) {
+cudaError_t max_clusters(void (*kernel)(KArgs...), int threads, size_t smem, Clusters& clusters) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
@@ -66,7 +70,7 @@ cudaError_t max_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int
   for (int c = 1; c <= kMaxSplit; ++c) {
     cfg.gridDim = dim3(c);
     at[0].val.clusterDim.x = c;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[c], kernel, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters.most[c], kernel, &cfg);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -321,20 +321,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_split_kernel(const __grid_con
 template <int NB, bool F32>
 cudaError_t launch(Fp8SplitArgs& p, int num_sms, cudaStream_t s) {
   constexpr size_t SMEM = SplitCfg<NB>::SMEM;
-  static int configured = -1, clusters[kMaxSplit + 1];
+  static PerDevice<Clusters, cudaError_t> fit;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (configured != dev) {
-    e = cudaFuncSetAttribute(fp8_split_kernel<NB, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
-    if (e != cudaSuccess) return e;
-    if ((e = max_clusters(fp8_split_kernel<NB, F32>, kThreads, SMEM, clusters)) != cudaSuccess) return e;
-    configured = dev;
-  }
+  const Clusters* clusters = nullptr;
+  e = fit.get(dev, &clusters, [](Clusters& c) {
+    if (const cudaError_t e = cudaFuncSetAttribute(fp8_split_kernel<NB, F32>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM))
+      return e;
+    return max_clusters(fp8_split_kernel<NB, F32>, kThreads, SMEM, c);
+  });
+  if (e != cudaSuccess) return e;
   const int tiles = (p.N + kTileN - 1) / kTileN;
   p.split = 1;  // the most CTAs that run at once, one a SM
   for (int c = 2; c <= kMaxSplit && c <= p.kbs; ++c)
-    if (tiles * c <= num_sms && tiles <= clusters[c]) p.split = c;
+    if (tiles * c <= num_sms && tiles <= clusters->most[c]) p.split = c;
   return launch_split<const Fp8SplitArgs>(fp8_split_kernel<NB, F32>, tiles * p.split, kThreads, SMEM, p.split, s, p);
 }
 

@@ -76,6 +76,7 @@
 
 #include "internal.h"
 #include "nvfp4_format.cuh"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "route_key.cuh"
 
@@ -1017,23 +1018,22 @@ Phase phase_of(int K, int m16_tiles, int blocks, size_t smem, int64_t entries, i
 
 template <int PHASE, int SPW>
 cudaError_t launch(const FewArgs& a, const FewMaps& m, int num_sms, cudaStream_t s) {
-  static int configured = -1;
-  static size_t dynamic = 0;
+  static PerDevice<size_t, cudaError_t> memory;  // dynamic shared memory of a CTA
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (configured != dev) {
+  const size_t* dynamic = nullptr;
+  e = memory.get(dev, &dynamic, [](size_t& bytes) {
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, few_kernel<PHASE, SPW>)) != cudaSuccess) return e;
+    if (const cudaError_t e = cudaFuncGetAttributes(&fa, few_kernel<PHASE, SPW>)) return e;
     // setmaxnreg.inc waits for what the other warps give back: launch only with the allocation it is sized for
     if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    dynamic = 232448 - 1024 - fa.sharedSizeBytes;
-    e = cudaFuncSetAttribute(few_kernel<PHASE, SPW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dynamic);
-    if (e != cudaSuccess) return e;
-    configured = dev;
-  }
-  const Phase first = phase_of(a.H, a.I / 8, 2 * a.I / 128, dynamic, a.T * a.k, num_sms);
-  const Phase second = phase_of(a.I, a.H / 16, a.H / 128, dynamic, a.T * a.k, num_sms);
+    bytes = 232448 - 1024 - fa.sharedSizeBytes;
+    return cudaFuncSetAttribute(few_kernel<PHASE, SPW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
+  if (e != cudaSuccess) return e;
+  const Phase first = phase_of(a.H, a.I / 8, 2 * a.I / 128, *dynamic, a.T * a.k, num_sms);
+  const Phase second = phase_of(a.I, a.H / 16, a.H / 128, *dynamic, a.T * a.k, num_sms);
   const Phase& g = PHASE == 0 ? first : second;
   const size_t smem = 1024 + (size_t)g.stages * g.stage_bytes + kPartBufs * kWarps * 512;
   return launch_kernel(few_kernel<PHASE, SPW>, dim3(num_sms), dim3(kThreads), smem, s, true, m, a, g, second);

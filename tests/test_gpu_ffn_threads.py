@@ -60,3 +60,39 @@ def test_two_threads_on_two_streams():
     for t in threads:
         t.join()
     assert not failures, failures[:5]
+
+
+FIRST_CALLS = """
+import sys, threading
+sys.path[:0] = ["tests", "."]
+import torch
+import test_gpu_ffn_threads as T
+calls = [T._calls(seed) for seed in (1, 1)]
+torch.cuda.synchronize()
+out, gate = [None, None], threading.Barrier(2)
+def work(i):
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out[i] = []
+        for call in calls[i]:
+            gate.wait()
+            out[i].append(call())
+        torch.cuda.current_stream().synchronize()
+threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+for a, b in zip(*out):
+    for s, t in zip(a, b):
+        assert torch.equal(s.view(torch.uint8), t.view(torch.uint8))
+print("equal")
+"""
+
+
+def test_first_calls_of_a_process_from_two_threads():
+    """What a kernel's first launch works out (attributes, clusters that fit) is complete for the thread beside it."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(2):
+        r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and r.stdout.split() == ["equal"], r.stdout + r.stderr
