@@ -303,6 +303,7 @@ struct FewArgs {
   uint16_t* out;          // bf16 [T][H]
   int* status;            // workspace byte 0
   void* table;            // [kFewTableBytes] routing tables between the launches
+  uint64_t call;          // the call's number, set by the launch
   int32_t* ids;           // [kFewAssignments] local expert of an assignment, -1: not computed
   float* h;               // [T * k][I]
   float* y;               // [T * k][H]

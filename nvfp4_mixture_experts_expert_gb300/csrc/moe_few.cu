@@ -74,6 +74,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "nvfp4_format.cuh"
 #include "per_device.h"
@@ -235,15 +237,16 @@ __device__ void route_all(const FewArgs& p, Route* r) {
 }
 
 // The first launch's first CTA leaves the tables for the second, whose CTAs then
-// need not route again: complete once `ready` holds kRouteReady, until the sum
-// takes it back.  The second launch starts after that CTA has triggered it; a CTA
-// that finds the tables missing all the same routes for itself.
+// need not route again: complete once `ready` holds the call's number, until the
+// sum takes it back.  The second launch starts after that CTA has triggered it; a
+// CTA that finds the tables missing all the same routes for itself.  Numbers are a
+// process's own, so what another call left, one whose later launches failed among
+// them, is not taken for this call's.
 struct alignas(16) RouteTable {
   uint64_t ready, pad;
   Route route;
 };
 static_assert(sizeof(RouteTable) <= kFewTableBytes, "the workspace's share");
-constexpr uint64_t kRouteReady = 0x6f75746564214d4bull;
 constexpr int kRouteWords = sizeof(Route) / 16;
 
 __device__ __forceinline__ void leave_route(const FewArgs& p, const Route& r) {
@@ -252,16 +255,16 @@ __device__ __forceinline__ void leave_route(const FewArgs& p, const Route& r) {
     reinterpret_cast<uint4*>(&t->route)[i] = reinterpret_cast<const uint4*>(&r)[i];
   __syncthreads();
   if (threadIdx.x == 0)
-    asm volatile("fence.acq_rel.gpu;\nst.release.gpu.global.b64 [%0], %1;" ::"l"(&t->ready), "l"(kRouteReady) : "memory");
+    asm volatile("fence.acq_rel.gpu;\nst.release.gpu.global.b64 [%0], %1;" ::"l"(&t->ready), "l"(p.call) : "memory");
 }
 __device__ __forceinline__ bool take_route(const FewArgs& p, Route* r) {
   const RouteTable* t = static_cast<const RouteTable*>(p.table);
   uint64_t ready;
   asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(ready) : "l"(&t->ready) : "memory");
-  if (ready == kRouteReady)
+  if (ready == p.call)
     for (int i = threadIdx.x; i < kRouteWords; i += kThreads)
       reinterpret_cast<uint4*>(r)[i] = __ldcg(reinterpret_cast<const uint4*>(&t->route) + i);
-  return __syncthreads_and(ready == kRouteReady);
+  return __syncthreads_and(ready == p.call);
 }
 
 // Eight E2M1 codes (one word) times a block scale: four f16 pairs, in order.
@@ -1046,7 +1049,10 @@ cudaError_t launch_phase(const FewArgs& a, const FewMaps& m, int K, int num_sms,
 
 }  // namespace
 
-cudaError_t launch_moe_few(const FewArgs& a, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s) {
+cudaError_t launch_moe_few(const FewArgs& args, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s) {
+  static std::atomic<uint64_t> calls{0x6f75746564214d4bull};  // nothing that memory is likely to hold
+  FewArgs a = args;
+  a.call = calls.fetch_add(1, std::memory_order_relaxed);
   FewMaps m = w13;
   m.next_w = w2.w;
   cudaError_t e = launch_phase<0>(a, m, a.H, num_sms, s);

@@ -61,3 +61,21 @@ def test_gates_far_below_zero_keep_their_silu():
     rel = 1.1 * gate.abs() * ((H / 16 * 2 + 40) * R.U32) + 16 * R.U32 + 2.0 ** -11 + (I / 16 * 2 + 40) * R.U32
     tol = (h.abs() * rel) @ w2.abs().T
     assert ((out.double() - ref).abs() <= tol + (ref.abs() + tol) * R.BF16).all()
+
+
+def test_routing_tables_of_another_call_are_not_taken():
+    """A ready word that an earlier call's failed launches left, in the middle of its tables (the layout: status 256
+    bytes, ids 1024, then the word): the next call computes with its own routes and takes the word back."""
+    import torch
+    T, H, I, E, k = 12, 512, 256, 24, 4
+    layer, w, x, logits = _layer(T, H, I, E, k)
+    others = [torch.roll(logits, i, 1) for i in range(4)]
+    want = []
+    for lg in others:
+        layer.workspace.fill_(0xFF)
+        want.append(layer(x, lg, w).clone())
+    word = layer.workspace[1280:1288].view(torch.int64)
+    for turn in range(8):
+        word.fill_(0x6f75746564214d4b + turn)
+        assert torch.equal(layer(x, others[turn % 4], w), want[turn % 4])
+        assert word.item() == 0
