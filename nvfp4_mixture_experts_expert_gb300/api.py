@@ -215,7 +215,9 @@ def add_rms_norm_fp8(x, residual, weight, eps=1e-6, normed=True, quantized=True,
     Returns (q, scales, y, s): float8_e4m3fn [T, H] and f32 [T, ceil(H/128)]
     (None with quantized=False), bf16 y (None with normed=False), bf16 s (None
     without a residual).  residual_out: where s goes; x or residual for in place.
-    Outputs of up to 16 MB together are parts of one allocation."""
+    q, scales and y of up to 16 MB together are parts of one allocation: it lives
+    as long as any of them, is saved or shared as a whole with any of them, and none
+    of them can be resized in place.  s, which the next layer needs, has its own."""
     return C.add_rms_norm_fp8(x, residual, weight, eps, normed, quantized, residual_out, _handle(stream))
 
 

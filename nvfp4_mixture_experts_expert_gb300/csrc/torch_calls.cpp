@@ -58,13 +58,13 @@ struct Where {
     }
   }
   // From the caching allocator, on this stream.
-  c10::Storage storage(int64_t bytes) const {
+  c10::Storage storage(int64_t bytes, bool resizable) const {
     c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
     return c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
-                                                              from->allocate(bytes), from, /*resizable=*/true));
+                                                              from->allocate(bytes), from, resizable));
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) const {
-    return part(storage(c10::multiply_integers(shape) * (int64_t)c10::elementSize(dtype)), 0, shape, dtype);
+    return part(storage(c10::multiply_integers(shape) * (int64_t)c10::elementSize(dtype), true), 0, shape, dtype);
   }
   // A contiguous tensor `offset` bytes into a storage.
   static at::Tensor part(c10::Storage s, int64_t offset, at::IntArrayRef shape, at::ScalarType dtype) {
@@ -76,14 +76,16 @@ struct Where {
   }
 };
 
-// The outputs of one call, parts of one allocation where they are small: up to
-// about kShared bytes the kernel takes no longer than the host does with an
-// allocation for each (5.0 us with four, 3.7 with one for all).
+// Outputs of one call that live about equally long, parts of one allocation where
+// they are small: up to about kShared bytes the kernel takes no longer than the
+// host does with an allocation for each (a call with four outputs 5.3 us with an
+// allocation each, 4.5 with one for three of them).  The shared
+// storage cannot be resized, which would let one part grow into the next.
 class Outputs {
  public:
   static constexpr int64_t kShared = 16 << 20, kAlign = 256;
   Outputs(const Where& at, int64_t bytes, int count) : at_(at) {
-    if (count > 1 && bytes + count * kAlign <= kShared) pool_ = at.storage(bytes + count * kAlign);
+    if (count > 1 && bytes + count * kAlign <= kShared) pool_ = at.storage(bytes + count * kAlign, false);
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) {
     if (!pool_) return at_.empty(shape, dtype);
@@ -150,10 +152,9 @@ PyObject* add_rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const bool sum = a[1] != Py_None && !s;
   const int64_t cols = (H + 127) / 128;
-  Outputs out_of(at, T * (H * (2 * sum + 2 * normed + quantized) + 4 * cols * quantized),
-                 sum + normed + 2 * quantized);
+  Outputs out_of(at, T * (H * (2 * normed + quantized) + 4 * cols * quantized), normed + 2 * quantized);
   if (sum) {
-    s = out_of.empty({T, H}, at::kBFloat16);
+    s = at.empty({T, H}, at::kBFloat16);
     ld_o = H;
   }
   if (normed) y = out_of.empty({T, H}, at::kBFloat16);
