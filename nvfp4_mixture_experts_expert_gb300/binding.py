@@ -122,7 +122,7 @@ _moe_set_swap_l2 = _sig("nvfp4_moe_set_swap_l2", c_int, [c_int, ctypes.POINTER(c
 
 def _p(t):
     """Device address of a torch tensor / int / None."""
-    return t if t is None or t.__class__ is int else t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 _raw_stream = _device = None
