@@ -42,6 +42,20 @@ void whole(const at::Tensor& t, const char* name, at::ScalarType dtype, at::IntA
                     " ", t.sizes(), " with strides ", t.strides(), " on ", t.device());
 }
 
+// A flag, and a stream's handle (none: the current stream), as Python has them;
+// what is neither leaves its Python exception standing.
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v;
+}
+std::optional<cudaStream_t> handle(PyObject* o) {
+  if (o == Py_None) return std::nullopt;
+  const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+  if (PyErr_Occurred()) throw python_error();
+  return reinterpret_cast<cudaStream_t>(v);
+}
+
 // The device of a call, and its stream: the current one, or the given handle,
 // in whose pool the outputs are then allocated.
 struct Where {
@@ -49,11 +63,11 @@ struct Where {
   c10::cuda::OptionalCUDAStreamGuard guard;
   at::Device dev;
   cudaStream_t stream;
-  Where(const at::Tensor& t, PyObject* s) : device(t.device()), dev(t.device()) {
-    if (s == Py_None) {
+  Where(const at::Tensor& t, std::optional<cudaStream_t> s) : device(t.device()), dev(t.device()) {
+    if (!s) {
       stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     } else {
-      stream = reinterpret_cast<cudaStream_t>(PyLong_AsUnsignedLongLong(s));
+      stream = *s;
       guard.reset_stream(c10::cuda::getStreamFromExternal(stream, dev.index()));
     }
   }
@@ -130,10 +144,11 @@ PyObject* add_rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[2], "weight");
   const double eps = PyFloat_AsDouble(a[3]);
   if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-  const bool normed = PyObject_IsTrue(a[4]), quantized = PyObject_IsTrue(a[5]);
+  const bool normed = truth(a[4]), quantized = truth(a[5]);
+  const std::optional<cudaStream_t> stream = handle(a[7]);
   need_cuda(x, "x");
   TORCH_CHECK_VALUE(x.dim() == 2, "x must have two dimensions, not ", x.dim());
-  const Where at(x, a[7]);
+  const Where at(x, stream);
   const int64_t T = x.size(0), H = x.size(1);
   const int64_t ld_x = rows(x, "x", at::kBFloat16, T, H, at.dev);
   const bool f32 = w.scalar_type() == at::kFloat;
@@ -181,17 +196,18 @@ PyObject* add_rms_norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* fp8_linear(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 7)) return nullptr;
+  const std::optional<cudaStream_t> stream = handle(p[6]);
+  const bool f32 = truth(p[4]);
   const at::Tensor &a = tensor(p[0], "a"), &sa = tensor(p[1], "a_scale"), &w = tensor(p[2], "w"),
                    &sw = tensor(p[3], "w_scale");
   need_cuda(a, "a");
   TORCH_CHECK_VALUE(a.dim() == 2 && w.dim() == 2, "a and w must have two dimensions, not ", a.dim(), " and ", w.dim());
-  const Where at(a, p[6]);
+  const Where at(a, stream);
   const int64_t M = a.size(0), K = a.size(1), N = w.size(0), kb = (K + 127) / 128;
   const int64_t ld_a = rows(a, "a", at::kFloat8_e4m3fn, M, K, at.dev);
   whole(w, "w", at::kFloat8_e4m3fn, {N, K}, at.dev);
   whole(sa, "a_scale", at::kFloat, {M, kb}, at.dev);
   whole(sw, "w_scale", at::kFloat, {(N + 127) / 128, kb}, at.dev);
-  const bool f32 = PyObject_IsTrue(p[4]);
   const at::ScalarType dtype = f32 ? at::kFloat : at::kBFloat16;
   int64_t ld_out = N;
   at::Tensor out;
@@ -221,9 +237,10 @@ PyObject* moe_few_tokens(PyObject*, PyObject* const* p, Py_ssize_t n) {
   TORCH_CHECK_VALUE(start >= INT32_MIN && start <= INT32_MAX, "experts_start must be a 32-bit number");
   const double gl = PyFloat_AsDouble(p[7]), ul = PyFloat_AsDouble(p[8]);
   if (PyErr_Occurred()) return nullptr;
+  const std::optional<cudaStream_t> stream = handle(p[11]);
   need_cuda(x, "hidden");
   TORCH_CHECK_VALUE(x.dim() == 2, "hidden must have two dimensions, not ", x.dim());
-  const Where at(x, p[11]);
+  const Where at(x, stream);
   const int64_t T = x.size(0);
   const int64_t ld = rows(x, "hidden", at::kBFloat16, T, H, at.dev);
   TORCH_CHECK_VALUE(T <= most, T, " tokens; this layer was made for ", most);
