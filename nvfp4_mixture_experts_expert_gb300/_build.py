@@ -4,13 +4,15 @@ Each .cu file under csrc/ is compiled in parallel to an object with
 ``-gencode arch=compute_103a,code=sm_103a``, then linked into one shared
 library (static CUDA runtime) next to this file.  csrc/torch_calls.cpp, the
 host side of the short operators on torch's tensors, becomes an extension
-module linked to that library.  Rebuilds only when a source or header is newer
-than the two.
+module linked to that library; where torch or its headers are missing, the
+library is built alone.  Each is rebuilt when a source or header of its own is
+newer than it, the extension also when torch or Python is another one.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -24,6 +26,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
 EXT_SRC = os.path.join(CSRC, "torch_calls.cpp")
 EXT = os.path.join(PKG, "_torch_calls.so")
+EXT_FOR = os.path.join(BUILD, "torch_calls.for")  # the torch and Python that EXT was built for
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -38,16 +41,41 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + [EXT_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+
+
+def lib_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  _headers())
+
+
+def torch_dir():
+    """Where torch lies, None without torch or its headers (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    where = os.path.dirname(spec.origin) if spec and spec.origin else None
+    return where if where and os.path.exists(os.path.join(where, "include", "ATen", "ATen.h")) else None
+
+
+def _ext_for(where) -> str:
+    with open(os.path.join(where, "version.py")) as f:
+        return f"{where}\n{sys.version}\n{f.read()}"
+
+
+def ext_up_to_date(where) -> bool:
+    if not _newer(EXT, [EXT_SRC] + _headers()) or not os.path.exists(EXT_FOR):
+        return False
+    with open(EXT_FOR) as f:
+        return f.read() == _ext_for(where)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    where = torch_dir()
+    return lib_up_to_date() and (where is None or ext_up_to_date(where))
 
 
 def _compile(src, extra):
@@ -86,28 +114,36 @@ def _link_ext(obj):
     os.replace(tmp, EXT)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libnvfp4moe.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    extra = list(extra_flags)
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
-        ext = ex.submit(_compile_ext)
-        results = list(ex.map(lambda s: _compile(s, extra), sources()))
-        ext_obj = ext.result()
-    objs = [o for o, _ in results]
-    if verbose:
-        for _, log in results:
-            if log.strip():
-                print(log, file=sys.stderr)
+def _link_lib(objs):
     tmp = LIB + ".tmp"
     cmd = [nvcc(), ARCH, "-shared", "-Xlinker", "-soname=libnvfp4moe.so", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_ext(ext_obj)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compile and link libnvfp4moe.so, and torch's extension where there is torch; returns the library's path."""
+    where = torch_dir()
+    lib = force or not lib_up_to_date()
+    ext = where is not None and (force or not ext_up_to_date(where))
+    if not lib and not ext:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
+        ext_obj = ex.submit(_compile_ext) if ext else None
+        if lib:
+            results = list(ex.map(lambda s: _compile(s, list(extra_flags)), sources()))
+            if verbose:
+                for _, log in results:
+                    if log.strip():
+                        print(log, file=sys.stderr)
+            _link_lib([o for o, _ in results])
+        if ext:
+            _link_ext(ext_obj.result())
+            with open(EXT_FOR, "w") as f:
+                f.write(_ext_for(where))
     return LIB
 
 
