@@ -8,10 +8,20 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _torch_calls as C
 from . import binding as B
 
-C.set_error(B.Nvfp4Error)
+try:
+    from . import _torch_calls as C
+    C.set_error(B.Nvfp4Error)
+except ImportError as e:  # the rest of this module needs the library alone
+    class _Missing:
+        def __init__(self, why):
+            self._why = str(why)
+
+        def __getattr__(self, name):
+            raise ImportError(f"{name} needs the extension _torch_calls.so, built with torch's headers by "
+                              f"`python -c 'import __graft_entry__ as g; g.build()'` ({self._why})")
+    C = _Missing(e)
 
 
 def _round_up(x, m):

@@ -82,3 +82,29 @@ def test_torch_is_found_without_importing_it():
     import torch
     from nvfp4_mixture_experts_expert_gb300 import _build as b
     assert b.torch_dir() == os.path.dirname(torch.__file__)
+
+
+def test_without_the_extension_the_older_calls_stay_and_its_own_fail_loudly(tmp_path):
+    import shutil
+    import subprocess
+    import sys
+    pytest.importorskip("torch")
+    from nvfp4_mixture_experts_expert_gb300 import _build as b
+    b.build()
+    shutil.copytree(b.PKG, tmp_path / "nvfp4_mixture_experts_expert_gb300",
+                    ignore=shutil.ignore_patterns("_torch_calls.so", "_build", "__pycache__", "csrc"))
+    code = """
+from nvfp4_mixture_experts_expert_gb300 import api
+assert callable(api.MoEForward) and callable(api.quantize_moe_weights)
+for call in (lambda: api.add_rms_norm_fp8(None, None, None), lambda: api.fp8_linear(None, None, None, None)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_torch_calls" in str(e)
+    else:
+        raise SystemExit("no ImportError")
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, env={**os.environ, "PYTHONPATH": str(tmp_path)},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["fine"], r.stdout + r.stderr
