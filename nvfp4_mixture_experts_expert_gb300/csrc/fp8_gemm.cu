@@ -22,9 +22,10 @@
 //   warps 4-11  epilogue: a TMEM lane quarter and half of the columns each
 // Every wait is bounded and reports in the library's status word.
 //
-// Measured (8192 x 4096 x 4096, bf16 out): 109 us in a row of launches, 2.5 PFLOP/s,
-// 0.66 of twice the measured bf16 rate (117 us over seconds, under the power
-// cap).  A K-block of a 128 x 256 tile takes ~900 cycles where its MMAs take 512:
+// Measured (8192 x 4096 x 4096, bf16 out): 115 to 118 us in a row of calls over
+// changing inputs, 2.3 to 2.4 PFLOP/s, 0.61 of twice the measured bf16 rate (the
+// power cap counts: 109 us in short runs, the figure that those below stand
+// against).  A K-block of a 128 x 256 tile takes ~900 cycles where its MMAs take 512:
 // the issuers wait for accumulators, of which TMEM holds two, and an accumulator's
 // way round (MMA, commit, the epilogue's wait of ~120 cycles and read of ~400,
 // arrival, issue ~200) is 1,700.  Built and not faster: CTA pairs with 256 x 256
@@ -543,7 +544,7 @@ cudaError_t launch_out(Fp8GemmArgs& p, bool f32, int num_sms, cudaStream_t s) {
 // The plan whose K-blocks take least time: columns of a tile, by its rounds of
 // tiles over the SMs, and where there is one round with SMs to spare, CTAs that
 // share a tile's K.  A K-block of a tile measured 503, 279 and 199 ns at 256, 128
-// and 64 columns (8192 x 4096 x 4096: 113, 125 and 172 us), so 64 pays when 256
+// and 64 columns (8192 x 4096 x 4096, at the time: 113, 125 and 172 us), so 64 pays when 256
 // leaves most SMs without a tile (128 x 4096 x 4096: 8.5 against 16.2 us), and the
 // join of a split K 3 and 2 us (300 x 1000 x 3600: 8.4 us with 128 columns and five
 // CTAs a tile against 10.7 with 64 and one; 100 x 512 x 4096 5.7 against 8.4; 256 x

@@ -56,10 +56,10 @@
 // brought into L2, so HBM idles little between the two.
 //
 // Bound: reading the chosen experts' weights, at 32 tokens (48 experts of H 4096,
-// I 2048, top 6: 680 MB) 100 us at the rate of a copy; the layer takes 127, of
+// I 2048, top 6: 680 MB) 100 us at the rate of a copy; the layer takes 125, of
 // which the first launch's stream runs at 6.5 TB/s.  The rest is what comes
 // before a launch's first tile (routing, activations, the ring's first copies),
-// the way from one launch to the next and the sum: ~18 us of one token's 30,
+// the way from one launch to the next and the sum: ~17 us of one token's 29,
 // whose weights take 12.5.  Measured beside what was kept, at the time (8 / 32
 // tokens, us in a row of calls): sixteen consumer warps 85 / 161 where eight took
 // 83 / 156; weights not marked for early eviction 90 / 165 instead of 83 / 156
@@ -1042,6 +1042,10 @@ cudaError_t launch(const FewArgs& a, const FewMaps& m, int num_sms, cudaStream_t
   return launch_kernel(few_kernel<PHASE, SPW>, dim3(num_sms), dim3(kThreads), smem, s, true, m, a, g, second);
 }
 
+// Above K = 4096 a warp holds up to eight slabs (W2's kernel then spills 436 bytes)
+// and the ring two or three tiles, which do not keep HBM busy: H 7168, I 2048, top
+// 8 of 16 takes 58.8 us for one token and 101 for eight, of 29.2 and 58.1 at the
+// rate of a copy.
 template <int PHASE>
 cudaError_t launch_phase(const FewArgs& a, const FewMaps& m, int K, int num_sms, cudaStream_t s) {
   return K > 4096 ? launch<PHASE, 8>(a, m, num_sms, s) : launch<PHASE, 4>(a, m, num_sms, s);

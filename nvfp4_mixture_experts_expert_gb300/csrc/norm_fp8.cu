@@ -11,13 +11,14 @@
 // of 0 without eps.
 //
 // Bound: HBM.  A row is read once and its outputs written once, 9 bytes an
-// element with every output.  What made the difference (8192 x 4096, 302 MB,
-// 44.5 us at the 6.79 TB/s of a copy): the norm weight is loaded beside x and
-// the residual instead of behind the row's sum (53.7 -> 49 us: a block's loads
-// are one trip to memory, not two), and launches are chained (pdl_wait at the
-// start; the blocks of the next kernel take a SM's place as this one's leave
-// it): 45.1 us in a row of calls, 1 x 4096 2.1 instead of 4.2 us, 1001 x 3584
-// with FP32 weights 5.1 instead of 8.3.  Tried and dropped: blocks that loop
+// element with every output.  8192 x 4096 (302 MB, 44.5 us at the 6.79 TB/s of a
+// copy) takes 45.0 us in a graph of calls, 1 x 4096 2.1, 1001 x 3584 with FP32
+// weights 6.5, 2048 x 7168 20.7 (132 MB: 19.5).  What made the difference, at the
+// time: the norm weight is loaded beside x and the residual instead of behind the
+// row's sum (53.7 -> 49 us: a block's loads are one trip to memory, not two), and
+// launches are chained (pdl_wait at the start; the blocks of the next kernel take
+// a SM's place as this one's leave it: 49 -> 45.1, 1 x 4096 4.2 -> 2.1, 1001 x
+// 3584 8.3 -> 5.1 before the codes' quotients).  Tried and dropped: blocks that loop
 // over rows with the next row's loads in flight (56 us: fewer threads a SM),
 // one vector a thread (50 us), streaming cache hints (50 us).
 #include <cuda_runtime.h>
@@ -162,7 +163,11 @@ cudaError_t launch_add_rmsnorm_fp8(const NormArgs& a, cudaStream_t s) {
     return launch_kernel(a.weight_f32 ? f32 : bf16, grid, block, 0, s, true, a);
   };
   // Two vectors a thread up to H = 4096, in the most blocks a SM whose
-  // registers do not spill; four above: 1024 threads reach H = 32768.
+  // registers do not spill; four above, where two are slower (2048 x 7168 25.6 us
+  // instead of 20.7, 1024 x 16384 33.9 instead of 33.8): 1024 threads reach H =
+  // 32768, though they spill a little (512 x 32768 33.6 us, with eight vectors in
+  // 512 threads 34.7).  Rows this long leave a SM one or two blocks, whose loads
+  // nothing overlaps with stores: 1.5 times the floor of 22.3 us.
   if (nvec <= 512) return go(add_rmsnorm_fp8_kernel<2, 256, 5, false>, add_rmsnorm_fp8_kernel<2, 256, 4, true>, 2);
   if (nvec <= 2048) return go(add_rmsnorm_fp8_kernel<4, 512, 1, false>, add_rmsnorm_fp8_kernel<4, 512, 1, true>, 4);
   return go(add_rmsnorm_fp8_kernel<4, 1024, 1, false>, add_rmsnorm_fp8_kernel<4, 1024, 1, true>, 4);
