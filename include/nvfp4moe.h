@@ -580,6 +580,130 @@ int nvfp4_moe_few_tokens_routed(const void* hidden, int64_t ld_hidden, const int
                                 const void* w2, const void* w2_sf, const float* w2_gs, float gate_limit,
                                 float up_limit, void* workspace, size_t workspace_bytes, void* out, void* stream);
 
+/* Element types and activations of the calls below. */
+enum { NVFP4_BF16 = 0, NVFP4_F16 = 1, NVFP4_F32 = 2 };
+enum {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_RELU = 1,
+  NVFP4_ACT_SILU = 2,       /* z * sigmoid(z) */
+  NVFP4_ACT_GELU = 3,       /* z * (1 + erf(z / sqrt 2)) / 2 */
+  NVFP4_ACT_GELU_TANH = 4,  /* z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2 */
+  NVFP4_ACT_SWIGLU = 5      /* silu(min(g, gate_limit)) * clamp(u, -up_limit, up_limit) */
+};
+
+/*
+ * nvfp4_sort_tokens -- rows of tokens copied into the order of the experts, as the
+ * MoE forward orders its slots, for products outside of it (nvfp4_expert_linear,
+ * nvfp4_quantize and nvfp4_grouped_gemm).
+ *
+ * Assignment f = t * top_k + j of token t belongs to expert topk_ids[t][j] -
+ * experts_start where that lies in [0, E), else to none (an expert held elsewhere).
+ * Rows are ordered by expert, then by f; an expert's first row is a multiple of
+ * `align`, the rows between the experts (pad rows) are zeros.  An expert that a
+ * token names twice gets two rows.
+ *   x         device [T][H] of `type` (NVFP4_BF16, _F16, _F32), row stride ld_x
+ *   topk_ids  device i32 [T][top_k], any values
+ *   rows      device [capacity][H] of `type`, row stride ld_rows, or NULL: the order
+ *             alone (x is not used then).  Rows behind the last expert's are not written.
+ *   offsets   device i32 [E + 1]: first row of each expert, the number of rows
+ *   counts    device i32 [E]: rows of each expert without pad rows
+ *   source    device i32 [capacity]: a row's assignment f, -1 for all other rows
+ *   inverse   device i32 [T][top_k]: an assignment's row, -1 where it has none
+ * capacity >= nvfp4_sort_tokens_capacity(T, E, top_k, align), which is T * top_k
+ * with align 1 (0 for sizes out of range).  T >= 0, 1 <= E <= 256, 1 <= top_k <=
+ * 32, align a power of two up to 128, capacity < 2^31; H times the type's size and
+ * the row strides in bytes multiples of 16.  x and rows 16-byte aligned, tables 4.
+ * Outputs overlap no input.  The order does not depend on timing.
+ */
+int64_t nvfp4_sort_tokens_capacity(int64_t T, int E, int top_k, int align);
+int nvfp4_sort_tokens(const void* x, int64_t ld_x, int type, const int32_t* topk_ids, int32_t experts_start, int64_t T,
+                      int64_t H, int E, int top_k, int align, int64_t capacity, void* rows, int64_t ld_rows,
+                      int32_t* offsets, int32_t* counts, int32_t* source, int32_t* inverse, void* stream);
+
+/* nvfp4_sort_tokens_grad -- dx[t] = sum over j of drows[inverse[t][j]] (FP32, in
+ * the order of j, rounded once); a token without rows gets zeros.  drows [..][H]
+ * and dx [T][H] of `type`; sizes, strides and alignment as nvfp4_sort_tokens. */
+int nvfp4_sort_tokens_grad(const void* drows, int64_t ld_drows, int type, const int32_t* inverse, int64_t T, int64_t H,
+                           int top_k, void* dx, int64_t ld_dx, void* stream);
+
+/*
+ * nvfp4_combine_tokens -- the experts' rows back to their tokens, weighted:
+ *   out[t] = residual[t] + sum over j of weights[t][j] * rows[inverse[t][j]]
+ * (FP32, in the order of j, rounded once; assignments without a row are left out).
+ *   rows [..][H], residual [T][H] (or NULL), out [T][H] of `type`; weights f32
+ *   [T][top_k].  out may be residual itself (same stride).
+ * nvfp4_combine_tokens_grad:
+ *   drows[inverse[t][j]] = weights[t][j] * dout[t]   (rounded once)
+ *   dweights[t][j] = dout[t] . rows[inverse[t][j]]   (FP32; 0 without a row)
+ * Pad rows of drows are zeros, rows behind the last are not written.  offsets,
+ * counts, E and align as nvfp4_sort_tokens gave and got them.  The gradient of
+ * residual is dout.  Sizes, strides and alignment as nvfp4_sort_tokens.
+ */
+int nvfp4_combine_tokens(const void* rows, int64_t ld_rows, int type, const float* weights, const int32_t* inverse,
+                         const void* residual, int64_t ld_residual, int64_t T, int64_t H, int top_k, void* out,
+                         int64_t ld_out, void* stream);
+int nvfp4_combine_tokens_grad(const void* dout, int64_t ld_dout, const void* rows, int64_t ld_rows, int type,
+                              const float* weights, const int32_t* offsets, const int32_t* counts,
+                              const int32_t* inverse, int64_t T, int64_t H, int E, int top_k, int align, void* drows,
+                              int64_t ld_drows, float* dweights, void* stream);
+
+/*
+ * nvfp4_linear -- matrix product of 16-bit operands with bias, activation and
+ * residual, of one matrix or of each expert:
+ *   z[m][n] = sum over k of x[m][k] * w[n][k] + bias[n]     (FP32)
+ *   out[m][n] = act(z[m][n]) + residual[m][n]               (rounded once)
+ * With NVFP4_ACT_SWIGLU w has 2N rows, the gate's and then the up's, and out the N
+ * columns act(z[m][n], z[m][N + n]); "wide" below is 2N then, else N.
+ *
+ * nvfp4_linear_shape: M rows of x, N output columns, K inputs; `type` of x and w
+ * (NVFP4_BF16 or _F16); the activation and, for SwiGLU, its limits (> 0, infinity
+ * for none).  groups 0: one matrix.  groups >= 1 (at most 256): w is [groups][wide]
+ * [K], bias [groups][wide], and rows offsets[g] .. offsets[g] + counts[g] - 1 belong
+ * to expert g (device i32 tables of nvfp4_sort_tokens; all rows below M).  The other
+ * rows are neither used nor written.
+ *   x         device [M][K], row stride ld_x
+ *   w         device [wide][K] contiguous
+ *   bias      device of bias_type (`type` or NVFP4_F32), or NULL
+ *   residual  device [M][N] of `type`, row stride ld_residual, or NULL
+ *   preact    device [M][wide] of `type` contiguous, or NULL: z, as nvfp4_linear_grad takes it
+ *   out       device [M][N] of out_type (`type` or NVFP4_F32), row stride ld_out; may be
+ *             residual itself (same type and stride)
+ * 0 <= M <= 2^22 (0: no work), N and K multiples of 8 up to 131072; row strides
+ * multiples of 8; pointers 16-byte aligned, tables 4.  A device-side timeout is
+ * reported in the library's status word (nvfp4_device_status).
+ */
+typedef struct {
+  int64_t M, N, K;
+  int type, activation;
+  float gate_limit, up_limit;
+  int groups;
+  const int32_t *offsets, *counts;
+} nvfp4_linear_shape;
+int nvfp4_linear(const nvfp4_linear_shape* shape, const void* x, int64_t ld_x, const void* w, const void* bias,
+                 int bias_type, const void* residual, int64_t ld_residual, void* preact, void* out, int64_t ld_out,
+                 int out_type, void* stream);
+
+/*
+ * nvfp4_linear_grad -- the gradients of nvfp4_linear from dy, that of its output:
+ *   dz = dy * act'(z)      (FP32, rounded to `type` as an operand of the products; limits
+ *                           pass the gradient up to and at their value; relu'(0) = 0)
+ *   dx = dz w,  dw = dz^T x  (FP32 sums, rounded once),  dbias = sum over m of dz (FP32, unrounded dz)
+ *   dy        device [M][N] of `type`, row stride ld_dy
+ *   preact    device [M][wide] of `type` contiguous: z; not used without an activation
+ *   dx        device [M][K] of `type`, row stride ld_dx, or NULL
+ *   dw        device [wide][K] of `type` contiguous (of each group), or NULL
+ *   dbias     device f32 [wide] (of each group), or NULL
+ * w is used for dx, x for dw.  Experts without rows get zeros in dw and dbias;
+ * M == 0 writes zeros there.  The gradient of residual is dy.
+ *   workspace device scratch of nvfp4_linear_grad_workspace_size() bytes (0: none
+ *             needed), 256-byte aligned, for one call at a time
+ * Sizes, strides and alignment as nvfp4_linear.
+ */
+size_t nvfp4_linear_grad_workspace_size(const nvfp4_linear_shape* shape, int products, int dbias);
+int nvfp4_linear_grad(const nvfp4_linear_shape* shape, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                      const void* w, const void* preact, void* dx, int64_t ld_dx, void* dw, float* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -305,6 +305,108 @@ class FFNBlock:
         return self.layer(y, logits, self.weights, *self.limits, stream=stream), s
 
 
+@dataclass
+class TokenOrder:
+    """Where sort_tokens has put the tokens' rows (see nvfp4_sort_tokens).  The tables
+    are parts of one allocation where they are small."""
+    offsets: torch.Tensor  # i32 [E + 1], an expert's first row; the last: rows in all
+    counts: torch.Tensor   # i32 [E], an expert's rows without pad rows
+    source: torch.Tensor   # i32 [capacity], a row's assignment t * top_k + j, -1 for all other rows
+    inverse: torch.Tensor  # i32 [T, top_k], an assignment's row, -1 for an expert held elsewhere
+    align: int = 1
+
+
+def sort_tokens(x, topk_ids, E, experts_start=0, align=1, out=None, stream=None):
+    """The tokens' rows in the order of the experts (see nvfp4_sort_tokens): x bf16,
+    f16 or f32 [T, H] (rows may be strided), topk_ids i32 [T, top_k] of the model's
+    experts, of which [experts_start, experts_start + E) are held here.  align: an
+    expert's first row is a multiple of it (128: the slots of grouped_gemm), with rows
+    of zeros between.  Returns (rows [capacity, H], TokenOrder); capacity is T * top_k
+    with align 1.  Rows behind the last expert's are not written: out keeps what it has
+    there, a new tensor anything."""
+    rows, *tables = C.sort_tokens(x, topk_ids, E, experts_start, align, out, _handle(stream))
+    return rows, TokenOrder(*tables, align)
+
+
+def sort_tokens_grad(grad_rows, order: TokenOrder, out=None, stream=None):
+    """The gradient of sort_tokens' x from that of its rows: each token's rows added up."""
+    return C.sort_tokens_grad(grad_rows, order.inverse, out, _handle(stream))
+
+
+def combine_tokens(rows, weights, order: TokenOrder, residual=None, out=None, stream=None):
+    """out[t] = residual[t] + sum over j of weights[t][j] * (row of token t at its j-th
+    expert) (see nvfp4_combine_tokens): rows bf16, f16 or f32 [capacity, H], weights f32
+    [T, top_k], residual of rows' type [T, H] (rows may be strided), out may be it."""
+    return C.combine_tokens(rows, weights, order.inverse, residual, out, _handle(stream))
+
+
+def combine_tokens_grad(grad_out, rows, weights, order: TokenOrder, out=None, stream=None):
+    """The gradients of combine_tokens' rows (into out, if given; rows behind the last
+    expert's are not written) and of its weights (f32).  That of residual is grad_out."""
+    return C.combine_tokens_grad(grad_out, rows, weights, order.offsets, order.counts, order.inverse, order.align, out,
+                                 _handle(stream))
+
+
+_ACTIVATIONS = {None: B.NVFP4_ACT_NONE, "relu": B.NVFP4_ACT_RELU, "silu": B.NVFP4_ACT_SILU, "gelu": B.NVFP4_ACT_GELU,
+                "gelu_tanh": B.NVFP4_ACT_GELU_TANH, "swiglu": B.NVFP4_ACT_SWIGLU}
+_INF = float("inf")
+
+
+def _activation(name):
+    try:
+        return _ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be one of {', '.join(map(str, _ACTIVATIONS))}, not {name!r}") from None
+
+
+def _f32(out_dtype, out, x):
+    dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    if dtype is not torch.float32 and dtype is not x.dtype:
+        raise ValueError(f"the output must be {x.dtype} as x, or torch.float32, not {dtype}")
+    return dtype is torch.float32
+
+
+def linear(x, w, bias=None, activation=None, residual=None, gate_limit=_INF, up_limit=_INF, out_dtype=None,
+           preact=False, out=None, stream=None):
+    """activation(x @ w.T + bias) + residual (see nvfp4_linear): x bf16 or f16 [M, K]
+    (rows may be strided), w [N, K] of x's type, bias [N] of x's type or f32, residual
+    [M, N] of x's type; the result is of x's type or f32.  activation: None, "relu",
+    "silu", "gelu", "gelu_tanh" or "swiglu", whose w (and bias) has 2N rows, the gate's
+    and the up's, with the two limits.  preact=True: returns (result, x @ w.T + bias),
+    the latter as linear_grad takes it."""
+    y, z = C.linear(x, w, None, bias, _activation(activation), gate_limit, up_limit, residual,
+                    _f32(out_dtype, out, x), preact, out, _handle(stream))
+    return (y, z) if preact else y
+
+
+def linear_grad(grad, x, w, preact=None, activation=None, gate_limit=_INF, up_limit=_INF, bias=False, inputs=True,
+                weights=True, out=None, stream=None):
+    """The gradients of linear from that of its result (see nvfp4_linear_grad): those of
+    x (into out, if given), w and bias (f32), None for what inputs, weights and bias do
+    not ask for.  With an activation preact is what linear(.., preact=True) returned.
+    The gradient of residual is grad."""
+    return C.linear_grad(grad, x, w, None, preact, _activation(activation), gate_limit, up_limit, bias, inputs, weights,
+                         out, _handle(stream))
+
+
+def expert_linear(rows, w, order: TokenOrder, bias=None, activation=None, residual=None, gate_limit=_INF,
+                  up_limit=_INF, out_dtype=None, preact=False, out=None, stream=None):
+    """linear for the rows of each expert in sort_tokens' order: w [E, N, K] ([E, 2N, K]
+    for "swiglu", as MoEWeights has them), bias [E, N].  Rows that belong to no expert
+    are neither used nor written: out keeps what it has there, a new tensor anything."""
+    y, z = C.linear(rows, w, (order.offsets, order.counts), bias, _activation(activation), gate_limit, up_limit,
+                    residual, _f32(out_dtype, out, rows), preact, out, _handle(stream))
+    return (y, z) if preact else y
+
+
+def expert_linear_grad(grad, rows, w, order: TokenOrder, preact=None, activation=None, gate_limit=_INF, up_limit=_INF,
+                       bias=False, inputs=True, weights=True, out=None, stream=None):
+    """linear_grad for the rows of each expert: the gradients of rows (written where
+    expert_linear writes), w and bias; an expert without rows has zeros."""
+    return C.linear_grad(grad, rows, w, (order.offsets, order.counts), preact, _activation(activation), gate_limit,
+                         up_limit, bias, inputs, weights, out, _handle(stream))
+
+
 class HostPipeline:
     """Streams batches from pinned host memory through one MoEForward.
 

@@ -37,6 +37,9 @@ NVFP4_ERR_CUDA = 4
 NVFP4_ERR_DEVICE = 5
 NVFP4_ERR_DEVICE_TIMEOUT = 6
 NVFP4_MOE_FEW_TOKENS_MAX = 32
+NVFP4_BF16, NVFP4_F16, NVFP4_F32 = 0, 1, 2
+(NVFP4_ACT_NONE, NVFP4_ACT_RELU, NVFP4_ACT_SILU, NVFP4_ACT_GELU, NVFP4_ACT_GELU_TANH,
+ NVFP4_ACT_SWIGLU) = range(6)
 
 
 class Nvfp4Error(RuntimeError):
@@ -51,6 +54,13 @@ class MoeLayout(ctypes.Structure):
         "sorted_token_ids", "row_weight", "inverse", "a1", "sfa1", "a2", "sfa2", "y", "h", "calib", "tile_done",
         "total")] + [
         ("capacity", c_i64), ("route_blocks", c_i64)]
+
+
+class LinearShape(ctypes.Structure):
+    """nvfp4_linear_shape."""
+    _fields_ = [("M", c_i64), ("N", c_i64), ("K", c_i64), ("type", c_int), ("activation", c_int),
+                ("gate_limit", c_float), ("up_limit", c_float), ("groups", c_int), ("offsets", c_ptr),
+                ("counts", c_ptr)]
 
 
 def _sig(name, res, args):
@@ -117,6 +127,21 @@ _few = _sig("nvfp4_moe_few_tokens", c_int, [c_ptr, c_i64, c_ptr, c_i64, c_i64, c
 _few_routed = _sig("nvfp4_moe_few_tokens_routed", c_int, [c_ptr, c_i64, c_ptr, c_ptr, ctypes.c_int32, c_i64, c_i64,
                                                           c_i64, c_int, c_int, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr,
                                                           c_ptr, c_float, c_float, c_ptr, c_size, c_ptr, c_ptr])
+_sort_capacity = _sig("nvfp4_sort_tokens_capacity", c_i64, [c_i64, c_int, c_int, c_int])
+_sort_tokens = _sig("nvfp4_sort_tokens", c_int, [c_ptr, c_i64, c_int, c_ptr, ctypes.c_int32, c_i64, c_i64, c_int, c_int,
+                                                 c_int, c_i64, c_ptr, c_i64, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr])
+_sort_grad = _sig("nvfp4_sort_tokens_grad", c_int, [c_ptr, c_i64, c_int, c_ptr, c_i64, c_i64, c_int, c_ptr, c_i64,
+                                                    c_ptr])
+_combine = _sig("nvfp4_combine_tokens", c_int, [c_ptr, c_i64, c_int, c_ptr, c_ptr, c_ptr, c_i64, c_i64, c_i64, c_int,
+                                                c_ptr, c_i64, c_ptr])
+_combine_grad = _sig("nvfp4_combine_tokens_grad", c_int, [c_ptr, c_i64, c_ptr, c_i64, c_int, c_ptr, c_ptr, c_ptr, c_ptr,
+                                                          c_i64, c_i64, c_int, c_int, c_int, c_ptr, c_i64, c_ptr,
+                                                          c_ptr])
+_linear = _sig("nvfp4_linear", c_int, [ctypes.POINTER(LinearShape), c_ptr, c_i64, c_ptr, c_ptr, c_int, c_ptr, c_i64,
+                                       c_ptr, c_ptr, c_i64, c_int, c_ptr])
+_linear_grad_ws = _sig("nvfp4_linear_grad_workspace_size", c_size, [ctypes.POINTER(LinearShape), c_int, c_int])
+_linear_grad = _sig("nvfp4_linear_grad", c_int, [ctypes.POINTER(LinearShape), c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_ptr,
+                                                 c_ptr, c_i64, c_ptr, c_ptr, c_ptr, c_size, c_ptr])
 _moe_set_swap_l2 = _sig("nvfp4_moe_set_swap_l2", c_int, [c_int, ctypes.POINTER(c_int)])
 
 
@@ -358,3 +383,51 @@ def nvfp4_moe_few_tokens_routed(hidden, ld_hidden, topk_ids, topk_weights, exper
     _check(_few_routed(_p(hidden), ld_hidden, _p(topk_ids), _p(topk_weights), experts_start, T, H, I, E, top_k,
                        _p(w13), _p(w13_sf), _p(w13_gs), _p(w2), _p(w2_sf), _p(w2_gs), gate_limit, up_limit,
                        _p(workspace), workspace_bytes, _p(out), _stream(stream)))
+
+
+def nvfp4_sort_tokens_capacity(T, E, top_k, align=1):
+    return _sort_capacity(T, E, top_k, align)
+
+
+def nvfp4_sort_tokens(x, ld_x, type, topk_ids, experts_start, T, H, E, top_k, align, capacity, rows, ld_rows, offsets,
+                      counts, source, inverse, stream=None):
+    _check(_sort_tokens(_p(x), ld_x, type, _p(topk_ids), experts_start, T, H, E, top_k, align, capacity, _p(rows),
+                        ld_rows, _p(offsets), _p(counts), _p(source), _p(inverse), _stream(stream)))
+
+
+def nvfp4_sort_tokens_grad(drows, ld_drows, type, inverse, T, H, top_k, dx, ld_dx, stream=None):
+    _check(_sort_grad(_p(drows), ld_drows, type, _p(inverse), T, H, top_k, _p(dx), ld_dx, _stream(stream)))
+
+
+def nvfp4_combine_tokens(rows, ld_rows, type, weights, inverse, residual, ld_residual, T, H, top_k, out, ld_out,
+                         stream=None):
+    _check(_combine(_p(rows), ld_rows, type, _p(weights), _p(inverse), _p(residual), ld_residual, T, H, top_k, _p(out),
+                    ld_out, _stream(stream)))
+
+
+def nvfp4_combine_tokens_grad(dout, ld_dout, rows, ld_rows, type, weights, offsets, counts, inverse, T, H, E, top_k,
+                              align, drows, ld_drows, dweights, stream=None):
+    _check(_combine_grad(_p(dout), ld_dout, _p(rows), ld_rows, type, _p(weights), _p(offsets), _p(counts), _p(inverse),
+                         T, H, E, top_k, align, _p(drows), ld_drows, _p(dweights), _stream(stream)))
+
+
+def linear_shape(M, N, K, type, activation=NVFP4_ACT_NONE, gate_limit=float("inf"), up_limit=float("inf"), groups=0,
+                 offsets=None, counts=None):
+    """nvfp4_linear_shape of one matrix, or of `groups` experts with their tables."""
+    return LinearShape(M, N, K, type, activation, gate_limit, up_limit, groups, _p(offsets), _p(counts))
+
+
+def nvfp4_linear(shape, x, ld_x, w, bias, bias_type, residual, ld_residual, preact, out, ld_out, out_type,
+                 stream=None):
+    _check(_linear(ctypes.byref(shape), _p(x), ld_x, _p(w), _p(bias), bias_type, _p(residual), ld_residual, _p(preact),
+                   _p(out), ld_out, out_type, _stream(stream)))
+
+
+def nvfp4_linear_grad_workspace_size(shape, products=True, dbias=False):
+    return _linear_grad_ws(ctypes.byref(shape), int(products), int(dbias))
+
+
+def nvfp4_linear_grad(shape, dy, ld_dy, x, ld_x, w, preact, dx, ld_dx, dw, dbias, workspace, workspace_bytes,
+                      stream=None):
+    _check(_linear_grad(ctypes.byref(shape), _p(dy), ld_dy, _p(x), ld_x, _p(w), _p(preact), _p(dx), ld_dx, _p(dw),
+                        _p(dbias), _p(workspace), workspace_bytes, _stream(stream)))

@@ -1180,4 +1180,365 @@ int nvfp4_moe_few_tokens_routed(const void* hidden, int64_t ld_hidden, const int
                       up_limit, workspace, workspace_bytes, out, stream);
 }
 
+static int64_t type_size(int type) { return type == NVFP4_F32 ? 4 : 2; }
+
+// Row strides in elements, for the calls that copy and add rows by 16 bytes.
+static int check_rows(int64_t T, int64_t H, int type) {
+  if (type != NVFP4_BF16 && type != NVFP4_F16 && type != NVFP4_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "type must be NVFP4_BF16, NVFP4_F16 or NVFP4_F32");
+  if (T < 0 || T > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+  if (H <= 0 || H > (1 << 24) || H * type_size(type) % 16)
+    return fail(NVFP4_ERR_UNSUPPORTED, "a row's bytes must be a positive multiple of 16 (H at most 2^24)");
+  return NVFP4_OK;
+}
+static bool bad_stride(int64_t ld, int64_t H, int type) { return ld < H || ld * type_size(type) % 16; }
+
+int64_t nvfp4_sort_tokens_capacity(int64_t T, int E, int top_k, int align) {
+  if (T < 0 || T > INT32_MAX || E < 1 || E > 256 || top_k < 1 || top_k > 32 || align < 1 || align > 128 ||
+      (align & (align - 1)))
+    return 0;
+  const int64_t n = T * top_k, most = n + (n < E ? n : E) * (align - 1);
+  return most > INT32_MAX ? 0 : most;
+}
+
+int nvfp4_sort_tokens(const void* x, int64_t ld_x, int type, const int32_t* topk_ids, int32_t experts_start, int64_t T,
+                      int64_t H, int E, int top_k, int align, int64_t capacity, void* rows, int64_t ld_rows,
+                      int32_t* offsets, int32_t* counts, int32_t* source, int32_t* inverse, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_rows(T, H, type)) return rc;
+  if (E < 1 || E > 256) return fail(NVFP4_ERR_UNSUPPORTED, "E must be in [1, 256]");
+  if (top_k < 1 || top_k > 32) return fail(NVFP4_ERR_UNSUPPORTED, "top_k must be in [1, 32]");
+  if (align < 1 || align > 128 || (align & (align - 1)))
+    return fail(NVFP4_ERR_INVALID_ARG, "align must be a power of two up to 128");
+  const int64_t need = nvfp4_sort_tokens_capacity(T, E, top_k, align);
+  if (need == 0 && T > 0) return fail(NVFP4_ERR_UNSUPPORTED, "more than 2^31 rows");
+  if (capacity < need || capacity > INT32_MAX)
+    return fail(NVFP4_ERR_INVALID_ARG, "capacity must be in [%lld, 2^31)", (long long)need);
+  if (!offsets || !counts || (T > 0 && (!topk_ids || !inverse)) || (capacity > 0 && !source) ||
+      (T > 0 && rows && !x))
+    return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (rows && (bad_stride(ld_x, H, type) || bad_stride(ld_rows, H, type)))
+    return fail(NVFP4_ERR_INVALID_ARG, "row strides must be >= H and multiples of 16 bytes");
+  if ((rows && (!aligned16(x) || !aligned16(rows))) || !aligned4(topk_ids) || !aligned4(offsets) ||
+      !aligned4(counts) || !aligned4(source) || !aligned4(inverse))
+    return fail(NVFP4_ERR_INVALID_ARG, "x and rows must be 16-byte aligned, tables 4");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  SortArgs a = {};
+  a.x = (const uint8_t*)x;
+  a.ld_x = ld_x * type_size(type);
+  a.rows = (uint8_t*)rows;
+  a.ld_rows = ld_rows * type_size(type);
+  a.ids = topk_ids;
+  a.start = experts_start;
+  a.offsets = offsets;
+  a.counts = counts;
+  a.source = source;
+  a.inverse = inverse;
+  a.T = T;
+  a.capacity = capacity;
+  a.E = E;
+  a.k = top_k;
+  a.align = align;
+  a.nvec = (int)(H * type_size(type) / 16);
+  cudaError_t e = launch_sort_tokens(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "sort_tokens launch");
+}
+
+static int combine_impl(const void* rows, int64_t ld_rows, int type, const float* weights, bool weighted,
+                        const int32_t* inverse, const void* residual, int64_t ld_residual, int64_t T, int64_t H,
+                        int top_k, void* out, int64_t ld_out, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_rows(T, H, type)) return rc;
+  if (top_k < 1 || top_k > 32) return fail(NVFP4_ERR_UNSUPPORTED, "top_k must be in [1, 32]");
+  if (T == 0) return NVFP4_OK;
+  if (!rows || (weighted && !weights) || !inverse || !out) return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (bad_stride(ld_rows, H, type) || bad_stride(ld_out, H, type) || (residual && bad_stride(ld_residual, H, type)))
+    return fail(NVFP4_ERR_INVALID_ARG, "row strides must be >= H and multiples of 16 bytes");
+  if (residual == out && ld_residual != ld_out)
+    return fail(NVFP4_ERR_INVALID_ARG, "an output in place of the residual needs its stride");
+  if (!aligned16(rows) || !aligned16(residual) || !aligned16(out) || !aligned4(weights) || !aligned4(inverse))
+    return fail(NVFP4_ERR_INVALID_ARG, "rows must be 16-byte aligned, weights and tables 4");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  CombineArgs a = {};
+  a.rows = (const uint8_t*)rows;
+  a.ld_rows = ld_rows * type_size(type);
+  a.weights = weights;
+  a.inverse = inverse;
+  a.residual = (const uint8_t*)residual;
+  a.ld_residual = ld_residual * type_size(type);
+  a.out = (uint8_t*)out;
+  a.ld_out = ld_out * type_size(type);
+  a.T = T;
+  a.k = top_k;
+  a.nvec = (int)(H * type_size(type) / 16);
+  cudaError_t e = launch_combine_tokens(a, type, dev->sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "combine_tokens launch");
+}
+
+int nvfp4_sort_tokens_grad(const void* drows, int64_t ld_drows, int type, const int32_t* inverse, int64_t T, int64_t H,
+                           int top_k, void* dx, int64_t ld_dx, void* stream) {
+  return combine_impl(drows, ld_drows, type, nullptr, false, inverse, nullptr, 0, T, H, top_k, dx, ld_dx, stream);
+}
+
+int nvfp4_combine_tokens(const void* rows, int64_t ld_rows, int type, const float* weights, const int32_t* inverse,
+                         const void* residual, int64_t ld_residual, int64_t T, int64_t H, int top_k, void* out,
+                         int64_t ld_out, void* stream) {
+  return combine_impl(rows, ld_rows, type, weights, true, inverse, residual, ld_residual, T, H, top_k, out, ld_out,
+                      stream);
+}
+
+int nvfp4_combine_tokens_grad(const void* dout, int64_t ld_dout, const void* rows, int64_t ld_rows, int type,
+                              const float* weights, const int32_t* offsets, const int32_t* counts,
+                              const int32_t* inverse, int64_t T, int64_t H, int E, int top_k, int align, void* drows,
+                              int64_t ld_drows, float* dweights, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_rows(T, H, type)) return rc;
+  if (E < 1 || E > 256) return fail(NVFP4_ERR_UNSUPPORTED, "E must be in [1, 256]");
+  if (top_k < 1 || top_k > 32) return fail(NVFP4_ERR_UNSUPPORTED, "top_k must be in [1, 32]");
+  if (align < 1 || align > 128 || (align & (align - 1)))
+    return fail(NVFP4_ERR_INVALID_ARG, "align must be a power of two up to 128");
+  if (T == 0) return NVFP4_OK;
+  if (!dout || !rows || !weights || !offsets || !counts || !inverse || !drows || !dweights)
+    return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (bad_stride(ld_dout, H, type) || bad_stride(ld_rows, H, type) || bad_stride(ld_drows, H, type))
+    return fail(NVFP4_ERR_INVALID_ARG, "row strides must be >= H and multiples of 16 bytes");
+  if (!aligned16(dout) || !aligned16(rows) || !aligned16(drows) || !aligned4(weights) || !aligned4(offsets) ||
+      !aligned4(counts) || !aligned4(inverse) || !aligned4(dweights))
+    return fail(NVFP4_ERR_INVALID_ARG, "rows must be 16-byte aligned, weights and tables 4");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  CombineGradArgs a = {};
+  a.dout = (const uint8_t*)dout;
+  a.ld_dout = ld_dout * type_size(type);
+  a.rows = (const uint8_t*)rows;
+  a.ld_rows = ld_rows * type_size(type);
+  a.weights = weights;
+  a.offsets = offsets;
+  a.counts = counts;
+  a.inverse = inverse;
+  a.drows = (uint8_t*)drows;
+  a.ld_drows = ld_drows * type_size(type);
+  a.dweights = dweights;
+  a.T = T;
+  a.E = E;
+  a.k = top_k;
+  a.align = align;
+  a.nvec = (int)(H * type_size(type) / 16);
+  cudaError_t e = launch_combine_tokens_grad(a, type, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "combine_tokens_grad launch");
+}
+
+// 16-bit matrices [depth][rows][cols] with a row stride (elements); box of 64
+// elements x box_rows, 128-byte swizzle; past the edges of each matrix zeros.
+static int make_half_map(CUtensorMap* map, const void* base, int64_t depth, int64_t rows, int64_t cols, int64_t ld,
+                         int box_rows, int type, bool three) {
+  auto fn = encode_fn();
+  if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * rows) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, type == NVFP4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        three ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return NVFP4_OK;
+}
+
+static int64_t linear_wide(const nvfp4_linear_shape* s) { return s->activation == NVFP4_ACT_SWIGLU ? 2 * s->N : s->N; }
+
+static int check_linear(const nvfp4_linear_shape* s) {
+  if (!s) return fail(NVFP4_ERR_INVALID_ARG, "null shape");
+  if (s->M < 0 || s->M > (1 << 22)) return fail(NVFP4_ERR_INVALID_ARG, "M must be in [0, 4194304]");
+  if (s->N <= 0 || s->N % 8 || s->N > 131072)
+    return fail(NVFP4_ERR_INVALID_ARG, "N must be a positive multiple of 8, at most 131072");
+  if (s->K <= 0 || s->K % 8 || s->K > 131072)
+    return fail(NVFP4_ERR_INVALID_ARG, "K must be a positive multiple of 8, at most 131072");
+  if (s->type != NVFP4_BF16 && s->type != NVFP4_F16)
+    return fail(NVFP4_ERR_INVALID_ARG, "type must be NVFP4_BF16 or NVFP4_F16");
+  if (s->activation < NVFP4_ACT_NONE || s->activation > NVFP4_ACT_SWIGLU)
+    return fail(NVFP4_ERR_INVALID_ARG, "unknown activation %d", s->activation);
+  if (s->activation == NVFP4_ACT_SWIGLU && (!(s->gate_limit > 0.f) || !(s->up_limit > 0.f)))
+    return fail(NVFP4_ERR_INVALID_ARG, "limits must be positive");
+  if (s->groups < 0 || s->groups > 256) return fail(NVFP4_ERR_UNSUPPORTED, "groups must be in [0, 256]");
+  if (s->groups && s->M && (!s->offsets || !s->counts)) return fail(NVFP4_ERR_INVALID_ARG, "null table");
+  if (!aligned4(s->offsets) || !aligned4(s->counts)) return fail(NVFP4_ERR_INVALID_ARG, "tables must be 4-byte aligned");
+  return NVFP4_OK;
+}
+
+// Plan, maps and launch of one product (args filled in but for these).
+static int run_linear_gemm(LinearArgs& t, const nvfp4_linear_shape* s, const void* a, int64_t a_rows, int64_t a_cols,
+                           int64_t ld_a, const void* b, int64_t b_depth, int64_t b_rows, int64_t b_cols, int64_t ld_b,
+                           const DeviceInfo* dev, void* stream) {
+  t.G = s->groups ? s->groups : 1;
+  t.offsets = s->groups ? s->offsets : nullptr;
+  t.counts = s->groups ? s->counts : nullptr;
+  t.status = dev->status;
+  t.stall = g_debug_stall_ms > 0;
+  cudaError_t e = linear_gemm_plan(t, dev->sms);
+  if (e != cudaSuccess) return cuda_fail(e, "linear plan");
+  if (int rc = make_half_map(&t.map_a, a, 1, a_rows, a_cols, ld_a, t.a_mn ? 64 : 128, s->type, false)) return rc;
+  if (int rc = make_half_map(&t.map_b, b, b_depth, b_rows, b_cols, ld_b, t.b_mn ? 64 : t.bn / 2, s->type, true))
+    return rc;
+  e = launch_linear_gemm(t, dev->sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "linear launch");
+}
+
+int nvfp4_linear(const nvfp4_linear_shape* s, const void* x, int64_t ld_x, const void* w, const void* bias,
+                 int bias_type, const void* residual, int64_t ld_residual, void* preact, void* out, int64_t ld_out,
+                 int out_type, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_linear(s)) return rc;
+  if ((bias && bias_type != s->type && bias_type != NVFP4_F32) || (out_type != s->type && out_type != NVFP4_F32))
+    return fail(NVFP4_ERR_INVALID_ARG, "bias and output must be of x's type or NVFP4_F32");
+  if (s->M == 0) return NVFP4_OK;
+  if (!x || !w || !out) return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (ld_x < s->K || ld_x % 8 || ld_out < s->N || ld_out % 8 || (residual && (ld_residual < s->N || ld_residual % 8)))
+    return fail(NVFP4_ERR_INVALID_ARG, "row strides must reach over the row and be multiples of 8");
+  if (residual == out && (ld_residual != ld_out || out_type != s->type))
+    return fail(NVFP4_ERR_INVALID_ARG, "an output in place of the residual needs its type and stride");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(preact) ||
+      !aligned16(out))
+    return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  LinearEpilogue ep = {};
+  ep.bias = bias;
+  ep.residual = residual;
+  ep.preact = preact;
+  ep.out = out;
+  ep.ld_residual = ld_residual;
+  ep.ld_preact = linear_wide(s);
+  ep.ld_out = ld_out;
+  ep.N = (int)s->N;
+  ep.wide = (int)linear_wide(s);
+  ep.type = s->type;
+  ep.out_type = out_type;
+  ep.bias_type = bias_type;
+  ep.act = s->activation;
+  ep.gate_limit = s->gate_limit;
+  ep.up_limit = s->up_limit;
+  if (linear_is_few(s->M, s->groups)) {
+    LinearFewArgs f = {};
+    f.a = (const uint8_t*)x;
+    f.w = (const uint8_t*)w;
+    f.ep = ep;
+    f.offsets = s->groups ? s->offsets : nullptr;
+    f.counts = s->groups ? s->counts : nullptr;
+    f.ld_a = ld_x;
+    f.M = (int)s->M;
+    f.K = (int)s->K;
+    f.G = s->groups ? s->groups : 1;
+    cudaError_t e = launch_linear_few(f, (cudaStream_t)stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "linear launch");
+  }
+  LinearArgs t;
+  memset(&t, 0, sizeof(t));
+  t.ep = ep;
+  t.M = (int)s->M;
+  t.N = (int)s->N;
+  t.K = (int)s->K;
+  return run_linear_gemm(t, s, x, s->M, s->K, ld_x, w, s->groups ? s->groups : 1, ep.wide, s->K, s->K, dev, stream);
+}
+
+// Workspace of the gradient: dz (where it is not dy), then the slabs' column sums.
+static size_t linear_grad_layout(const nvfp4_linear_shape* s, int products, int dbias, size_t* partial) {
+  const int64_t wide = linear_wide(s);
+  size_t off = products && s->activation != NVFP4_ACT_NONE ? (size_t)round_up(s->M * wide * 2, 256) : 0;
+  *partial = off;
+  if (dbias) off += (size_t)round_up(linear_grad_slabs(s->M, s->groups) * wide * 4, 256);
+  return s->M ? off : 0;
+}
+
+size_t nvfp4_linear_grad_workspace_size(const nvfp4_linear_shape* s, int products, int dbias) {
+  size_t partial;
+  return check_linear(s) == NVFP4_OK ? linear_grad_layout(s, products, dbias, &partial) : 0;
+}
+
+int nvfp4_linear_grad(const nvfp4_linear_shape* s, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                      const void* w, const void* preact, void* dx, int64_t ld_dx, void* dw, float* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_linear(s)) return rc;
+  const int64_t wide = linear_wide(s), G = s->groups ? s->groups : 1;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(w) || !aligned16(preact) || !aligned16(dx) || !aligned16(dw) ||
+      !aligned4(dbias))
+    return fail(NVFP4_ERR_INVALID_ARG, "pointers must be 16-byte aligned (dbias 4)");
+  const bool act = s->activation != NVFP4_ACT_NONE;
+  size_t partial = 0;
+  const size_t need = linear_grad_layout(s, dx || dw, dbias != nullptr, &partial);
+  if (s->M > 0) {
+    if (!dy || (act && !preact) || (dw && !x) || (dx && !w)) return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+    if (ld_dy < s->N || ld_dy % 8 || (dw && (ld_x < s->K || ld_x % 8)) || (dx && (ld_dx < s->K || ld_dx % 8)))
+      return fail(NVFP4_ERR_INVALID_ARG, "row strides must reach over the row and be multiples of 8");
+    if (need && (!workspace || workspace_bytes < need))
+      return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes needed", need);
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  cudaError_t e = cudaSuccess;
+  if (s->M == 0) {
+    if (dw) e = cudaMemsetAsync(dw, 0, (size_t)(G * wide * s->K) * 2, (cudaStream_t)stream);
+    if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, (size_t)(G * wide) * 4, (cudaStream_t)stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "linear_grad");
+  }
+  const void* dz = dy;
+  int64_t ld_dz = ld_dy;
+  if (dbias || (act && (dx || dw))) {
+    LinearGradArgs g = {};
+    g.dy = dy;
+    g.ld_dy = ld_dy;
+    g.z = preact;
+    if (act && (dx || dw)) {
+      dz = g.dz = workspace;
+      ld_dz = wide;
+    }
+    if (dbias) {
+      g.partial = reinterpret_cast<float*>((uint8_t*)workspace + partial);
+      g.dbias = dbias;
+    }
+    g.offsets = s->groups ? s->offsets : nullptr;
+    g.counts = s->groups ? s->counts : nullptr;
+    g.M = (int)s->M;
+    g.N = (int)s->N;
+    g.wide = (int)wide;
+    g.G = (int)G;
+    g.type = s->type;
+    g.act = s->activation;
+    g.gate_limit = s->gate_limit;
+    g.up_limit = s->up_limit;
+    e = launch_linear_dz(g, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "linear_grad launch");
+  }
+  LinearArgs t;
+  if (dx) {
+    memset(&t, 0, sizeof(t));
+    t.ep.out = dx;
+    t.ep.ld_out = ld_dx;
+    t.ep.type = t.ep.out_type = s->type;
+    t.ep.N = t.N = (int)s->K;
+    t.M = (int)s->M;
+    t.K = (int)wide;
+    t.b_mn = 1;
+    if (int rc = run_linear_gemm(t, s, dz, s->M, wide, ld_dz, w, G, wide, s->K, s->K, dev, stream)) return rc;
+  }
+  if (dw) {
+    memset(&t, 0, sizeof(t));
+    t.ep.out = dw;
+    t.ep.ld_out = s->K;
+    t.ep.type = t.ep.out_type = s->type;
+    t.ep.N = t.N = (int)s->K;
+    t.M = (int)wide;
+    t.K = (int)s->M;
+    t.a_mn = t.b_mn = t.by_k = 1;
+    if (int rc = run_linear_gemm(t, s, dz, s->M, wide, ld_dz, x, 1, s->M, s->K, ld_x, dev, stream)) return rc;
+  }
+  return NVFP4_OK;
+}
+
 }  // extern "C"

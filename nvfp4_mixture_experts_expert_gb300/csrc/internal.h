@@ -319,4 +319,91 @@ struct FewMaps {
 };
 cudaError_t launch_moe_few(const FewArgs& a, const FewMaps& w13, const FewMaps& w2, int num_sms, cudaStream_t s);
 
+// ---------------------------------------------------------------- token_sort.cu
+enum TensorType { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };  // NVFP4_BF16 ..
+struct SortArgs {
+  const uint8_t* x;  // [T] rows of nvec 16-byte vectors; row strides in bytes here and below
+  int64_t ld_x, ld_rows;
+  const int32_t* ids;  // [T][k] global experts
+  uint8_t* rows;       // [capacity], or null: the order alone
+  int32_t *offsets, *counts, *source, *inverse;
+  int64_t T, capacity;
+  int start, E, k, align, nvec;
+};
+cudaError_t launch_sort_tokens(const SortArgs& a, cudaStream_t s);
+struct CombineArgs {
+  const uint8_t* rows;
+  const float* weights;      // [T][k], or null: each 1
+  const uint8_t* residual;   // or null
+  const int32_t* inverse;
+  uint8_t* out;
+  int64_t ld_rows, ld_residual, ld_out, T;
+  int k, nvec;
+};
+cudaError_t launch_combine_tokens(const CombineArgs& a, int type, int num_sms, cudaStream_t s);
+struct CombineGradArgs {
+  const uint8_t *dout, *rows;
+  const float* weights;
+  const int32_t *offsets, *counts, *inverse;
+  uint8_t* drows;
+  float* dweights;
+  int64_t ld_dout, ld_rows, ld_drows, T;
+  int E, k, align, nvec;
+};
+cudaError_t launch_combine_tokens_grad(const CombineGradArgs& a, int type, cudaStream_t s);
+
+// ---------------------------------------------------------------- linear_gemm.cu, linear_few.cu
+enum Activation { kActNone, kActRelu, kActSilu, kActGelu, kActGeluTanh, kActSwiglu };  // NVFP4_ACT_..
+struct LinearEpilogue {
+  const void* bias;      // [G][wide], or null
+  const void* residual;  // [rows][N] of `type`, or null
+  void* preact;          // [rows][wide] of `type`, or null
+  void* out;             // [rows][N]
+  int64_t ld_residual, ld_preact, ld_out;
+  int N, wide;           // output columns; rows of w (twice N for SwiGLU)
+  int type, out_type, bias_type, act;
+  float gate_limit, up_limit;
+};
+struct LinearArgs {
+  CUtensorMap map_a;  // see linear_gemm.cu
+  CUtensorMap map_b;
+  LinearEpilogue ep;
+  const int32_t *offsets, *counts;  // rows of each group, or null: one group of M rows
+  int* status;
+  int M, N, K;   // output rows (a group's, with by_k), output columns, contraction (N: of the output, not twice it)
+  int G;         // groups
+  int a_mn, b_mn;  // operand stored with its output dimension contiguous
+  int by_k;      // the groups' rows are the contraction (weight gradients)
+  int second;    // rows of B from the first to the second half of a tile
+  int stall;     // failure-detection check: only a tile's first K-block is loaded
+  int bn, split;               // set by linear_gemm_plan
+  int m_tiles, n_tiles, tiles; // set by the launch (tiles: where the host knows them)
+};
+cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms);  // from the sizes, groups and activation
+cudaError_t launch_linear_gemm(LinearArgs& p, int num_sms, cudaStream_t s);
+constexpr int64_t kLinearFewRows = 8;  // rows (of a group) of one pass of the few-row kernel
+bool linear_is_few(int64_t M, int groups);  // whether that kernel is used
+struct LinearFewArgs {
+  const uint8_t *a, *w;  // 16-bit [M][K] (row stride ld_a elements), [G][wide][K]
+  LinearEpilogue ep;
+  const int32_t *offsets, *counts;
+  int64_t ld_a;
+  int M, K, G;
+};
+cudaError_t launch_linear_few(const LinearFewArgs& p, cudaStream_t s);
+
+// ---------------------------------------------------------------- linear_grad.cu
+struct LinearGradArgs {
+  const void *dy, *z;  // [rows][N], [rows][wide]
+  void* dz;            // [rows][wide], or null
+  float* partial;      // [linear_grad_slabs()][wide], or null
+  float* dbias;        // [G][wide], with partial
+  const int32_t *offsets, *counts;  // or null
+  int64_t ld_dy;
+  int M, N, wide, G, type, act;
+  float gate_limit, up_limit;
+};
+int64_t linear_grad_slabs(int64_t M, int groups);  // groups 0: one matrix
+cudaError_t launch_linear_dz(const LinearGradArgs& p, cudaStream_t s);
+
 }  // namespace nvfp4

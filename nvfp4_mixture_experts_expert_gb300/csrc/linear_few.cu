@@ -1,0 +1,129 @@
+// 16-bit linear for few rows of activations, of one matrix or of each expert (see
+// nvfp4_linear, nvfp4_linear_shape):
+//
+//   out[m][n] = act(sum_k x[m][k] * w[n][k] + bias[n]) + residual[m][n]
+//
+// A block computes 16 rows of w (SwiGLU: eight of the gate and their eight of the
+// up half) against up to kLinearFewRows rows of x at a time.  w is the M operand of
+// mma.sync.m16n8k16: the K order inside a block of 64 is free as long as both
+// operands use the same, so a lane holds 32 consecutive bytes of its rows (the
+// four lanes of a quad together one 128-byte line) and nothing is staged.  The
+// block's warps split K; their sums are added in a fixed order.
+//
+// Bound: reading w.  Launches are chained, and a block has its part of w fetched
+// into L2 before it waits for the kernel before (not with experts: which of them
+// have rows is that kernel's result).
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "linear_epilogue.cuh"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kRows = (int)kLinearFewRows;
+static_assert(kRows == 8, "the N of one mma");
+
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 32 bytes at p + off (16-byte granules past `end` read as zero).
+__device__ __forceinline__ void load32(const uint8_t* p, int off, int end, uint32_t (&v)[8]) {
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const uint4 a = off < end ? __ldg(reinterpret_cast<const uint4*>(p + off)) : z;
+  const uint4 b = off + 16 < end ? __ldg(reinterpret_cast<const uint4*>(p + off + 16)) : z;
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kWarps * 32) linear_few_kernel(const LinearFewArgs p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const bool pairs = p.ep.act == kActSwiglu;
+  const int out_cols = pairs ? 8 : 16;
+  const int n0 = blockIdx.x * out_cols, group = blockIdx.y;
+  const int bytes = p.K * 2, kbs = (p.K + 63) / 64;
+  __shared__ float4 part[kWarps][32];
+  __shared__ float sums[kRows][16];
+  const uint8_t* w = p.w + (int64_t)group * p.ep.wide * bytes;
+  const uint8_t* w0 = w + (int64_t)min(n0 + g, p.ep.N - 1) * bytes;
+  const uint8_t* w1 = w + (int64_t)(pairs ? p.ep.N + min(n0 + g, p.ep.N - 1) : min(n0 + g + 8, p.ep.N - 1)) * bytes;
+  if (!p.counts) {
+    for (int kb = warp; kb < kbs; kb += kWarps) {
+      const int off = kb * 128 + q * 32;
+      if (off < bytes) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + off));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + off));
+      }
+    }
+  }
+  pdl_trigger();
+  pdl_wait();
+  const int rows = p.counts ? p.counts[group] : p.M;
+  const int64_t row0 = p.counts ? p.offsets[group] : 0;
+  for (int m0 = 0; m0 < rows; m0 += kRows) {
+    const int here = min(kRows, rows - m0);
+    const uint8_t* x = p.a + (row0 + m0 + min(g, here - 1)) * p.ld_a * 2;
+    float acc[4] = {};
+#pragma unroll 2
+    for (int kb = warp; kb < kbs; kb += kWarps) {
+      const int off = kb * 128 + q * 32;
+      uint32_t a0[8], a1[8], b[8];
+      load32(w0, off, bytes, a0);
+      load32(w1, off, bytes, a1);
+      load32(x, off, bytes, b);  // lanes past the last row repeat it: their sums are not stored
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mma16<BF16>(acc, a0[2 * i], a1[2 * i], a0[2 * i + 1], a1[2 * i + 1], b[2 * i], b[2 * i + 1]);
+    }
+    part[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (threadIdx.x < kRows * 16) {
+      const int r = threadIdx.x & 15, m = threadIdx.x >> 4;
+      const int src = (r & 7) * 4 + m / 2, c = (r >> 3) * 2 + (m & 1);
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) v += reinterpret_cast<const float*>(&part[i][src])[c];
+      sums[m][r] = v;
+    }
+    __syncthreads();
+    const int per = out_cols / 8, m = threadIdx.x / per, c = threadIdx.x % per * 8, col = n0 + c;
+    if (m < here && col < p.ep.N) {
+      float z[8], u[8], bias[8], bias_u[8];
+      load_bias(p.ep, group, col, bias, bias_u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = sums[m][c + i], u[i] = sums[m][8 + i];
+      finish8(p.ep, row0 + m0 + m, col, z, u, bias, bias_u);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+// One pass over w; with experts as long as most have a pass of rows at most.
+bool linear_is_few(int64_t M, int groups) { return groups ? M <= 4 * (int64_t)groups : M <= kLinearFewRows; }
+
+cudaError_t launch_linear_few(const LinearFewArgs& p, cudaStream_t s) {
+  const int out_cols = p.ep.act == kActSwiglu ? 8 : 16;
+  const dim3 grid((p.ep.N + out_cols - 1) / out_cols, p.G);
+  return launch_kernel(p.ep.type == kTypeBf16 ? linear_few_kernel<true> : linear_few_kernel<false>, grid,
+                       dim3(kWarps * 32), 0, s, true, p);
+}
+
+}  // namespace nvfp4

@@ -285,6 +285,295 @@ PyObject* moe_few_tokens(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Element type of rows of tokens (`all`) or of a linear's operands (16 bits).
+int type_of(const at::Tensor& t, const char* name, bool all) {
+  switch (t.scalar_type()) {
+    case at::kBFloat16: return NVFP4_BF16;
+    case at::kHalf: return NVFP4_F16;
+    case at::kFloat:
+      if (all) return NVFP4_F32;
+    default:
+      TORCH_CHECK_VALUE(false, name, " must be ", all ? "bfloat16, float16 or float32" : "bfloat16 or float16", ", not ",
+                        t.scalar_type());
+  }
+}
+
+void two_dims(const at::Tensor& t, const char* name) {
+  TORCH_CHECK_VALUE(t.dim() == 2, name, " must have two dimensions, not ", t.dim());
+}
+
+int64_t number(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+int small_number(PyObject* o, const char* name) {
+  const int64_t v = number(o);
+  TORCH_CHECK_VALUE(v >= INT32_MIN && v <= INT32_MAX, name, " must be a 32-bit number");
+  return (int)v;
+}
+
+// An optional matrix with contiguous rows: its address and row stride.
+struct Rows {
+  void* p = nullptr;
+  int64_t ld = 0;
+  Rows(PyObject* o, const char* name, at::ScalarType dtype, int64_t T, int64_t cols, at::Device dev) {
+    if (o == Py_None) return;
+    const at::Tensor& t = tensor(o, name);
+    ld = rows(t, name, dtype, T, cols, dev);
+    p = t.data_ptr();
+  }
+};
+
+const int32_t* table(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::Device dev) {
+  whole(t, name, at::kInt, shape, dev);
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// An output: the given matrix [T, cols], or a new one.
+at::Tensor output(PyObject* o, const Where& at, at::ScalarType dtype, int64_t T, int64_t cols, int64_t& ld) {
+  ld = cols;
+  if (o == Py_None) return at.empty({T, cols}, dtype);
+  const at::Tensor& t = tensor(o, "out");
+  ld = rows(t, "out", dtype, T, cols, at.dev);
+  return t;
+}
+
+PyObject* tuple_of(std::initializer_list<std::optional<at::Tensor>> parts) {
+  PyObject* out = PyTuple_New((Py_ssize_t)parts.size());
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const auto& t : parts) PyTuple_SET_ITEM(out, i++, wrap(t));
+  return out;
+}
+
+// x, topk_ids, E, experts_start, align, out | None, stream | None
+PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 7)) return nullptr;
+  const at::Tensor &x = tensor(a[0], "x"), &ids = tensor(a[1], "topk_ids");
+  const int E = small_number(a[2], "E"), start = small_number(a[3], "experts_start"), align = small_number(a[4], "align");
+  const std::optional<cudaStream_t> stream = handle(a[6]);
+  need_cuda(x, "x");
+  two_dims(x, "x");
+  two_dims(ids, "topk_ids");
+  const Where at(x, stream);
+  const int type = type_of(x, "x", true);
+  const int64_t T = x.size(0), H = x.size(1), k = ids.size(1);
+  const int64_t ld_x = rows(x, "x", x.scalar_type(), T, H, at.dev);
+  const int32_t* id = table(ids, "topk_ids", {T, k}, at.dev);
+  TORCH_CHECK_VALUE(k <= INT32_MAX, "topk_ids has too many columns");
+  const int64_t capacity = nvfp4_sort_tokens_capacity(T, E, (int)k, align);
+  int64_t ld = H;
+  at::Tensor out;
+  if (a[5] != Py_None || capacity > 0 || T == 0) out = output(a[5], at, x.scalar_type(), capacity, H, ld);
+  const bool sizes = E >= 1 && E <= 256;  // refused below otherwise
+  Outputs tables(at, 4 * (2 * (sizes ? E : 0) + 1 + capacity + T * k), 4);
+  at::Tensor offsets = tables.empty({sizes ? E + 1 : 1}, at::kInt), counts = tables.empty({sizes ? E : 1}, at::kInt),
+             source = tables.empty({capacity}, at::kInt), inverse = tables.empty({T, k}, at::kInt);
+  auto i32 = [](at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+  const int rc = nvfp4_sort_tokens(x.data_ptr(), ld_x, type, id, start, T, H, E, (int)k, align, capacity,
+                                   out.defined() ? out.data_ptr() : nullptr, ld, i32(offsets), i32(counts), i32(source),
+                                   i32(inverse), at.stream);
+  if (rc != NVFP4_OK) return failed(rc);
+  return tuple_of({out, offsets, counts, source, inverse});
+  END_HANDLE_TH_ERRORS
+}
+
+// drows, inverse, out | None, stream | None
+PyObject* sort_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 4)) return nullptr;
+  const at::Tensor &d = tensor(a[0], "grad_rows"), &inv = tensor(a[1], "the order's inverse");
+  const std::optional<cudaStream_t> stream = handle(a[3]);
+  need_cuda(d, "grad_rows");
+  two_dims(d, "grad_rows");
+  two_dims(inv, "the order's inverse");
+  const Where at(d, stream);
+  const int type = type_of(d, "grad_rows", true);
+  const int64_t T = inv.size(0), k = inv.size(1), H = d.size(1);
+  const int64_t ld_d = rows(d, "grad_rows", d.scalar_type(), d.size(0), H, at.dev);
+  const int32_t* inverse = table(inv, "the order's inverse", {T, k}, at.dev);
+  int64_t ld;
+  const at::Tensor out = output(a[2], at, d.scalar_type(), T, H, ld);
+  const int rc = nvfp4_sort_tokens_grad(d.data_ptr(), ld_d, type, inverse, T, H, (int)k, out.data_ptr(), ld, at.stream);
+  return rc == NVFP4_OK ? THPVariable_Wrap(out) : failed(rc);
+  END_HANDLE_TH_ERRORS
+}
+
+// rows, weights, inverse, residual | None, out | None, stream | None
+PyObject* combine_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 6)) return nullptr;
+  const at::Tensor &r = tensor(a[0], "rows"), &w = tensor(a[1], "weights"), &inv = tensor(a[2], "the order's inverse");
+  const std::optional<cudaStream_t> stream = handle(a[5]);
+  need_cuda(r, "rows");
+  two_dims(r, "rows");
+  two_dims(inv, "the order's inverse");
+  const Where at(r, stream);
+  const int type = type_of(r, "rows", true);
+  const int64_t T = inv.size(0), k = inv.size(1), H = r.size(1);
+  const int64_t ld_r = rows(r, "rows", r.scalar_type(), r.size(0), H, at.dev);
+  const int32_t* inverse = table(inv, "the order's inverse", {T, k}, at.dev);
+  whole(w, "weights", at::kFloat, {T, k}, at.dev);
+  const Rows res(a[3], "residual", r.scalar_type(), T, H, at.dev);
+  int64_t ld;
+  const at::Tensor out = output(a[4], at, r.scalar_type(), T, H, ld);
+  const int rc = nvfp4_combine_tokens(r.data_ptr(), ld_r, type, static_cast<const float*>(w.data_ptr()), inverse,
+                                      res.p, res.ld, T, H, (int)k, out.data_ptr(), ld, at.stream);
+  return rc == NVFP4_OK ? THPVariable_Wrap(out) : failed(rc);
+  END_HANDLE_TH_ERRORS
+}
+
+// dout, rows, weights, offsets, counts, inverse, align, out | None, stream | None
+PyObject* combine_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 9)) return nullptr;
+  const at::Tensor &d = tensor(a[0], "grad_out"), &r = tensor(a[1], "rows"), &w = tensor(a[2], "weights"),
+                   &off = tensor(a[3], "the order's offsets"), &cnt = tensor(a[4], "the order's counts"),
+                   &inv = tensor(a[5], "the order's inverse");
+  const int align = small_number(a[6], "align");
+  const std::optional<cudaStream_t> stream = handle(a[8]);
+  need_cuda(d, "grad_out");
+  two_dims(d, "grad_out");
+  two_dims(r, "rows");
+  two_dims(inv, "the order's inverse");
+  const Where at(d, stream);
+  const int type = type_of(d, "grad_out", true);
+  const int64_t T = inv.size(0), k = inv.size(1), H = d.size(1), E = cnt.numel(), R = r.size(0);
+  const int64_t ld_d = rows(d, "grad_out", d.scalar_type(), T, H, at.dev);
+  const int64_t ld_r = rows(r, "rows", d.scalar_type(), R, H, at.dev);
+  whole(w, "weights", at::kFloat, {T, k}, at.dev);
+  const int32_t *inverse = table(inv, "the order's inverse", {T, k}, at.dev),
+                *counts = table(cnt, "the order's counts", {E}, at.dev),
+                *offsets = table(off, "the order's offsets", {E + 1}, at.dev);
+  int64_t ld;
+  const at::Tensor out = output(a[7], at, d.scalar_type(), R, H, ld);
+  at::Tensor dw = at.empty({T, k}, at::kFloat);
+  const int rc = nvfp4_combine_tokens_grad(d.data_ptr(), ld_d, r.data_ptr(), ld_r, type,
+                                           static_cast<const float*>(w.data_ptr()), offsets, counts, inverse, T, H,
+                                           (int)E, (int)k, align, out.data_ptr(), ld,
+                                           static_cast<float*>(dw.data_ptr()), at.stream);
+  if (rc != NVFP4_OK) return failed(rc);
+  return tuple_of({out, dw});
+  END_HANDLE_TH_ERRORS
+}
+
+// What the linear and its gradient share: sizes, activation (a number) with its
+// limits, and (offsets, counts) of the experts or None.
+struct Shape {
+  nvfp4_linear_shape s = {};
+  int64_t wide, groups;
+  Shape(const at::Tensor& x, const at::Tensor& w, int64_t N, PyObject* act, PyObject* gate, PyObject* up,
+        PyObject* order, at::Device dev) {
+    s.M = x.size(0);
+    s.K = x.size(1);
+    s.type = type_of(x, "x", false);
+    s.activation = small_number(act, "activation");
+    const double gl = PyFloat_AsDouble(gate), ul = PyFloat_AsDouble(up);
+    if (PyErr_Occurred()) throw python_error();
+    s.gate_limit = (float)gl;
+    s.up_limit = (float)ul;
+    const bool experts = order != Py_None;
+    TORCH_CHECK_VALUE(w.dim() == (experts ? 3 : 2), "w must have ", experts ? "three" : "two", " dimensions, not ", w.dim());
+    wide = w.size(experts);
+    groups = experts ? w.size(0) : 0;
+    const bool pairs = s.activation == NVFP4_ACT_SWIGLU;
+    TORCH_CHECK_VALUE(!pairs || wide % 2 == 0, "w needs a gate half and an up half, not ", wide, " rows");
+    s.N = pairs ? wide / 2 : wide;
+    TORCH_CHECK_VALUE(N < 0 || N == s.N, "the gradient has ", N, " columns, the output ", s.N);
+    if (!experts) {
+      whole(w, "w", x.scalar_type(), {wide, s.K}, dev);
+      return;
+    }
+    TORCH_CHECK_VALUE(groups >= 1 && groups <= 256, "1 to 256 experts, not ", groups);
+    whole(w, "w", x.scalar_type(), {groups, wide, s.K}, dev);
+    TORCH_CHECK_VALUE(PyTuple_Check(order) && PyTuple_GET_SIZE(order) == 2, "offsets and counts expected");
+    s.groups = (int)groups;
+    s.offsets = table(tensor(PyTuple_GET_ITEM(order, 0), "the order's offsets"), "the order's offsets", {groups + 1}, dev);
+    s.counts = table(tensor(PyTuple_GET_ITEM(order, 1), "the order's counts"), "the order's counts", {groups}, dev);
+  }
+};
+
+// x, w, (offsets, counts) | None, bias | None, activation, gate_limit, up_limit, residual | None, f32, preact,
+// out | None, stream | None -> (out, preact | None)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 12)) return nullptr;
+  const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
+  const bool f32 = truth(a[8]), keep = truth(a[9]);
+  const std::optional<cudaStream_t> stream = handle(a[11]);
+  need_cuda(x, "x");
+  two_dims(x, "x");
+  const Where at(x, stream);
+  const Shape sh(x, w, -1, a[4], a[5], a[6], a[2], at.dev);
+  const int64_t M = sh.s.M, ld_x = rows(x, "x", x.scalar_type(), M, sh.s.K, at.dev);
+  const void* bias = nullptr;
+  int bias_type = sh.s.type;
+  if (a[3] != Py_None) {
+    const at::Tensor& b = tensor(a[3], "bias");
+    const bool wide_bias = b.scalar_type() == at::kFloat;
+    const at::ScalarType dtype = wide_bias ? at::kFloat : x.scalar_type();
+    if (sh.groups)
+      whole(b, "bias", dtype, {sh.groups, sh.wide}, at.dev);
+    else
+      whole(b, "bias", dtype, {sh.wide}, at.dev);
+    bias = b.data_ptr();
+    if (wide_bias) bias_type = NVFP4_F32;
+  }
+  const Rows res(a[7], "residual", x.scalar_type(), M, sh.s.N, at.dev);
+  int64_t ld;
+  const at::Tensor out = output(a[10], at, f32 ? at::kFloat : x.scalar_type(), M, sh.s.N, ld);
+  std::optional<at::Tensor> z;
+  if (keep) z = at.empty({M, sh.wide}, x.scalar_type());
+  const int rc = nvfp4_linear(&sh.s, x.data_ptr(), ld_x, w.data_ptr(), bias, bias_type, res.p, res.ld,
+                              z ? z->data_ptr() : nullptr, out.data_ptr(), ld, f32 ? NVFP4_F32 : sh.s.type, at.stream);
+  if (rc != NVFP4_OK) return failed(rc);
+  return tuple_of({out, z});
+  END_HANDLE_TH_ERRORS
+}
+
+// dy, x, w, (offsets, counts) | None, preact | None, activation, gate_limit, up_limit, bias, inputs, weights,
+// out | None, stream | None -> (dx, dw, dbias), None where not asked for
+PyObject* linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 13)) return nullptr;
+  const at::Tensor &dy = tensor(a[0], "grad"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
+  const bool bias = truth(a[8]), inputs = truth(a[9]), weights = truth(a[10]);
+  const std::optional<cudaStream_t> stream = handle(a[12]);
+  need_cuda(x, "x");
+  two_dims(x, "x");
+  two_dims(dy, "grad");
+  const Where at(x, stream);
+  const Shape sh(x, w, dy.size(1), a[5], a[6], a[7], a[3], at.dev);
+  const int64_t M = sh.s.M, ld_x = rows(x, "x", x.scalar_type(), M, sh.s.K, at.dev);
+  const int64_t ld_dy = rows(dy, "grad", x.scalar_type(), M, sh.s.N, at.dev);
+  const void* z = nullptr;
+  if (sh.s.activation != NVFP4_ACT_NONE) {
+    TORCH_CHECK_VALUE(a[4] != Py_None, "the gradient of an activation needs preact");
+    const at::Tensor& t = tensor(a[4], "preact");
+    whole(t, "preact", x.scalar_type(), {M, sh.wide}, at.dev);
+    z = t.data_ptr();
+  }
+  TORCH_CHECK_VALUE(inputs || a[11] == Py_None, "out is for the gradient of x");
+  std::optional<at::Tensor> dx, dw, db;
+  int64_t ld_dx = 0;
+  if (inputs) dx = output(a[11], at, x.scalar_type(), M, sh.s.K, ld_dx);
+  if (weights) dw = sh.groups ? at.empty({sh.groups, sh.wide, sh.s.K}, x.scalar_type())
+                              : at.empty({sh.wide, sh.s.K}, x.scalar_type());
+  if (bias) db = sh.groups ? at.empty({sh.groups, sh.wide}, at::kFloat) : at.empty({sh.wide}, at::kFloat);
+  const int64_t bytes = (int64_t)nvfp4_linear_grad_workspace_size(&sh.s, inputs || weights, bias);
+  at::Tensor ws;  // lives until the call is enqueued; its memory is reused in the stream's order
+  if (bytes) ws = at.empty({bytes}, at::kByte);
+  const int rc = nvfp4_linear_grad(&sh.s, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, w.data_ptr(), z,
+                                   dx ? dx->data_ptr() : nullptr, ld_dx, dw ? dw->data_ptr() : nullptr,
+                                   db ? static_cast<float*>(db->data_ptr()) : nullptr,
+                                   bytes ? ws.data_ptr() : nullptr, (size_t)bytes, at.stream);
+  if (rc != NVFP4_OK) return failed(rc);
+  return tuple_of({dx, dw, db});
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XDECREF(g_error);
@@ -293,8 +582,9 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 }
 
 #define CALL(name) {#name, (PyCFunction)(void*)name, METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {CALL(add_rms_norm_fp8), CALL(fp8_linear), CALL(moe_few_tokens),
-                           {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {CALL(add_rms_norm_fp8), CALL(fp8_linear), CALL(moe_few_tokens), CALL(sort_tokens),
+                           CALL(sort_tokens_grad), CALL(combine_tokens), CALL(combine_tokens_grad), CALL(linear),
+                           CALL(linear_grad), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr,
                         nullptr};
 

@@ -1,0 +1,347 @@
+"""The linear with bias, activation and residual, its expert form and their
+gradients against 64 bits."""
+import math
+
+import pytest
+
+import expert_ops_reference as R
+
+pytestmark = pytest.mark.gpu
+
+INF = math.inf
+ACTS = [None, "relu", "silu", "gelu", "gelu_tanh", "swiglu"]
+
+
+def _randn(g, *shape):
+    import torch
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _inputs(M, N, K, dtype, act, bias, residual, seed=0, pad=8, experts=None):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = getattr(torch, dtype)
+    wide = 2 * N if act == "swiglu" else N
+    lead = () if experts is None else (experts,)
+    x = _randn(g, M, K + pad).to(t)[:, :K]
+    w = (_randn(g, *lead, wide, K) / math.sqrt(K)).to(t)
+    b = None if bias is None else _randn(g, *lead, wide).to(t if bias == "same" else torch.float32)
+    res = _randn(g, M, N + pad).to(t)[:, :N] if residual else None
+    return x, w, b, res
+
+
+def _check(x, w, b, res, act, limits, out_dtype, out, z=None):
+    zr, zt, yr, yt = R.linear(x, w, b, act, res, limits, out_dtype)
+    R.check(out, yr, yt)
+    if z is not None:
+        R.check(z, zr, R.rounded(zr, zt, z.dtype))
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 31, 64, 127, 128, 129, 300])
+@pytest.mark.parametrize("N,K", [(8, 8), (48, 4096), (264, 400), (1000, 1288)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_linear_plain(M, N, K, dtype):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, w, _, _ = _inputs(M, N, K, dtype, None, None, False, seed=M)
+    for out_dtype in (x.dtype, torch.float32):
+        out = torch.full((M, N), float("nan"), dtype=out_dtype, device="cuda")
+        assert api.linear(x, w, out=out).data_ptr() == out.data_ptr()
+        _check(x, w, None, None, None, (INF, INF), out_dtype, out)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 40, 264), (6, 136, 1032), (70, 72, 2056), (333, 264, 520), (1500, 1160, 328)])
+@pytest.mark.parametrize("dtype,bias,residual,f32", [("bfloat16", "same", True, False), ("float16", "f32", False, True),
+                                                      ("float16", None, True, False), ("bfloat16", "f32", True, True)])
+def test_linear_epilogue(M, N, K, act, dtype, bias, residual, f32):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, w, b, res = _inputs(M, N, K, dtype, act, bias, residual, seed=N)
+    limits = (1.5, 0.75) if act == "swiglu" and bias else (INF, INF)
+    out_dtype = torch.float32 if f32 else x.dtype
+    out, z = api.linear(x, w, b, act, res, *limits, out_dtype=out_dtype, preact=True)
+    _check(x, w, b, res, act, limits, out_dtype, out, z)
+    assert torch.equal(out, api.linear(x, w, b, act, res, *limits, out_dtype=out_dtype))
+
+
+@pytest.mark.parametrize("M,N,K", [(20, 136, 66000), (3, 8, 131072), (128, 8200, 200), (2048, 2304, 1032),
+                                   (4100, 520, 136)])
+def test_linear_larger(M, N, K):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, w, b, res = _inputs(M, N, K, "bfloat16", None, "same", True, seed=1)
+    out = api.linear(x, w, b, residual=res, out_dtype=torch.float32)
+    _check(x, w, b, res, None, (INF, INF), torch.float32, out)
+    assert torch.equal(out, api.linear(x, w, b, residual=res, out_dtype=torch.float32))
+
+
+def test_rows_depend_on_themselves_alone_and_extremes():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    for M in (8, 200):
+        x, w, b, _ = _inputs(M, 72, 264, "bfloat16", "silu", "same", False)
+        want = api.linear(x, w, b, "silu")
+        x[3] = float("nan")
+        x[5, 0] = float("inf")
+        got = api.linear(x, w, b, "silu")
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[3] = keep[5] = False
+        assert torch.equal(got[keep], want[keep]) and got[3].isnan().all() and not got[5].isfinite().all()
+    # far arguments of the activations, through an identity product
+    v = torch.tensor([-3e38, -1e4, -200, -89, -20, 0, 20, 89, 200, 1e4, 3e38, float("inf"), -float("inf"),
+                      float("nan"), -0.0, 1e-30], device="cuda")
+    x = torch.zeros(16, 16, device="cuda")
+    x[:, 0] = v
+    w = torch.zeros(16, 16, device="cuda")
+    w[:8, 0] = 1
+    for rows in (16, 8):
+        for act in ACTS[1:5]:
+            got = api.linear(x[:rows].bfloat16(), w.bfloat16()[:8], activation=act, out_dtype=torch.float32)[:, 0]
+            z = x[:rows, 0].bfloat16().double()
+            ref = torch.where(z.isinf() & (z < 0), 0.0 * z if act != "relu" else 0.0, R.act(z, act))
+            fin = z.isfinite()
+            R.check(got[fin], ref[fin], 16 * R.U32 * (1 + z[fin].abs()))
+            assert got[z.isnan()].isnan().all() and (got[z == INF] == INF).all()
+
+
+def test_residual_in_place_and_strided_output():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    for M in (5, 150):
+        x, w, b, res = _inputs(M, 136, 264, "float16", "gelu", "same", True)
+        want = api.linear(x, w, b, "gelu", res)
+        buf = torch.full((M + 2, 160), float("nan"), dtype=x.dtype, device="cuda")
+        out = buf[1:M + 1, 8:144]
+        out.copy_(res)
+        api.linear(x, w, b, "gelu", out, out=out)
+        assert torch.equal(out, want)
+        buf[1:M + 1, 8:144] = float("nan")
+        assert buf.isnan().all()
+
+
+# ------------------------------------------------------------------ gradient
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 40, 264), (9, 264, 72), (130, 136, 1032), (700, 72, 136), (1500, 1160, 328)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_linear_grad(M, N, K, act, dtype):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x, w, _, _ = _inputs(M, N, K, dtype, act, None, False, seed=N)
+    dy = _randn(g, M, N + 8).to(x.dtype)[:, :N]
+    z = None if act is None else (2 * _randn(g, M, w.shape[0])).to(x.dtype)
+    limits = (1.5, 0.75) if act == "swiglu" else (INF, INF)
+    dx, dw, db = api.linear_grad(dy, x, w, z, act, *limits, bias=True)
+    (rx, tx), (rw, tw), (rb, tb) = R.linear_grad(dy, x, w, z, act, limits, x.dtype)
+    R.check(db, rb, tb)
+    R.check(dx, rx, tx)
+    R.check(dw, rw, tw)
+    only = api.linear_grad(dy, x, w, z, act, *limits, weights=False)
+    assert torch.equal(only[0], dx) and only[1] is None and only[2] is None
+    only = api.linear_grad(dy, x, w, z, act, *limits, inputs=False)
+    assert only[0] is None and torch.equal(only[1], dw)
+    only = api.linear_grad(dy, x, w, z, act, *limits, inputs=False, weights=False, bias=True)
+    assert torch.equal(only[2], db)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_grad_against_differences(act):
+    """Central differences of the FP64 definition: off by h^2 of the third derivative."""
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, w, b, _ = _inputs(24, 16, 40, "bfloat16", act, "same", False, seed=5)
+    dy = _randn(g, 24, 16).to(x.dtype)
+    limits = (1.0, 1.0)
+    _, z = api.linear(x, w, b, act, None, *limits, preact=True)
+    dx, dw, db = api.linear_grad(dy, x, w, z, act, *limits, bias=True)
+    # the gradient is taken at the rounded z: the constant that makes it the definition's z
+    shift = z.double() - x.double() @ w.double().T
+
+    def loss(x, w, extra):
+        return (dy.double() * R.act(x @ w.T + shift + extra, act, limits)).sum()
+
+    h = 1e-6
+    X, W, Z = x.double(), w.double(), torch.zeros(w.shape[0], dtype=torch.float64, device="cuda")
+    (_, tx), (_, tw), (_, tb) = R.linear_grad(dy, x, w, z, act, limits, x.dtype)
+    near = {"relu": (0.0,), "swiglu": (1.0, -1.0)}.get(act, ())  # no difference across a kink
+    assert all(((z.double() - v).abs() > 1e-4).all() for v in near) or act in ("relu", "swiglu")
+    for k in range(12):
+        for at, (which, got, tol) in ((divmod(7 * k, 40), (0, dx, tx)), ((k % w.shape[0], 3 * k % 40), (1, dw, tw)),
+                                      ((k % w.shape[0],), (2, db, tb))):
+            args = [X.clone(), W.clone(), Z.clone()]
+            args[which][at] += h
+            up = loss(*args)
+            args[which][at] -= 2 * h
+            diff = (up - loss(*args)) / (2 * h)
+            assert abs(float(got[at]) - float(diff)) <= float(tol[at]) + 1e-4, (act, which, at)
+
+
+def test_linear_no_rows():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, w, b, _ = _inputs(0, 16, 24, "bfloat16", "silu", "same", False)
+    out, z = api.linear(x, w, b, "silu", preact=True)
+    assert out.shape == (0, 16) and z.shape == (0, 16)
+    dx, dw, db = api.linear_grad(out, x, w, z, "silu", bias=True)
+    assert dx.shape == (0, 24) and not dw.any() and not db.any()
+
+
+# ------------------------------------------------------------------ experts
+
+
+def _experts(T, k, E, model, K, N, dtype, act, bias, seed=0, align=1, skew=False):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    g = torch.Generator().manual_seed(seed)
+    logits = torch.randn(T, model, generator=g) + (4.0 * torch.randn(1, model, generator=g) if skew else 0)
+    ids = logits.topk(k, dim=1).indices.to(torch.int32)
+    t = getattr(torch, dtype)
+    x = torch.zeros(T, 8, dtype=t, device="cuda")
+    _, order = api.sort_tokens(x, ids.cuda(), E, (model - E) // 2, align)
+    n = order.source.numel()
+    rows, w, b, res = _inputs(n, N, K, dtype, act, bias, True, seed=seed, experts=E)
+    rows = torch.where((order.source >= 0)[:, None], rows, torch.full_like(rows, float("nan")))
+    return rows, w, b, res, order
+
+
+EXPERTS = [(1, 6, 32, 32, 264, 136), (9, 2, 5, 10, 72, 264), (40, 4, 12, 24, 520, 72), (300, 3, 7, 7, 264, 200),
+           (1500, 2, 5, 5, 136, 1032), (700, 8, 100, 130, 72, 40)]
+
+
+def _slices(order):
+    ends, counts = order.offsets.tolist(), order.counts.tolist()
+    return [slice(ends[e], ends[e] + counts[e]) for e in range(len(counts))]
+
+
+@pytest.mark.parametrize("T,k,E,model,K,N", EXPERTS)
+@pytest.mark.parametrize("act,dtype,bias,align,skew", [(None, "bfloat16", None, 1, False),
+                                                       ("swiglu", "bfloat16", "f32", 1, True),
+                                                       ("gelu", "float16", "same", 16, True),
+                                                       ("swiglu", "float16", "same", 128, False)])
+def test_expert_linear(T, k, E, model, K, N, act, dtype, bias, align, skew):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    rows, w, b, res, order = _experts(T, k, E, model, K, N, dtype, act, bias, seed=T, align=align, skew=skew)
+    limits = (1.5, 0.75) if act == "swiglu" else (INF, INF)
+    for residual in (None, res):
+        out = torch.full((rows.shape[0], N), 7.0, dtype=rows.dtype, device="cuda")
+        got, z = api.expert_linear(rows, w, order, b, act, residual, *limits, preact=True, out=out)
+        assert got.data_ptr() == out.data_ptr()
+        used = torch.zeros(rows.shape[0], dtype=torch.bool, device="cuda")
+        for e, at in enumerate(_slices(order)):
+            used[at] = True
+            _check(rows[at], w[e], None if b is None else b[e], None if residual is None else residual[at], act, limits,
+                   out.dtype, out[at], z[at])
+        assert (out[~used] == 7).all()
+
+
+@pytest.mark.parametrize("T,k,E,model,K,N", EXPERTS)
+@pytest.mark.parametrize("act,dtype,align,skew", [(None, "bfloat16", 1, True), ("swiglu", "bfloat16", 1, False),
+                                                  ("silu", "float16", 16, True)])
+def test_expert_linear_grad(T, k, E, model, K, N, act, dtype, align, skew):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    rows, w, _, _, order = _experts(T, k, E, model, K, N, dtype, act, None, seed=T, align=align, skew=skew)
+    n = rows.shape[0]
+    g = torch.Generator(device="cuda").manual_seed(T)
+    nan = lambda t: torch.where((order.source >= 0)[:, None], t, torch.full_like(t, float("nan")))
+    dy = nan(_randn(g, n, N).to(rows.dtype))
+    z = None if act is None else nan((2 * _randn(g, n, w.shape[1])).to(rows.dtype))
+    limits = (1.5, 0.75) if act == "swiglu" else (INF, INF)
+    out = torch.full((n, K), 7.0, dtype=rows.dtype, device="cuda")
+    dx, dw, db = api.expert_linear_grad(dy, rows, w, order, z, act, *limits, bias=True, out=out)
+    used = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for e, at in enumerate(_slices(order)):
+        used[at] = True
+        (rx, tx), (rw, tw), (rb, tb) = R.linear_grad(dy[at], rows[at], w[e], None if z is None else z[at], act, limits,
+                                                     rows.dtype)
+        R.check(dx[at], rx, tx)
+        R.check(dw[e], rw, tw)
+        R.check(db[e], rb, tb)
+        if at.start == at.stop:
+            assert not dw[e].any() and not db[e].any()
+    assert (dx[~used] == 7).all()
+
+
+def test_expert_linear_without_rows():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    for T in (4, 700):
+        ids = torch.full((T, 2), 99, dtype=torch.int32, device="cuda")
+        rows, order = api.sort_tokens(torch.ones(T, 16, dtype=torch.bfloat16, device="cuda"), ids, 3)
+        w = torch.ones(3, 8, 16, dtype=torch.bfloat16, device="cuda")
+        out = torch.full((2 * T, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+        api.expert_linear(rows, w, order, out=out)
+        assert (out == 7).all()
+        dx = torch.full((2 * T, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        _, dw, db = api.expert_linear_grad(out, rows, w, order, bias=True, out=dx)
+        assert (dx == 7).all() and not dw.any() and not db.any()
+
+
+def test_refusals_of_the_python_calls():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api, binding
+    x, w, b, res = _inputs(12, 16, 24, "bfloat16", None, "same", True)
+    rows, order = api.sort_tokens(x, torch.zeros(12, 1, dtype=torch.int32, device="cuda"), 2)
+    we = torch.stack((w, w))
+    for call in (lambda: api.linear(x, w.half()), lambda: api.linear(x.float(), w.float()), lambda: api.linear(x, w.cpu()),
+                 lambda: api.linear(x, w[:, :16]), lambda: api.linear(x, we), lambda: api.linear(x, w, b[:8]),
+                 lambda: api.linear(x, w, b.half()), lambda: api.linear(x, w, residual=res[:4]),
+                 lambda: api.linear(x, w, residual=res.float()), lambda: api.linear(x, w, out=res[:4]),
+                 lambda: api.linear(x[0], w), lambda: api.linear(x.t(), w), lambda: api.linear(x, w[:15], activation="swiglu"),
+                 lambda: api.linear(x, w, out_dtype=torch.float16),
+                 lambda: api.linear_grad(res, x, w, activation="silu"), lambda: api.linear_grad(res[:4], x, w),
+                 lambda: api.linear_grad(res[:, :8], x, w), lambda: api.linear_grad(res, x, w, inputs=False, out=x),
+                 lambda: api.expert_linear(rows, w, order), lambda: api.expert_linear(rows, we[:1], order),
+                 lambda: api.expert_linear(rows, we, order, bias=b)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: api.linear(x[:, :20], w[:, :20].contiguous()), lambda: api.linear(x, w[:12].contiguous()),
+                 lambda: api.linear(x, w, activation="swiglu", gate_limit=-1.0)):
+        with pytest.raises(binding.Nvfp4Error):
+            call()
+
+
+def test_other_stream_and_graph():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, w, b, res = _inputs(200, 264, 520, "bfloat16", "silu", "same", True)
+    want, z = api.linear(x, w, b, "silu", res, preact=True)
+    grads = api.linear_grad(res, x, w, z, "silu", bias=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got, zs = api.linear(x, w, b, "silu", res, preact=True, stream=s)
+    more = api.linear_grad(res, x, w, zs, "silu", bias=True, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(grads, more))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, z = api.linear(x, w, b, "silu", res, preact=True)
+        more = api.linear_grad(res, x, w, z, "silu", bias=True)
+    x.mul_(0.5)
+    for _ in range(2):
+        g.replay()
+    want, z = api.linear(x, w, b, "silu", res, preact=True)
+    assert torch.equal(out, want)
+    assert all(torch.equal(a, b) for a, b in zip(more, api.linear_grad(res, x, w, z, "silu", bias=True)))
+
+
+def test_a_stalled_product_is_reported():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api, binding
+    x, w, _, _ = _inputs(300, 136, 520, "bfloat16", None, None, False)
+    want = api.linear(x, w)
+    torch.cuda.synchronize()
+    assert binding.nvfp4_device_status(reset=True) == 0
+    binding.nvfp4_moe_set_debug_stall(50)
+    try:
+        api.linear(x, w)
+        torch.cuda.synchronize()
+    finally:
+        binding.nvfp4_moe_set_debug_stall(0)
+    assert binding.nvfp4_device_status(reset=True) == binding.NVFP4_ERR_DEVICE_TIMEOUT
+    assert torch.equal(api.linear(x, w), want) and binding.nvfp4_device_status() == 0
