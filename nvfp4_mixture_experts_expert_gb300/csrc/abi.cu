@@ -1369,10 +1369,18 @@ static int check_linear(const nvfp4_linear_shape* s) {
   return NVFP4_OK;
 }
 
+// Whether every 32-byte piece of a matrix's rows is aligned to 32 bytes.
+static int whole_sectors(const void* p, int64_t ld, int size) {
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld * size % 32 == 0;
+}
+
 // Plan, maps and launch of one product (args filled in but for these).
 static int run_linear_gemm(LinearArgs& t, const nvfp4_linear_shape* s, const void* a, int64_t a_rows, int64_t a_cols,
                            int64_t ld_a, const void* b, int64_t b_depth, int64_t b_rows, int64_t b_cols, int64_t ld_b,
                            const DeviceInfo* dev, void* stream) {
+  t.ep.out_v8 = whole_sectors(t.ep.out, t.ep.ld_out, t.ep.out_type == NVFP4_F32 ? 4 : 2);
+  t.ep.residual_v8 = whole_sectors(t.ep.residual, t.ep.ld_residual, 2);
+  t.ep.preact_v8 = whole_sectors(t.ep.preact, t.ep.ld_preact, 2) && t.ep.N % 16 == 0;
   t.G = s->groups ? s->groups : 1;
   t.offsets = s->groups ? s->offsets : nullptr;
   t.counts = s->groups ? s->counts : nullptr;

@@ -363,6 +363,7 @@ struct LinearEpilogue {
   int N, wide;           // output columns; rows of w (twice N for SwiGLU)
   int type, out_type, bias_type, act;
   float gate_limit, up_limit;
+  int residual_v8, preact_v8, out_v8;  // their rows' 16-column pieces lie on multiples of 32 bytes
 };
 struct LinearArgs {
   CUtensorMap map_a;  // see linear_gemm.cu
@@ -376,7 +377,7 @@ struct LinearArgs {
   int by_k;      // the groups' rows are the contraction (weight gradients)
   int second;    // rows of B from the first to the second half of a tile
   int stall;     // failure-detection check: only a tile's first K-block is loaded
-  int bn, split;               // set by linear_gemm_plan
+  int bn, pair, split;         // columns of a tile, CTA pairs, CTAs that share a tile's K: set by linear_gemm_plan
   int m_tiles, n_tiles, tiles; // set by the launch (tiles: where the host knows them)
 };
 cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms);  // from the sizes, groups and activation

@@ -6,6 +6,7 @@
 
 #include "internal.h"
 #include "nvfp4_format.cuh"
+#include "ptx.cuh"
 
 namespace nvfp4 {
 
@@ -26,6 +27,88 @@ __device__ __forceinline__ float activate(int act, float z) {
 __device__ __forceinline__ float at_most(float z, float bound) { return z > bound ? bound : z; }
 __device__ __forceinline__ float at_least(float z, float bound) { return z < bound ? bound : z; }
 
+__device__ __forceinline__ float swiglu(float g, float u, float gate_limit, float up_limit) {
+  return silu(at_most(g, gate_limit)) * at_least(at_most(u, up_limit), -up_limit);
+}
+
+// Two 16-bit values of one word.
+__device__ __forceinline__ void unpack2(int type, uint32_t v, float& a, float& b) {
+  if (type == kTypeBf16) {
+    a = bf16_lo(v), b = bf16_hi(v);
+  } else {
+    const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    a = d.x, b = d.y;
+  }
+}
+__device__ __forceinline__ uint32_t pack2(int type, float a, float b) {
+  if (type == kTypeBf16) return pack_bf16x2(a, b);
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// kEpilogueColumns consecutive values of a row, of which `left` exist (a multiple of
+// 8); v8: the row's addresses are multiples of 32 bytes, and whole sectors are moved.
+constexpr int kEpilogueColumns = 16;
+__device__ __forceinline__ void load_row(const void* p, int64_t at, bool v8, int left, uint32_t (&u)[8]) {
+  const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+  if (v8 && left >= 16) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "l"(q));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = 8 * i < left ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0, 0, 0, 0);
+    u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+  }
+}
+template <int WORDS>
+__device__ __forceinline__ void store_words(uint32_t* q, bool v8, int left, const uint32_t (&u)[WORDS]) {
+  if (v8 && left >= 16) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 8)
+      st_global_v8(q + i, u[i], u[i + 1], u[i + 2], u[i + 3], u[i + 4], u[i + 5], u[i + 6], u[i + 7]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; i += 4)
+    if (i * 16 < left * WORDS) *reinterpret_cast<uint4*>(q + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+}
+__device__ __forceinline__ void store_row(void* p, int64_t at, int type, bool v8, int left, const float (&f)[16]) {
+  if (type == kTypeF32) {
+    uint32_t u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(f[i]);
+    store_words(reinterpret_cast<uint32_t*>(static_cast<float*>(p) + at), v8, left, u);
+    return;
+  }
+  uint32_t u[8];
+  if (type == kTypeBf16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = pack2(kTypeBf16, f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = pack2(kTypeF16, f[2 * i], f[2 * i + 1]);
+  }
+  store_words(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + at), v8, left, u);
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void activate_as(float (&z)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] = activate(ACT, z[i]);
+}
+template <int N>
+__device__ __forceinline__ void activate_all(int act, float (&z)[N]) {
+  switch (act) {
+    case kActRelu: return activate_as<kActRelu>(z);
+    case kActSilu: return activate_as<kActSilu>(z);
+    case kActGelu: return activate_as<kActGelu>(z);
+    case kActGeluTanh: return activate_as<kActGeluTanh>(z);
+  }
+}
+
 // Eight consecutive values of a 16-bit or FP32 row.
 __device__ __forceinline__ void load8(const void* p, int64_t at, int type, float (&f)[8]) {
   if (type == kTypeF32) {
@@ -37,14 +120,7 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int type, float
   const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (type == kTypeBf16) {
-      f[2 * i] = bf16_lo(u[i]), f[2 * i + 1] = bf16_hi(u[i]);
-    } else {
-      const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      f[2 * i] = d.x, f[2 * i + 1] = d.y;
-    }
-  }
+  for (int i = 0; i < 4; ++i) unpack2(type, u[i], f[2 * i], f[2 * i + 1]);
 }
 __device__ __forceinline__ void store8(void* p, int64_t at, int type, const float (&f)[8]) {
   if (type == kTypeF32) {
@@ -55,14 +131,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int type, const floa
   }
   uint32_t u[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (type == kTypeBf16) {
-      u[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    } else {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
+  for (int i = 0; i < 4; ++i) u[i] = pack2(type, f[2 * i], f[2 * i + 1]);
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -91,11 +160,9 @@ __device__ __forceinline__ void finish8(const LinearEpilogue& p, int64_t row, in
   }
   if (p.act == kActSwiglu) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      z[i] = silu(at_most(z[i], p.gate_limit)) * at_least(at_most(u[i], p.up_limit), -p.up_limit);
-  } else if (p.act != kActNone) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = activate(p.act, z[i]);
+    for (int i = 0; i < 8; ++i) z[i] = swiglu(z[i], u[i], p.gate_limit, p.up_limit);
+  } else {
+    activate_all(p.act, z);
   }
   if (p.residual) {
     float r[8];
