@@ -1389,7 +1389,7 @@ static int run_linear_gemm(LinearArgs& t, const nvfp4_linear_shape* s, const voi
   cudaError_t e = linear_gemm_plan(t, dev->sms);
   if (e != cudaSuccess) return cuda_fail(e, "linear plan");
   if (int rc = make_half_map(&t.map_a, a, 1, a_rows, a_cols, ld_a, t.a_mn ? 64 : 128, s->type, false)) return rc;
-  if (int rc = make_half_map(&t.map_b, b, b_depth, b_rows, b_cols, ld_b, t.b_mn ? 64 : t.bn / 2, s->type, true))
+  if (int rc = make_half_map(&t.map_b, b, b_depth, b_rows, b_cols, ld_b, t.b_mn ? 64 : t.pair || t.ep.act == kActSwiglu ? t.bn / 2 : t.bn, s->type, true))
     return rc;
   e = launch_linear_gemm(t, dev->sms, (cudaStream_t)stream);
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "linear launch");

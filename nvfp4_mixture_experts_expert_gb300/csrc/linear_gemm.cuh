@@ -1,0 +1,693 @@
+// 16-bit matrix products on the 5th-generation tensor cores with bias, activation
+// and residual in the epilogue, over one matrix or over groups of rows (see
+// nvfp4_linear, nvfp4_expert_linear and their gradients):
+//
+//   out[m][n] = act(sum_k A[m][k] * B[n][k] + bias[n]) + residual[m][n]
+//
+// The three products of a linear are one kernel; what changes is which dimension
+// of an operand is contiguous in memory, which the tensor core takes as it is:
+//   forward    A = x  [rows][K]        B = w [G][wide][K]     both by their rows
+//   dx         A = dz [rows][wide]     B = w, read along its columns (b_mn)
+//   dw         A = dz, B = x, both read along their columns (a_mn, b_mn); the
+//              rows are the contraction, a group's rows one product (by_k)
+// An operand read by rows lies in the ring as rows of 64 elements (128 bytes,
+// SWIZZLE_128B), one read along columns as chunks of 64 columns x 64 rows.
+//
+// Groups: an expert's rows offsets[g] .. + counts[g] are tiled by themselves, a
+// tile's rows behind the group's last are computed and not stored.  With by_k, rows
+// behind the group's last are set to zero in the ring before the product.
+//
+// Persistent, tiles of 128 x BN, FP32 accumulators in TMEM, two of them, so that a
+// tile's epilogue runs beside the next one's products.  Where a problem has few
+// tiles, K is split over the CTAs of a cluster, which add their sums through shared
+// memory.  10 warps: 0 TMA, 1 MMA issue (and TMEM), 2 to 9 epilogue (a lane quarter
+// and half of the columns each).  Every wait is bounded and reports in the
+// library's status word.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fp8_mma.cuh"
+#include "internal.h"
+#include "linear_epilogue.cuh"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+// Compiled apart (one source file each), so that a kernel holds only the code that it runs.
+enum LinearEpi { kEpiPlain, kEpiActivation, kEpiSwiglu };
+
+namespace linear_gemm {
+
+constexpr int kBM = 128;
+constexpr int kBK = 64;
+constexpr int kEpiWarp0 = 2;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kMaxGroups = 256;
+constexpr int kBiasBytes = 2 * 128 * 4;  // an epilogue warp's: the bias of up to 128 columns, SwiGLU of both halves
+constexpr int kChunkBytes = 64 * 128;       // 64 columns x 64 rows of an operand read along columns
+
+template <int BN, bool PAIR>
+struct Cfg {
+  static constexpr int A_BYTES = kBM * kBK * 2;
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // of B that this CTA holds
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * kBK * 2;
+  static constexpr int STAGES = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 7;
+  static constexpr int UNIT_ROWS = PAIR ? 2 * kBM : kBM;  // of a tile
+  static constexpr int BUFS = 2;
+  static constexpr int TMEM_COLS = BUFS * BN;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kEpiWarps * kBiasBytes +
+                                 8 * (2 * STAGES + 2 * BUFS) + 16 + 4 * (kMaxGroups + 4);
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
+
+// Shared-memory addresses: ring, bias, barriers (full: a stage has landed;
+// empty: its products are done; acc_full, acc_empty: an accumulator), tiles before
+// each group.
+struct Smem {
+  uint32_t stages, bias, full, empty, acc_full, acc_empty;
+  uint32_t* tmem_slot;
+  int* abort_flag;
+  int* first_tile;  // [G + 1], in m-tiles
+};
+
+template <int BN, bool PAIR>
+__device__ __forceinline__ Smem carve(uint8_t* raw) {
+  using C = Cfg<BN, PAIR>;
+  Smem s;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  s.stages = smem_u32(base);
+  s.bias = s.stages + C::STAGES * C::STAGE_BYTES;
+  s.full = s.bias + kEpiWarps * kBiasBytes;
+  s.empty = s.full + 8 * C::STAGES;
+  s.acc_full = s.empty + 8 * C::STAGES;
+  s.acc_empty = s.acc_full + 8 * C::BUFS;
+  s.tmem_slot = reinterpret_cast<uint32_t*>(base + (s.acc_empty + 8 * C::BUFS - s.stages));
+  s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
+  s.first_tile = s.abort_flag + 1;
+  return s;
+}
+
+// This CTA's part of a tile: its group, where its operands start, how many of its
+// rows exist (in a pair's second half none, or less, may), and its contraction (K-blocks kb0 .. kb1 of this CTA; k0: first row with by_k; k_end:
+// length).
+struct Tile {
+  int g, m0, n0, rows, kb0, kb1, k0, k_end;
+  int64_t out_row;
+};
+
+// Walks the tiles of a role in its order; tiles of a group are neighbours, the
+// group's rows run fastest (the CTAs at work share few column tiles of B).
+template <bool SPLIT, bool PAIR, bool SWIGLU>
+struct Walk {
+  static constexpr int UNIT = PAIR ? 2 * kBM : kBM;
+  const LinearArgs& p;
+  const int* first_tile;
+  int it, step, rank, g = 0;
+  int out_cols;  // columns of the output that a tile covers
+  __device__ Walk(const LinearArgs& p, const int* first_tile, int bn)
+      : p(p), first_tile(first_tile), out_cols(SWIGLU ? bn / 2 : bn) {
+    it = SPLIT ? blockIdx.x / p.split : PAIR ? blockIdx.x / 2 : blockIdx.x;
+    rank = SPLIT ? blockIdx.x % p.split : PAIR ? blockIdx.x % 2 : 0;
+    step = SPLIT ? 1 << 30 : PAIR ? gridDim.x / 2 : gridDim.x;
+  }
+  __device__ bool next(Tile& t) {
+    const int m_total = p.by_k ? p.G * p.m_tiles : first_tile[p.G];
+    if (it >= m_total * p.n_tiles) return false;
+    if (p.by_k) {
+      const int per = p.m_tiles * p.n_tiles;
+      g = it / per;
+      const int r = it - g * per, n = r / p.m_tiles;
+      t.m0 = (r - n * p.m_tiles) * UNIT + (PAIR ? rank * kBM : 0);
+      t.n0 = n * out_cols;
+      t.rows = min(kBM, p.M - t.m0);
+      t.out_row = (int64_t)g * p.M + t.m0;
+      t.k0 = p.counts ? p.offsets[g] : 0;
+      t.k_end = p.counts ? p.counts[g] : p.K;
+    } else {
+      while (it >= first_tile[g + 1] * p.n_tiles) ++g;
+      const int mt = first_tile[g + 1] - first_tile[g], r = it - first_tile[g] * p.n_tiles, n = r / mt;
+      const int m = (r - n * mt) * UNIT + (PAIR ? rank * kBM : 0);
+      t.m0 = m + (p.counts ? p.offsets[g] : 0);
+      t.n0 = n * out_cols;
+      t.rows = min(kBM, (p.counts ? p.counts[g] : p.M) - m);
+      t.out_row = t.m0;
+      t.k0 = 0;
+      t.k_end = p.K;
+    }
+    t.g = g;
+    const int kbs = (t.k_end + kBK - 1) / kBK;
+    t.kb0 = SPLIT ? (int)((int64_t)kbs * rank / p.split) : 0;
+    t.kb1 = SPLIT ? (int)((int64_t)kbs * (rank + 1) / p.split) : kbs;
+    it += step;
+    return true;
+  }
+};
+
+// Boxes into this CTA's shared memory.  PAIR: the barrier is the first CTA's (a
+// cluster address), which counts what lands in both.
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    tma_load_2d(dst, map, x, y, bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                         uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// FP32 accumulators, both operands FP16 or both BF16, either read along columns.
+__device__ __forceinline__ uint32_t idesc_f16(int type, int a_mn, int b_mn, int m, int n) {
+  const uint32_t fmt = type == kTypeBf16 ? 1u : 0u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+template <int BN, bool SPLIT, bool PAIR, bool SWIGLU>
+__device__ void load_loop(const LinearArgs& p, const Smem& L) {
+  using C = Cfg<BN, PAIR>;
+  volatile int* abort = L.abort_flag;
+  const int lane = threadIdx.x & 31;
+  const bool leader = elect_one();
+  uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
+  bool ok = true;
+  Walk<SPLIT, PAIR, SWIGLU> walk(p, L.first_tile, BN);
+  const uint32_t full0 = PAIR ? mapa_shared(L.full, 0) : L.full;
+  Tile t;
+  while (ok && !*abort && walk.next(t)) {
+    const int kb1 = p.stall && t.kb1 > t.kb0 ? t.kb0 + 1 : t.kb1;
+    for (int kb = t.kb0; kb < kb1; ++kb) {
+      ok = warp_wait(L.empty + 8 * stage, phase ^ 1u, abort, p.status);
+      if (!ok) break;
+      const uint32_t a = L.stages + stage * C::STAGE_BYTES, b = a + C::A_BYTES, bar = full0 + 8 * stage;
+      const uint32_t now = stage;
+      issued |= 1u << stage;
+      issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (leader) {
+        const int k = t.k0 + kb * kBK;
+        if (!PAIR || walk.rank == 0) mbar_arrive_expect_tx(L.full + 8 * now, (PAIR ? 2 : 1) * C::STAGE_BYTES);
+        if (p.a_mn) {
+#pragma unroll
+          for (int i = 0; i < kBM / 64; ++i) load_box<PAIR>(a + i * kChunkBytes, &p.map_a, t.m0 + 64 * i, k, bar);
+        } else {
+          load_box<PAIR>(a, &p.map_a, k, t.m0, bar);
+        }
+        if (p.b_mn) {
+          const int g = p.by_k ? 0 : t.g, n0 = t.n0 + (PAIR ? walk.rank * C::B_ROWS : 0);
+#pragma unroll
+          for (int i = 0; i < C::B_ROWS / 64; ++i) load_box<PAIR>(b + i * kChunkBytes, &p.map_b, n0 + 64 * i, k, g, bar);
+        } else if (PAIR) {
+          load_box<PAIR>(b, &p.map_b, k, t.n0 + walk.rank * p.second, t.g, bar);
+        } else {
+          load_box<PAIR>(b, &p.map_b, k, t.n0, t.g, bar);
+          if (SWIGLU) load_box<PAIR>(b + BN * kBK, &p.map_b, k, t.n0 + p.second, t.g, bar);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  // The copies land before the warp leaves, also where another role gives up later.
+  // A pair's second CTA, whose barriers are the first's, has them consumed when both
+  // meet at the end, or gives them time.
+  if (PAIR && walk.rank != 0) {
+    if (!ok || *abort) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (lane == 0) {
+    for (int s = 0; s < C::STAGES; ++s)
+      if (issued & (1u << s)) {
+        volatile int no_abort = 0;
+        if (!wait_bounded(L.full + 8 * s, (issued_parity >> s) & 1u, &no_abort, nullptr, kDrainNs)) break;
+      }
+  }
+  __syncwarp();
+}
+
+// Rows `from` .. 15 behind it, up to a multiple of 16, of `chunks` column chunks: zero.
+__device__ __forceinline__ void zero_rows(uint32_t at, int chunks, int from, int lane) {
+  const int to = (from + 15) & ~15, per = (to - from) * 8;  // 16-byte pieces of a chunk
+  for (int i = lane; i < chunks * per; i += 32) {
+    const int c = i / per, r = i - c * per;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * kChunkBytes + from * 128 + r * 16), "r"(0)
+                 : "memory");
+  }
+}
+
+// A group's last K-block with by_k, behind which the next group's rows follow: sets
+// them to zero in this CTA's operands; returns the steps of 16 that count.
+template <int BN>
+__device__ __forceinline__ int end_of_group(uint32_t at, int left, int lane) {
+  zero_rows(at, kBM / 64 + BN / 64, left, lane);
+  fence_proxy_async_smem();
+  __syncwarp();
+  return (left + 15) / 16;
+}
+
+template <int BN, bool SPLIT, bool PAIR, bool SWIGLU>
+__device__ void mma_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
+  using C = Cfg<BN, PAIR>;
+  volatile int* abort = L.abort_flag;
+  const int lane = threadIdx.x & 31;
+  const bool leader = elect_one();
+  const uint32_t idesc = idesc_f16(p.ep.type, p.a_mn, p.b_mn, C::UNIT_ROWS, BN);
+  // by rows: 8-row groups 1024 bytes apart; along columns: the same for 8 of K, 64-column chunks kChunkBytes apart
+  const uint64_t a0 = smem_desc(L.stages, p.a_mn ? kChunkBytes : 16, 1024, 2);
+  const uint64_t b0 = smem_desc(L.stages + C::A_BYTES, p.b_mn ? kChunkBytes : 16, 1024, 2);
+  const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;  // 16 of K
+  uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1, last = 0, last_phase = 0;
+  bool issued = false, ok = true, ready = false;
+  const bool ends = !PAIR && p.by_k && p.counts;  // not planned as pairs
+  Walk<SPLIT, PAIR, SWIGLU> walk(p, L.first_tile, BN);
+  Tile t;
+  while (ok && walk.next(t)) {
+    if (t.kb0 == t.kb1) continue;  // nothing to add up: the epilogue takes zeros
+    ok = warp_wait(L.acc_empty + 8 * buf, buf_phase, abort, p.status);
+    if (!ok) break;
+    const uint32_t d = tmem + buf * BN;
+    for (int kb = t.kb0; kb < t.kb1; ++kb) {
+      if (!ready) {
+        ok = warp_wait(L.full + 8 * stage, phase, abort, p.status);
+        if (!ok) break;
+      }
+      const int left = t.k_end - kb * kBK;
+      const bool end = ends && left < kBK;
+      const int steps = end ? end_of_group<BN>(L.stages + stage * C::STAGE_BYTES, left, lane) : kBK / 16;
+      tc_fence_after();
+      const uint32_t now = stage;
+      last = stage;
+      last_phase = phase;
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      // whether the next stage is there, asked while this one's products are issued
+      const uint32_t next = mbar_test_wait(L.full + 8 * stage, phase);
+      if (leader) {
+        const uint64_t ad = a0 + (uint64_t)now * (C::STAGE_BYTES >> 4);
+        const uint64_t bd = b0 + (uint64_t)now * (C::STAGE_BYTES >> 4);
+#pragma unroll
+        for (int i = 0; i < kBK / 16; ++i)
+          if (i < steps) tc_mma_f16<PAIR>(d, ad + i * a_step, bd + i * b_step, idesc, kb != t.kb0 || i != 0);
+        if constexpr (PAIR) {
+          tc_commit_pair_mc(L.empty + 8 * now, 3);
+          if (kb + 1 == t.kb1) tc_commit_pair_mc(L.acc_full + 8 * buf, 3);
+        } else {
+          tc_commit(L.empty + 8 * now);
+          if (kb + 1 == t.kb1) tc_commit(L.acc_full + 8 * buf);
+        }
+      }
+      ready = __all_sync(0xffffffffu, next);
+      issued = true;
+    }
+    if (++buf == C::BUFS) {
+      buf = 0;
+      buf_phase ^= 1u;
+    }
+  }
+  // The products end before the warp leaves and TMEM is freed, also where another role gives up later.
+  if (lane == 0 && issued) {
+    volatile int no_abort = 0;
+    wait_bounded(L.empty + 8 * last, last_phase, &no_abort, nullptr, kDrainNs);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void st_shared_f4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// The bias of the warp's columns col .. col + n - 1 (and, for SwiGLU, of their up
+// columns) into shared memory as FP32, zeros past the last column.
+template <bool SWIGLU>
+__device__ __forceinline__ void stage_bias(const LinearEpilogue& p, uint32_t to, int g, int col, int n, int lane) {
+  __syncwarp();  // the reads of the tile before are done
+  if (4 * lane < n) {
+    const int c = col + 4 * lane;
+#pragma unroll
+    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+      uint32_t f[4] = {};
+      const int64_t at = (int64_t)g * p.wide + h * p.N + c;
+      if (c < p.N) {
+        if (p.bias_type == kTypeF32) {
+          const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.bias) + at);
+          f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + at);
+          float a, b;
+          unpack2(p.bias_type, v.x, a, b), f[0] = __float_as_uint(a), f[1] = __float_as_uint(b);
+          unpack2(p.bias_type, v.y, a, b), f[2] = __float_as_uint(a), f[3] = __float_as_uint(b);
+        }
+      }
+      st_shared_f4(to + h * 512 + lane * 16, f[0], f[1], f[2], f[3]);
+    }
+  }
+  __syncwarp();
+}
+template <int W>
+__device__ __forceinline__ void add_bias(uint32_t at, float (&z)[W]) {
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const float4 b = ld_shared_f4(at + 16 * i);
+    z[4 * i] += b.x, z[4 * i + 1] += b.y, z[4 * i + 2] += b.z, z[4 * i + 3] += b.w;
+  }
+}
+
+// Columns of the warp's rows, zeros where nothing was added up.
+template <int W>
+__device__ __forceinline__ void read_columns(bool some, uint32_t at, float (&f)[W]) {
+  uint32_t v[W];
+  if (some) {
+    tmem_load_cols(at, v);
+    tmem_load_wait();
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    asm volatile("" : "+r"(v[i]));  // no use moves above the wait
+    f[i] = some ? __uint_as_float(v[i]) : 0.f;
+  }
+}
+
+template <int BN, bool SPLIT, bool PAIR, int EPI>
+__device__ void epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
+  using C = Cfg<BN, PAIR>;
+  constexpr bool SWIGLU = EPI == kEpiSwiglu;
+  constexpr int COLS = SWIGLU ? BN / 4 : BN / 2;                     // output columns of this warp
+  constexpr int W = EPI == kEpiPlain && COLS >= 32 ? 32 : 16;        // held at a time
+  volatile int* abort = L.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
+  const uint32_t bias = L.bias + (warp - kEpiWarp0) * kBiasBytes;
+  const LinearEpilogue& ep = p.ep;
+  const int type = ep.type, out_type = ep.out_type, out_size = out_type == kTypeF32 ? 4 : 2;
+  // a pair's accumulators are free when both CTAs have read them: the first CTA's barrier counts
+  const uint32_t acc_empty = PAIR && cluster_ctarank() ? mapa_shared(L.acc_empty, 0) : L.acc_empty;
+  uint32_t buf = 0, phase = 0;
+  Walk<SPLIT, PAIR, SWIGLU> walk(p, L.first_tile, BN);
+  Tile t;
+  while (walk.next(t)) {
+    const bool some = t.kb0 != t.kb1;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN;
+    if constexpr (SPLIT) {  // the range's sums, a row of the tile per thread, for the join
+      if (some && !warp_wait_asleep(L.acc_full + 8 * buf, phase, abort, p.status)) break;
+      tc_fence_after();
+      const uint32_t to = L.stages + ((quarter * 32 + lane) * (BN + 4) + half * (BN / 2)) * 4;
+#pragma unroll
+      for (int c = 0; c < BN / 2; c += 32) {
+        float f[32];
+        read_columns(some, lanes + half * (BN / 2) + c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared_f4(to + c * 4 + 16 * i, __float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                       __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+      }
+      break;  // one tile
+    }
+    const int n0 = t.n0 + half * COLS;
+    const int left = quarter * 32 + lane < t.rows ? p.N - n0 : 0;  // columns that this thread's row has from n0 on
+    const int64_t row = t.out_row + quarter * 32 + lane;
+    uint8_t* out = static_cast<uint8_t*>(ep.out) + (row * ep.ld_out + n0) * out_size;
+    const uint8_t* res = static_cast<const uint8_t*>(ep.residual) + (row * ep.ld_residual + n0) * 2;
+    uint8_t* pre = static_cast<uint8_t*>(ep.preact) + (row * ep.ld_preact + n0) * 2;
+    // the residual's next two pieces are on their way: each alone would add its trip to memory
+    uint32_t r0[W / 2], r1[W / 2];
+    auto residual = [&](int c, uint32_t(&r)[W / 2]) {
+      if (ep.residual && c < COLS && c < left) load_row(res + 2 * c, ep.residual_v8, left - c, r);
+    };
+    residual(0, r0);
+    residual(W, r1);
+    if (ep.bias) stage_bias<SWIGLU>(ep, bias, t.g, n0, COLS, lane);
+    if (some && !warp_wait_asleep(L.acc_full + 8 * buf, phase, abort, p.status)) break;
+    tc_fence_after();
+    auto piece = [&](int c, uint32_t(&r)[W / 2]) {
+      __syncwarp();
+      float z[W], u[SWIGLU ? W : 1];
+      read_columns(some, lanes + half * COLS + c, z);
+      if constexpr (SWIGLU) read_columns(some, lanes + BN / 2 + half * COLS + c, u);
+      if (some && c + W >= COLS) {  // everything is in registers: the accumulator is free
+        tc_fence_before();
+        __syncwarp();
+        if (PAIR && acc_empty != L.acc_empty) {
+          if (lane == 0) mbar_arrive_remote(acc_empty + 8 * buf);
+        } else {
+          arrive_if(lane == 0, L.acc_empty + 8 * buf);
+        }
+      }
+      if (ep.bias) {
+        add_bias(bias + 4 * c, z);
+        if constexpr (SWIGLU) add_bias(bias + 512 + 4 * c, u);
+      }
+      if (c >= left) return;
+      if (ep.preact) {
+        store_row(pre + 2 * c, type, ep.preact_v8, left - c, z);
+        if constexpr (SWIGLU) store_row(pre + 2 * (p.N + c), type, ep.preact_v8, left - c, u);
+      }
+      if constexpr (SWIGLU) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) z[i] = swiglu(z[i], u[i], ep.gate_limit, ep.up_limit);
+      }
+      if constexpr (EPI == kEpiActivation) activate_all(ep.act, z);
+      if (ep.residual) {
+        add_row(type, r, z);
+        residual(c + 2 * W, r);
+      }
+      store_row(out + c * out_size, out_type, ep.out_v8, left - c, z);
+    };
+    constexpr int PIECES = COLS / W;
+#pragma unroll 1
+    for (int c = 0; c < PIECES / 2 * 2 * W; c += 2 * W) {
+      piece(c, r0);
+      piece(c + W, r1);
+    }
+    if constexpr (PIECES % 2 != 0) piece(COLS - W, r0);
+    if (some && ++buf == C::BUFS) {
+      buf = 0;
+      phase ^= 1u;
+    }
+  }
+  __syncwarp();
+}
+
+// The cluster's CTAs add up the ranges' sums in K order, each its share of the
+// tile's rows, eight output columns a lane.
+template <int BN, bool SWIGLU>
+__device__ void join_ranges(const LinearArgs& p, const Smem& L) {
+  Walk<true, false, SWIGLU> walk(p, L.first_tile, BN);
+  Tile t;
+  if (!walk.next(t)) return;
+  const int per = walk.out_cols / 8, rank = walk.rank;
+  const int tid = threadIdx.x - kEpiWarp0 * 32;
+  const int r0 = kBM * rank / p.split, r1 = min(kBM * (rank + 1) / p.split, t.rows);
+  for (int i = tid; i < (r1 - r0) * per; i += kEpiWarps * 32) {
+    const int r = r0 + i / per, c = i % per * 8, col = t.n0 + c;
+    if (col >= p.N) continue;
+    float z[8] = {}, u[8] = {}, b[8], bu[8];
+    load_bias(p.ep, t.g, col, b, bu);
+    auto add = [&](float(&s)[8], int at) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 v[kMaxSplit];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          if (q < p.split) v[q] = ld_shared_cluster_v4(mapa_shared(L.stages + (r * (BN + 4) + at + 4 * h) * 4, q));
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          if (q < p.split) {
+            s[4 * h] += __uint_as_float(v[q].x);
+            s[4 * h + 1] += __uint_as_float(v[q].y);
+            s[4 * h + 2] += __uint_as_float(v[q].z);
+            s[4 * h + 3] += __uint_as_float(v[q].w);
+          }
+      }
+    };
+    add(z, c);
+    if (SWIGLU) add(u, BN / 2 + c);
+    finish8(p.ep, t.out_row + r, col, z, u, b, bu);
+  }
+}
+
+// first_tile[g]: m-tiles before group g.
+template <int UNIT>
+__device__ void count_tiles(const LinearArgs& p, int* first_tile) {
+  if (!p.counts) {
+    if (threadIdx.x == 0) {
+      first_tile[0] = 0;
+      first_tile[1] = p.m_tiles;
+    }
+    return;
+  }
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  int sum = 0;
+  for (int base = 0; base < p.G; base += 32) {
+    const int c = base + lane < p.G ? (p.counts[base + lane] + UNIT - 1) / UNIT : 0;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (base + lane < p.G) first_tile[base + lane] = sum + incl - c;
+    sum += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) first_tile[p.G] = sum;
+}
+
+template <int BN, bool SPLIT, bool PAIR, int EPI>
+__global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ LinearArgs p) {
+  using C = Cfg<BN, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  const Smem L = carve<BN, PAIR>(smem_raw);
+  constexpr bool SWIGLU = EPI == kEpiSwiglu;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(L.full + 8 * s, 1);
+      mbar_init(L.empty + 8 * s, 1);
+    }
+    for (int b = 0; b < C::BUFS; ++b) {
+      mbar_init(L.acc_full + 8 * b, 1);
+      mbar_init(L.acc_empty + 8 * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
+    }
+    *L.abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&p.map_a);
+    prefetch_tmap(&p.map_b);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(L.tmem_slot), C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(L.tmem_slot), C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  pdl_wait();
+  count_tiles<C::UNIT_ROWS>(p, L.first_tile);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers are initialised, their TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem = *L.tmem_slot;
+  if (warp == 0) load_loop<BN, SPLIT, PAIR, SWIGLU>(p, L);
+  if (warp == 1 && (!PAIR || cluster_ctarank() == 0)) mma_loop<BN, SPLIT, PAIR, SWIGLU>(p, L, tmem);
+  if (warp >= kEpiWarp0) epilogue_loop<BN, SPLIT, PAIR, EPI>(p, L, tmem);
+  __syncwarp();
+  if constexpr (SPLIT) {
+    cluster_sync_all();
+    if (warp >= kEpiWarp0) join_ranges<BN, SWIGLU>(p, L);
+    __syncwarp();
+    cluster_arrive_relaxed();  // the other CTAs' reads of this one's shared memory
+    cluster_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // neither frees TMEM or leaves while the other may still touch it
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int BN, bool SPLIT, bool PAIR, int EPI>
+cudaError_t configure() {
+  static PerDevice<char, cudaError_t> done;
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+  const char* none = nullptr;
+  return done.get(dev, &none, [](char&) {
+    return cudaFuncSetAttribute(linear_gemm_kernel<BN, SPLIT, PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Cfg<BN, PAIR>::SMEM);
+  });
+}
+
+template <int BN, bool PAIR, int EPI>
+cudaError_t launch(LinearArgs& p, int slots, cudaStream_t s) {
+  using C = Cfg<BN, PAIR>;
+  const int out_cols = EPI == kEpiSwiglu ? BN / 2 : BN;
+  p.m_tiles = (p.M + C::UNIT_ROWS - 1) / C::UNIT_ROWS;
+  p.n_tiles = (p.N + out_cols - 1) / out_cols;
+  p.second = EPI == kEpiSwiglu ? p.N : BN / 2;
+  cudaError_t e;
+  if constexpr (BN < 256) {
+    if (p.split > 1) {
+      if ((e = configure<BN, true, false, EPI>()) != cudaSuccess) return e;
+      return launch_split<const LinearArgs>(linear_gemm_kernel<BN, true, false, EPI>, p.m_tiles * p.n_tiles * p.split,
+                                            kThreads, C::SMEM, p.split, s, p);
+    }
+  }
+  if ((e = configure<BN, false, PAIR, EPI>()) != cudaSuccess) return e;
+  // groups by rows: at most one tile more than the rows' for each
+  const int64_t m = p.by_k ? (int64_t)p.G * p.m_tiles : p.counts ? (int64_t)p.m_tiles + p.G : p.m_tiles;
+  const int64_t tiles = m * p.n_tiles;
+  const int grid = (int)(tiles < slots ? tiles : slots);
+  if (PAIR)
+    return launch_split<const LinearArgs>(linear_gemm_kernel<BN, false, PAIR, EPI>, 2 * grid, kThreads, C::SMEM, 2, s, p);
+  return launch_kernel(linear_gemm_kernel<BN, false, PAIR, EPI>, dim3(grid), dim3(kThreads), C::SMEM, s, true, p);
+}
+
+template <int EPI>
+cudaError_t launch_form(LinearArgs& p, int slots, cudaStream_t s) {
+  if (p.pair) return launch<256, true, EPI>(p, slots, s);
+  return p.bn == 256   ? launch<256, false, EPI>(p, slots, s)
+         : p.bn == 128 ? launch<128, false, EPI>(p, slots, s)
+                       : launch<64, false, EPI>(p, slots, s);
+}
+
+}  // namespace linear_gemm
+
+// The launch of a planned product; slots: CTAs, or pairs, that the GPU holds at a time.
+cudaError_t launch_linear_plain(LinearArgs& p, int slots, cudaStream_t s);
+cudaError_t launch_linear_activation(LinearArgs& p, int slots, cudaStream_t s);
+cudaError_t launch_linear_swiglu(LinearArgs& p, int slots, cudaStream_t s);
+
+}  // namespace nvfp4

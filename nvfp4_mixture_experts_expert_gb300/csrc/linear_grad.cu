@@ -25,7 +25,7 @@ __device__ __forceinline__ float slope(int act, float z) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
     case kActSilu: {
-      const float s = 1.f / (1.f + expf(-z));
+      const float s = sigmoid(z);
       return s * (1.f + z * (1.f - s));
     }
     case kActGelu: return 0.5f * (1.f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_dz_kernel(const LinearGrad
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float g = at_most(z[i], p.gate_limit), uc = at_least(at_most(u[i], p.up_limit), -p.up_limit);
-          const float sg = 1.f / (1.f + expf(-g));
+          const float sg = sigmoid(g);
           const float dg = z[i] > p.gate_limit ? 0.f : d[i] * uc * (sg * (1.f + g * (1.f - sg)));
           const float du = fabsf(u[i]) > p.up_limit ? 0.f : d[i] * (g * sg);
           z[i] = dg, u[i] = du;
