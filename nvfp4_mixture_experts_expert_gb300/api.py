@@ -407,6 +407,36 @@ def expert_linear_grad(grad, rows, w, order: TokenOrder, preact=None, activation
                          up_limit, bias, inputs, weights, out, _handle(stream))
 
 
+class ExpertFFN:
+    """The MoE layer's experts on unquantized weights, for given routing: tokens sorted by
+    expert, gate and up product with SwiGLU, down product, and back with the routing
+    weights.  w13 [E, 2I, H] and w2 [E, H, I] bf16 or f16, as quantize_moe_weights takes
+    them (bf16); the layer holds the experts [experts_start, experts_start + E)."""
+
+    def __init__(self, w13, w2, experts_start=0, gate_limit=10.0, up_limit=10.0):
+        self.w13, self.w2, self.experts_start = w13, w2, experts_start
+        self.limits = dict(activation="swiglu", gate_limit=gate_limit, up_limit=up_limit)
+
+    def __call__(self, hidden, topk_ids, topk_weights, residual=None, keep=False, stream=None):
+        """hidden [T, H], topk_ids i32 and topk_weights f32 [T, top_k].  keep=True: returns
+        (output, what grad takes)."""
+        rows, order = sort_tokens(hidden, topk_ids, self.w13.shape[0], self.experts_start, stream=stream)
+        h = expert_linear(rows, self.w13, order, preact=keep, stream=stream, **self.limits)
+        h, z = h if keep else (h, None)
+        y = expert_linear(h, self.w2, order, stream=stream)
+        out = combine_tokens(y, topk_weights, order, residual, stream=stream)
+        return (out, (rows, order, z, h, y, topk_weights)) if keep else out
+
+    def grad(self, grad_out, kept, stream=None):
+        """The gradients of hidden, topk_weights, w13 and w2 from that of the output (that of
+        residual is grad_out)."""
+        rows, order, z, h, y, weights = kept
+        grad_y, grad_weights = combine_tokens_grad(grad_out, y, weights, order, stream=stream)
+        grad_h, grad_w2, _ = expert_linear_grad(grad_y, h, self.w2, order, stream=stream)
+        grad_rows, grad_w13, _ = expert_linear_grad(grad_h, rows, self.w13, order, z, stream=stream, **self.limits)
+        return sort_tokens_grad(grad_rows, order, stream=stream), grad_weights, grad_w13, grad_w2
+
+
 class HostPipeline:
     """Streams batches from pinned host memory through one MoEForward.
 

@@ -10,12 +10,16 @@
 
 namespace nvfp4 {
 
-// 1 / (1 + exp(-z)) and silu by an exponential in (0, 1], whose sum's reciprocal needs
-// no care for its range: the division of z / (1 + expf(-z)) takes the slow path for
-// far negative z (8192 x 4096 x 4096 243 us instead of 165).
+// 1 / (1 + exp(-z)) by an exponential in (0, 1] and the reciprocal of a number in
+// (1, 2], both of a few FP32 units in the last place (of the result's size where it is
+// near 0: an absolute 2^-22): an accurate expf and a division take z / (1 + expf(-z))
+// to the slow path of the division for far negative z (8192 x 4096 x 4096 with silu 243
+// us instead of 160), and a gradient's pass over dy and z to its arithmetic.
 __device__ __forceinline__ float sigmoid(float z) {
-  const float e = expf(-fabsf(z));
-  return __fdividef(z < 0.f ? e : 1.f, 1.f + e);
+  const float e = __expf(-fabsf(z));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return (z < 0.f ? e : 1.f) * r;
 }
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 
@@ -25,14 +29,22 @@ __device__ __forceinline__ float activate(int act, float z) {
     case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case kActSilu: return silu(z);
     case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    case kActGeluTanh: return 0.5f * z * (1.f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
+    case kActGeluTanh: return z * sigmoid(1.59576912f * (z + 0.044715f * z * z * z));  // (1 + tanh(a)) / 2 = sigmoid(2 a)
     default: return z;
   }
 }
 
-// min and max that keep a NaN, as a comparison with a bound does.
-__device__ __forceinline__ float at_most(float z, float bound) { return z > bound ? bound : z; }
-__device__ __forceinline__ float at_least(float z, float bound) { return z < bound ? bound : z; }
+// min and max that keep a NaN.
+__device__ __forceinline__ float at_most(float z, float bound) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(bound));
+  return r;
+}
+__device__ __forceinline__ float at_least(float z, float bound) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(bound));
+  return r;
+}
 
 __device__ __forceinline__ float swiglu(float g, float u, float gate_limit, float up_limit) {
   return silu(at_most(g, gate_limit)) * at_least(at_most(u, up_limit), -up_limit);
@@ -96,6 +108,16 @@ __device__ __forceinline__ void store_words(void* p, bool v8, int left, const ui
     if (i * W / WORDS < left) *reinterpret_cast<uint4*>(q + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
 }
 template <int W>
+__device__ __forceinline__ void pack_row(int type, const float (&f)[W], uint32_t (&u)[W / 2]) {
+  if (type == kTypeBf16) {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) u[i] = pack2(kTypeBf16, f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) u[i] = pack2(kTypeF16, f[2 * i], f[2 * i + 1]);
+  }
+}
+template <int W>
 __device__ __forceinline__ void store_row(void* p, int type, bool v8, int left, const float (&f)[W]) {
   if (type == kTypeF32) {
     uint32_t u[W];
@@ -105,13 +127,7 @@ __device__ __forceinline__ void store_row(void* p, int type, bool v8, int left, 
     return;
   }
   uint32_t u[W / 2];
-  if (type == kTypeBf16) {
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) u[i] = pack2(kTypeBf16, f[2 * i], f[2 * i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) u[i] = pack2(kTypeF16, f[2 * i], f[2 * i + 1]);
-  }
+  pack_row(type, f, u);
   store_words<W>(p, v8, left, u);
 }
 

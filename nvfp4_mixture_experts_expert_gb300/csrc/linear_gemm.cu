@@ -41,7 +41,7 @@ cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms) {
   struct Form {
     int bn, pair, block_ns, tile_ns, join_ns;
   };
-  constexpr Form kForms[4] = {{256, 1, 310, 3100, 0}, {256, 0, 385, 2700, 0}, {128, 0, 275, 1600, 3500}, {64, 0, 245, 1000, 3000}};
+  constexpr Form kForms[4] = {{256, 1, 310, 3100, 0}, {256, 0, 385, 2700, 0}, {128, 0, 250, 1600, 4500}, {64, 0, 190, 1000, 3000}};
   const bool pairs = p.ep.act == kActSwiglu;
   const int64_t k = p.counts && p.by_k ? (p.K + p.G - 1) / p.G : p.K;  // of a group, on average
   const int64_t kbs = (k + kBK - 1) / kBK;

@@ -52,13 +52,17 @@ template <int BN, bool PAIR>
 struct Cfg {
   static constexpr int A_BYTES = kBM * kBK * 2;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // of B that this CTA holds
-  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * kBK * 2;
-  static constexpr int STAGES = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 7;
+  static constexpr int BLOCK_BYTES = A_BYTES + B_ROWS * kBK * 2;  // a K-block's operands
+  // K-blocks of a ring stage: two take a small tile's products past what a stage costs
+  // the warps (128 columns 275 -> 250 ns a block, 64 245 -> 190); a pair's lose 5 %
+  static constexpr int BLOCKS = BN == 256 ? 1 : 2;
+  static constexpr int STAGE_BYTES = BLOCKS * BLOCK_BYTES;
+  static constexpr int STAGES = PAIR ? 6 : BN == 64 ? 4 : BN == 128 ? 3 : 4;
   static constexpr int UNIT_ROWS = PAIR ? 2 * kBM : kBM;  // of a tile
   static constexpr int BUFS = 2;
   static constexpr int TMEM_COLS = BUFS * BN;
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kEpiWarps * kBiasBytes +
-                                 8 * (2 * STAGES + 2 * BUFS) + 16 + 4 * (kMaxGroups + 4);
+                                 8 * (2 * STAGES + 2 * BUFS) + 16 + 4 * (3 * kMaxGroups + 4);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -70,6 +74,7 @@ struct Smem {
   uint32_t* tmem_slot;
   int* abort_flag;
   int* first_tile;  // [G + 1], in m-tiles
+  int *first_row, *rows;  // [G], of the groups: read by every role for every tile
 };
 
 template <int BN, bool PAIR>
@@ -86,6 +91,8 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
   s.tmem_slot = reinterpret_cast<uint32_t*>(base + (s.acc_empty + 8 * C::BUFS - s.stages));
   s.abort_flag = reinterpret_cast<int*>(s.tmem_slot + 1);
   s.first_tile = s.abort_flag + 1;
+  s.first_row = s.first_tile + kMaxGroups + 1;
+  s.rows = s.first_row + kMaxGroups;
   return s;
 }
 
@@ -103,17 +110,17 @@ template <bool SPLIT, bool PAIR, bool SWIGLU>
 struct Walk {
   static constexpr int UNIT = PAIR ? 2 * kBM : kBM;
   const LinearArgs& p;
-  const int* first_tile;
+  const Smem& L;
   int it, step, rank, g = 0;
   int out_cols;  // columns of the output that a tile covers
-  __device__ Walk(const LinearArgs& p, const int* first_tile, int bn)
-      : p(p), first_tile(first_tile), out_cols(SWIGLU ? bn / 2 : bn) {
+  __device__ Walk(const LinearArgs& p, const Smem& L, int bn)
+      : p(p), L(L), out_cols(SWIGLU ? bn / 2 : bn) {
     it = SPLIT ? blockIdx.x / p.split : PAIR ? blockIdx.x / 2 : blockIdx.x;
     rank = SPLIT ? blockIdx.x % p.split : PAIR ? blockIdx.x % 2 : 0;
     step = SPLIT ? 1 << 30 : PAIR ? gridDim.x / 2 : gridDim.x;
   }
   __device__ bool next(Tile& t) {
-    const int m_total = p.by_k ? p.G * p.m_tiles : first_tile[p.G];
+    const int m_total = p.by_k ? p.G * p.m_tiles : L.first_tile[p.G];
     if (it >= m_total * p.n_tiles) return false;
     if (p.by_k) {
       const int per = p.m_tiles * p.n_tiles;
@@ -123,15 +130,15 @@ struct Walk {
       t.n0 = n * out_cols;
       t.rows = min(kBM, p.M - t.m0);
       t.out_row = (int64_t)g * p.M + t.m0;
-      t.k0 = p.counts ? p.offsets[g] : 0;
-      t.k_end = p.counts ? p.counts[g] : p.K;
+      t.k0 = L.first_row[g];
+      t.k_end = L.rows[g];
     } else {
-      while (it >= first_tile[g + 1] * p.n_tiles) ++g;
-      const int mt = first_tile[g + 1] - first_tile[g], r = it - first_tile[g] * p.n_tiles, n = r / mt;
+      while (it >= L.first_tile[g + 1] * p.n_tiles) ++g;
+      const int mt = L.first_tile[g + 1] - L.first_tile[g], r = it - L.first_tile[g] * p.n_tiles, n = r / mt;
       const int m = (r - n * mt) * UNIT + (PAIR ? rank * kBM : 0);
-      t.m0 = m + (p.counts ? p.offsets[g] : 0);
+      t.m0 = m + L.first_row[g];
       t.n0 = n * out_cols;
-      t.rows = min(kBM, (p.counts ? p.counts[g] : p.M) - m);
+      t.rows = min(kBM, L.rows[g] - m);
       t.out_row = t.m0;
       t.k0 = 0;
       t.k_end = p.K;
@@ -199,6 +206,30 @@ __device__ __forceinline__ uint32_t idesc_f16(int type, int a_mn, int b_mn, int 
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// The operands of the K-block from k on.
+template <int BN, bool PAIR, bool SWIGLU>
+__device__ __forceinline__ void load_block(const LinearArgs& p, const Tile& t, int rank, uint32_t a, int k,
+                                           uint32_t bar) {
+  using C = Cfg<BN, PAIR>;
+  const uint32_t b = a + C::A_BYTES;
+  if (p.a_mn) {
+#pragma unroll
+    for (int i = 0; i < kBM / 64; ++i) load_box<PAIR>(a + i * kChunkBytes, &p.map_a, t.m0 + 64 * i, k, bar);
+  } else {
+    load_box<PAIR>(a, &p.map_a, k, t.m0, bar);
+  }
+  if (p.b_mn) {
+    const int g = p.by_k ? 0 : t.g, n0 = t.n0 + (PAIR ? rank * C::B_ROWS : 0);
+#pragma unroll
+    for (int i = 0; i < C::B_ROWS / 64; ++i) load_box<PAIR>(b + i * kChunkBytes, &p.map_b, n0 + 64 * i, k, g, bar);
+  } else if (PAIR) {
+    load_box<PAIR>(b, &p.map_b, k, t.n0 + rank * p.second, t.g, bar);
+  } else {
+    load_box<PAIR>(b, &p.map_b, k, t.n0, t.g, bar);
+    if (SWIGLU) load_box<PAIR>(b + BN * kBK, &p.map_b, k, t.n0 + p.second, t.g, bar);
+  }
+}
+
 template <int BN, bool SPLIT, bool PAIR, bool SWIGLU>
 __device__ void load_loop(const LinearArgs& p, const Smem& L) {
   using C = Cfg<BN, PAIR>;
@@ -207,43 +238,29 @@ __device__ void load_loop(const LinearArgs& p, const Smem& L) {
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;
-  Walk<SPLIT, PAIR, SWIGLU> walk(p, L.first_tile, BN);
+  Walk<SPLIT, PAIR, SWIGLU> walk(p, L, BN);
   const uint32_t full0 = PAIR ? mapa_shared(L.full, 0) : L.full;
   Tile t;
   while (ok && !*abort && walk.next(t)) {
     const int kb1 = p.stall && t.kb1 > t.kb0 ? t.kb0 + 1 : t.kb1;
-    for (int kb = t.kb0; kb < kb1; ++kb) {
+    for (int kb = t.kb0; kb < kb1; kb += C::BLOCKS) {
       ok = warp_wait(L.empty + 8 * stage, phase ^ 1u, abort, p.status);
       if (!ok) break;
-      const uint32_t a = L.stages + stage * C::STAGE_BYTES, b = a + C::A_BYTES, bar = full0 + 8 * stage;
-      const uint32_t now = stage;
+      if (leader) {
+        const uint32_t bar = full0 + 8 * stage;
+        const int blocks = min(C::BLOCKS, kb1 - kb);
+        if (!PAIR || walk.rank == 0) mbar_arrive_expect_tx(L.full + 8 * stage, (PAIR ? 2 : 1) * blocks * C::BLOCK_BYTES);
+#pragma unroll
+        for (int i = 0; i < C::BLOCKS; ++i)
+          if (i < blocks) load_block<BN, PAIR, SWIGLU>(p, t, walk.rank, L.stages + stage * C::STAGE_BYTES + i * C::BLOCK_BYTES, t.k0 + (kb + i) * kBK, bar);
+      }
+      __syncwarp();
       issued |= 1u << stage;
       issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
       if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
-      if (leader) {
-        const int k = t.k0 + kb * kBK;
-        if (!PAIR || walk.rank == 0) mbar_arrive_expect_tx(L.full + 8 * now, (PAIR ? 2 : 1) * C::STAGE_BYTES);
-        if (p.a_mn) {
-#pragma unroll
-          for (int i = 0; i < kBM / 64; ++i) load_box<PAIR>(a + i * kChunkBytes, &p.map_a, t.m0 + 64 * i, k, bar);
-        } else {
-          load_box<PAIR>(a, &p.map_a, k, t.m0, bar);
-        }
-        if (p.b_mn) {
-          const int g = p.by_k ? 0 : t.g, n0 = t.n0 + (PAIR ? walk.rank * C::B_ROWS : 0);
-#pragma unroll
-          for (int i = 0; i < C::B_ROWS / 64; ++i) load_box<PAIR>(b + i * kChunkBytes, &p.map_b, n0 + 64 * i, k, g, bar);
-        } else if (PAIR) {
-          load_box<PAIR>(b, &p.map_b, k, t.n0 + walk.rank * p.second, t.g, bar);
-        } else {
-          load_box<PAIR>(b, &p.map_b, k, t.n0, t.g, bar);
-          if (SWIGLU) load_box<PAIR>(b + BN * kBK, &p.map_b, k, t.n0 + p.second, t.g, bar);
-        }
-      }
-      __syncwarp();
     }
   }
   // The copies land before the warp leaves, also where another role gives up later.
@@ -264,21 +281,18 @@ __device__ void load_loop(const LinearArgs& p, const Smem& L) {
   __syncwarp();
 }
 
-// Rows `from` .. 15 behind it, up to a multiple of 16, of `chunks` column chunks: zero.
-__device__ __forceinline__ void zero_rows(uint32_t at, int chunks, int from, int lane) {
-  const int to = (from + 15) & ~15, per = (to - from) * 8;  // 16-byte pieces of a chunk
-  for (int i = lane; i < chunks * per; i += 32) {
-    const int c = i / per, r = i - c * per;
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * kChunkBytes + from * 128 + r * 16), "r"(0)
-                 : "memory");
-  }
-}
-
 // A group's last K-block with by_k, behind which the next group's rows follow: sets
-// them to zero in this CTA's operands; returns the steps of 16 that count.
+// them to zero up to a multiple of 16 (in both operands: what lies there may be
+// infinite); returns the steps of 16 that count.
 template <int BN>
 __device__ __forceinline__ int end_of_group(uint32_t at, int left, int lane) {
-  zero_rows(at, kBM / 64 + BN / 64, left, lane);
+  for (int r = left + (lane >> 3); r < ((left + 15) & ~15); r += 4) {
+#pragma unroll
+    for (int c = 0; c < kBM / 64 + BN / 64; ++c)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * kChunkBytes + r * 128 + (lane & 7) * 16),
+                   "r"(0)
+                   : "memory");
+  }
   fence_proxy_async_smem();
   __syncwarp();
   return (left + 15) / 16;
@@ -298,21 +312,25 @@ __device__ void mma_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1, last = 0, last_phase = 0;
   bool issued = false, ok = true, ready = false;
   const bool ends = !PAIR && p.by_k && p.counts;  // not planned as pairs
-  Walk<SPLIT, PAIR, SWIGLU> walk(p, L.first_tile, BN);
+  Walk<SPLIT, PAIR, SWIGLU> walk(p, L, BN);
   Tile t;
   while (ok && walk.next(t)) {
     if (t.kb0 == t.kb1) continue;  // nothing to add up: the epilogue takes zeros
     ok = warp_wait(L.acc_empty + 8 * buf, buf_phase, abort, p.status);
     if (!ok) break;
     const uint32_t d = tmem + buf * BN;
-    for (int kb = t.kb0; kb < t.kb1; ++kb) {
+    for (int kb = t.kb0; kb < t.kb1; kb += C::BLOCKS) {
       if (!ready) {
         ok = warp_wait(L.full + 8 * stage, phase, abort, p.status);
         if (!ok) break;
       }
-      const int left = t.k_end - kb * kBK;
-      const bool end = ends && left < kBK;
-      const int steps = end ? end_of_group<BN>(L.stages + stage * C::STAGE_BYTES, left, lane) : kBK / 16;
+      const int blocks = min(C::BLOCKS, t.kb1 - kb);
+      int steps = kBK / 16;  // of the last block
+      if (ends) {
+        const int at = kb + blocks - 1, left = t.k_end - at * kBK;
+        if (left < kBK)
+          steps = end_of_group<BN>(L.stages + stage * C::STAGE_BYTES + (blocks - 1) * C::BLOCK_BYTES, left, lane);
+      }
       tc_fence_after();
       const uint32_t now = stage;
       last = stage;
@@ -327,14 +345,21 @@ __device__ void mma_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
         const uint64_t ad = a0 + (uint64_t)now * (C::STAGE_BYTES >> 4);
         const uint64_t bd = b0 + (uint64_t)now * (C::STAGE_BYTES >> 4);
 #pragma unroll
-        for (int i = 0; i < kBK / 16; ++i)
-          if (i < steps) tc_mma_f16<PAIR>(d, ad + i * a_step, bd + i * b_step, idesc, kb != t.kb0 || i != 0);
+        for (int j = 0; j < C::BLOCKS; ++j)
+          if (j < blocks) {
+#pragma unroll
+            for (int i = 0; i < kBK / 16; ++i)
+              if (j + 1 < blocks || i < steps)
+                tc_mma_f16<PAIR>(d, ad + j * (C::BLOCK_BYTES >> 4) + i * a_step, bd + j * (C::BLOCK_BYTES >> 4) + i * b_step,
+                                 idesc, kb != t.kb0 || i != 0 || j != 0);
+          }
+        const bool done = kb + C::BLOCKS >= t.kb1;
         if constexpr (PAIR) {
           tc_commit_pair_mc(L.empty + 8 * now, 3);
-          if (kb + 1 == t.kb1) tc_commit_pair_mc(L.acc_full + 8 * buf, 3);
+          if (done) tc_commit_pair_mc(L.acc_full + 8 * buf, 3);
         } else {
           tc_commit(L.empty + 8 * now);
-          if (kb + 1 == t.kb1) tc_commit(L.acc_full + 8 * buf);
+          if (done) tc_commit(L.acc_full + 8 * buf);
         }
       }
       ready = __all_sync(0xffffffffu, next);
@@ -428,7 +453,7 @@ __device__ void epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem)
   // a pair's accumulators are free when both CTAs have read them: the first CTA's barrier counts
   const uint32_t acc_empty = PAIR && cluster_ctarank() ? mapa_shared(L.acc_empty, 0) : L.acc_empty;
   uint32_t buf = 0, phase = 0;
-  Walk<SPLIT, PAIR, SWIGLU> walk(p, L.first_tile, BN);
+  Walk<SPLIT, PAIR, SWIGLU> walk(p, L, BN);
   Tile t;
   while (walk.next(t)) {
     const bool some = t.kb0 != t.kb1;
@@ -517,7 +542,7 @@ __device__ void epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem)
 // tile's rows, eight output columns a lane.
 template <int BN, bool SWIGLU>
 __device__ void join_ranges(const LinearArgs& p, const Smem& L) {
-  Walk<true, false, SWIGLU> walk(p, L.first_tile, BN);
+  Walk<true, false, SWIGLU> walk(p, L, BN);
   Tile t;
   if (!walk.next(t)) return;
   const int per = walk.out_cols / 8, rank = walk.rank;
@@ -551,13 +576,15 @@ __device__ void join_ranges(const LinearArgs& p, const Smem& L) {
   }
 }
 
-// first_tile[g]: m-tiles before group g.
+// The groups' tables: first rows, rows, and the m-tiles before each.
 template <int UNIT>
-__device__ void count_tiles(const LinearArgs& p, int* first_tile) {
+__device__ void read_groups(const LinearArgs& p, const Smem& L) {
   if (!p.counts) {
     if (threadIdx.x == 0) {
-      first_tile[0] = 0;
-      first_tile[1] = p.m_tiles;
+      L.first_row[0] = 0;
+      L.rows[0] = p.by_k ? p.K : p.M;
+      L.first_tile[0] = 0;
+      L.first_tile[1] = p.m_tiles;
     }
     return;
   }
@@ -565,17 +592,21 @@ __device__ void count_tiles(const LinearArgs& p, int* first_tile) {
   const int lane = threadIdx.x;
   int sum = 0;
   for (int base = 0; base < p.G; base += 32) {
-    const int c = base + lane < p.G ? (p.counts[base + lane] + UNIT - 1) / UNIT : 0;
+    const int g = base + lane, rows = g < p.G ? p.counts[g] : 0, c = (rows + UNIT - 1) / UNIT;
     int incl = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (base + lane < p.G) first_tile[base + lane] = sum + incl - c;
+    if (g < p.G) {
+      L.first_row[g] = p.offsets[g];
+      L.rows[g] = rows;
+      L.first_tile[g] = sum + incl - c;
+    }
     sum += __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (lane == 0) first_tile[p.G] = sum;
+  if (lane == 0) L.first_tile[p.G] = sum;
 }
 
 template <int BN, bool SPLIT, bool PAIR, int EPI>
@@ -609,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     }
   }
   pdl_wait();
-  count_tiles<C::UNIT_ROWS>(p, L.first_tile);
+  read_groups<C::UNIT_ROWS>(p, L);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers are initialised, their TMEM allocated

@@ -20,21 +20,41 @@ namespace {
 constexpr int kSlabRows = 64;
 constexpr int kWarps = 8;
 
-// d act(z) / dz.
-__device__ __forceinline__ float slope(int act, float z) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
-    case kActSilu: {
-      const float s = sigmoid(z);
-      return s * (1.f + z * (1.f - s));
-    }
-    case kActGelu: return 0.5f * (1.f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
-    case kActGeluTanh: {
-      const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * (0.79788456f * (1.f + 0.134145f * z * z));
-    }
-    default: return 1.f;
+// d act(z) / dz.  The terms with a factor z vanish long before kFar, and are 0 * inf
+// at an infinite z without it.
+constexpr float kFar = 1e4f;
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+  const float f = at_least(at_most(z, kFar), -kFar);
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
+  if constexpr (ACT == kActSilu) {
+    const float s = sigmoid(z);
+    return s + f * s * (1.f - s);
   }
+  if constexpr (ACT == kActGelu)
+    return 0.5f * (1.f + erff(z * 0.70710678f)) + f * expf(-0.5f * f * f) * 0.39894228f;
+  if constexpr (ACT == kActGeluTanh) {
+    const float s = sigmoid(1.59576912f * (z + 0.044715f * z * z * z));
+    return s + f * s * (1.f - s) * (1.59576912f * (1.f + 0.134145f * f * f));
+  }
+  return 1.f;
+}
+
+// What eight columns of a row need of dy and z, as loaded (z and u: SwiGLU's gate and up).
+struct Piece {
+  uint4 d, z, u;
+};
+template <int ACT>
+__device__ __forceinline__ void load_piece(const LinearGradArgs& p, int64_t row, int col, Piece& v) {
+  v.d = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dy) + row * p.ld_dy + col);
+  const uint16_t* z = static_cast<const uint16_t*>(p.z) + row * p.wide + col;
+  if constexpr (ACT != kActNone) v.z = *reinterpret_cast<const uint4*>(z);
+  if constexpr (ACT == kActSwiglu) v.u = *reinterpret_cast<const uint4*>(z + p.N);
+}
+template <int TYPE>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  unpack2(TYPE, v.x, f[0], f[1]), unpack2(TYPE, v.y, f[2], f[3]);
+  unpack2(TYPE, v.z, f[4], f[5]), unpack2(TYPE, v.w, f[6], f[7]);
 }
 
 // The slab of a block: its group and rows.  Slabs of a group are neighbours.
@@ -79,9 +99,11 @@ __device__ __forceinline__ bool slab_at(const LinearGradArgs& p, int s, Slab& ou
   return true;
 }
 
-// 256 columns of a slab a block, eight a lane.
-template <bool PAIRS>
-__global__ void __launch_bounds__(kWarps * 32) linear_dz_kernel(const LinearGradArgs p) {
+// 256 columns of a slab a block, eight a lane; a warp's rows two at a time.
+template <int ACT, int TYPE>
+__global__ void __launch_bounds__(kWarps * 32, ACT == kActSwiglu ? 3 : 4) linear_dz_kernel(const LinearGradArgs p) {
+  constexpr bool PAIRS = ACT == kActSwiglu;
+  constexpr int ROWS = 2;
   pdl_trigger();
   pdl_wait();
   __shared__ int found[2];
@@ -89,39 +111,43 @@ __global__ void __launch_bounds__(kWarps * 32) linear_dz_kernel(const LinearGrad
   Slab s;
   if (!slab_at(p, blockIdx.x, s, found)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.y * 256 + lane * 8;
-  float sum[8] = {}, sum_u[8] = {};
+  float sum[8] = {}, sum_u[8] = {};  // of the rounded products (no fused multiply-add): the same with and without dz
   if (col < p.N) {
-    for (int r = warp; r < s.rows; r += kWarps) {
-      const int64_t row = s.row0 + r;
-      float d[8], z[8], u[8];
-      load8(p.dy, row * p.ld_dy + col, p.type, d);
-      if (PAIRS) {
-        load8(p.z, row * p.wide + col, p.type, z);
-        load8(p.z, row * p.wide + p.N + col, p.type, u);
+    for (int r0 = warp; r0 < s.rows; r0 += ROWS * kWarps) {
+      Piece v[ROWS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float g = at_most(z[i], p.gate_limit), uc = at_least(at_most(u[i], p.up_limit), -p.up_limit);
-          const float sg = sigmoid(g);
-          const float dg = z[i] > p.gate_limit ? 0.f : d[i] * uc * (sg * (1.f + g * (1.f - sg)));
-          const float du = fabsf(u[i]) > p.up_limit ? 0.f : d[i] * (g * sg);
-          z[i] = dg, u[i] = du;
-          sum[i] += dg, sum_u[i] += du;
-        }
-      } else {
-        if (p.act != kActNone) {
-          load8(p.z, row * p.wide + col, p.type, z);
+      for (int j = 0; j < ROWS; ++j)
+        if (r0 + j * kWarps < s.rows) load_piece<ACT>(p, s.row0 + r0 + j * kWarps, col, v[j]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = d[i] * slope(p.act, z[i]);
+      for (int j = 0; j < ROWS; ++j) {
+        if (r0 + j * kWarps >= s.rows) break;
+        const int64_t at = (s.row0 + r0 + j * kWarps) * p.wide + col;
+        float d[8], z[8], u[8];
+        unpack8<TYPE>(v[j].d, d);
+        if constexpr (ACT != kActNone) unpack8<TYPE>(v[j].z, z);
+        if constexpr (PAIRS) {
+          unpack8<TYPE>(v[j].u, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float g = at_least(at_most(z[i], p.gate_limit), -kFar);
+            const float uc = at_least(at_most(u[i], p.up_limit), -p.up_limit);
+            const float sg = sigmoid(g), h = g * sg;
+            z[i] = z[i] > p.gate_limit ? 0.f : __fmul_rn(d[i] * uc, fmaf(h, 1.f - sg, sg));
+            u[i] = u[i] == uc ? __fmul_rn(d[i], h) : 0.f;
+            const float du = u[i];
+            sum[i] = __fadd_rn(sum[i], z[i]), sum_u[i] = __fadd_rn(sum_u[i], du);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = d[i];
+          for (int i = 0; i < 8; ++i) {
+            z[i] = ACT == kActNone ? d[i] : d[i] * slope<ACT>(z[i]);
+            sum[i] = __fadd_rn(sum[i], z[i]);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += z[i];
-      }
-      if (p.dz) {
-        store8(p.dz, row * p.wide + col, p.type, z);
-        if (PAIRS) store8(p.dz, row * p.wide + p.N + col, p.type, u);
+        if (p.dz) {
+          store8(p.dz, at, TYPE, z);
+          if (PAIRS) store8(p.dz, at + p.N, TYPE, u);
+        }
       }
     }
   }
@@ -142,31 +168,32 @@ __global__ void __launch_bounds__(kWarps * 32) linear_dz_kernel(const LinearGrad
   }
 }
 
-// dbias[g][c]: the partial rows of group g's slabs, in order.
-__global__ void __launch_bounds__(256) linear_dbias_kernel(const LinearGradArgs p) {
+// dbias[g][c]: the partial rows of group g's slabs.  32 columns a block; each warp
+// adds every eighth slab in order, then the warps' sums in order.
+__global__ void __launch_bounds__(kWarps * 32) linear_dbias_kernel(const LinearGradArgs p) {
   pdl_trigger();
   pdl_wait();
-  const int g = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-  __shared__ int first;
-  int slabs = (p.M + kSlabRows - 1) / kSlabRows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.y, c = blockIdx.x * 32 + lane;
+  __shared__ float part[kWarps][32];
+  int first = 0, slabs = (p.M + kSlabRows - 1) / kSlabRows;
   if (p.counts) {
-    if (threadIdx.x < 32) {
-      int n = 0;
-      for (int i = threadIdx.x; i < g; i += 32) n += (p.counts[i] + kSlabRows - 1) / kSlabRows;
+    for (int i = lane; i < g; i += 32) first += (p.counts[i] + kSlabRows - 1) / kSlabRows;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (threadIdx.x == 0) first = n;
-    }
+    for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
     slabs = (p.counts[g] + kSlabRows - 1) / kSlabRows;
-  } else if (threadIdx.x == 0) {
-    first = 0;
   }
-  __syncthreads();
-  if (c >= p.wide) return;
-  const float* from = p.partial + (int64_t)first * p.wide + c;
   float v = 0.f;
+  if (c < p.wide) {
+    const float* from = p.partial + (int64_t)first * p.wide + c;
 #pragma unroll 8
-  for (int s = 0; s < slabs; ++s) v += from[(int64_t)s * p.wide];
+    for (int s = warp; s < slabs; s += kWarps) v += from[(int64_t)s * p.wide];
+  }
+  part[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || c >= p.wide) return;
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += part[w][lane];
   p.dbias[(int64_t)g * p.wide + c] = v;
 }
 
@@ -176,10 +203,19 @@ int64_t linear_grad_slabs(int64_t M, int groups) { return (M + kSlabRows - 1) / 
 
 cudaError_t launch_linear_dz(const LinearGradArgs& p, cudaStream_t s) {
   const dim3 grid((unsigned)linear_grad_slabs(p.M, p.counts ? p.G : 0), (p.N + 255) / 256);
-  cudaError_t e = launch_kernel(p.act == kActSwiglu ? linear_dz_kernel<true> : linear_dz_kernel<false>, grid,
-                                dim3(kWarps * 32), 0, s, true, p);
+  auto go = [&](auto bf16, auto f16) {
+    return launch_kernel(p.type == kTypeBf16 ? bf16 : f16, grid, dim3(kWarps * 32), 0, s, true, p);
+  };
+#define DZ(act) go(linear_dz_kernel<act, kTypeBf16>, linear_dz_kernel<act, kTypeF16>)
+  const cudaError_t e = p.act == kActRelu       ? DZ(kActRelu)
+                        : p.act == kActSilu     ? DZ(kActSilu)
+                        : p.act == kActGelu     ? DZ(kActGelu)
+                        : p.act == kActGeluTanh ? DZ(kActGeluTanh)
+                        : p.act == kActSwiglu   ? DZ(kActSwiglu)
+                                                : DZ(kActNone);
+#undef DZ
   if (e != cudaSuccess || !p.partial) return e;
-  return launch_kernel(linear_dbias_kernel, dim3((p.wide + 255) / 256, p.G), dim3(256), 0, s, true, p);
+  return launch_kernel(linear_dbias_kernel, dim3((p.wide + 31) / 32, p.G), dim3(kWarps * 32), 0, s, true, p);
 }
 
 }  // namespace nvfp4

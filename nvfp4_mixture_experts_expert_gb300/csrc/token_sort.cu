@@ -27,10 +27,24 @@ constexpr int kMaxTopK = 32;
 constexpr int kOrderWarps = 32;
 constexpr int kOrderCtas = 8;
 constexpr int kFusedAssignments = 2048;
+constexpr int kHeld = 8;  // ids a lane
 
+// 0 .. E - 1, or E: held elsewhere.
 __device__ __forceinline__ int local_expert(int32_t id, int32_t start, int E) {
   const int64_t e = (int64_t)id - start;
-  return e >= 0 && e < E ? (int)e : -1;
+  return e >= 0 && e < E ? (int)e : E;
+}
+
+// The lanes with the same expert (0 .. 2^bits - 1), by a vote on each bit: a
+// match.any over this many different values takes the warp ~200 cycles (the order of
+// 49152 assignments 14.3 us instead of ORDER_US).
+__device__ __forceinline__ uint32_t same_expert(int e, int bits) {
+  uint32_t peers = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t set = __ballot_sync(0xffffffffu, (e >> b) & 1);
+    peers &= (e >> b) & 1 ? set : ~set;
+  }
+  return peers;
 }
 
 // Warp 0: s_off[e] = sum of the aligned counts before e, s_off[E] the total.
@@ -67,21 +81,40 @@ __global__ void __cluster_dims__(kOrderCtas, 1, 1) __launch_bounds__(kOrderWarps
   pdl_wait();
   const int64_t n = p.T * p.k, g = (int64_t)rank * kOrderWarps + warp, warps = kOrderCtas * kOrderWarps;
   const int64_t f0 = n * g / warps, f1 = n * (g + 1) / warps;
-  for (int64_t base = f0; base < f1; base += 32) {
-    const int64_t f = base + lane;
-    const int e = f < f1 ? local_expert(p.ids[f], p.start, E) : -1;
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(peers) - 1) hist[warp][e] += __popc(peers);
-    __syncwarp();
+  const int bits = 32 - __clz(E);  // of 0 .. E; E: no expert held here
+  // 32 kHeld ids at a time, and those of a range that has no more stay in registers
+  const bool one = f1 - f0 <= 32 * kHeld;
+  int e[kHeld];
+  uint32_t peers[kHeld];
+  auto take = [&](int64_t base) {
+    int id[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) id[i] = base + i * 32 + lane < f1 ? p.ids[base + i * 32 + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (base + i * 32 >= f1) break;
+      e[i] = base + i * 32 + lane < f1 ? local_expert(id[i], p.start, E) : E;
+      peers[i] = same_expert(e[i], bits);
+    }
+  };
+  for (int64_t base = f0; base < f1; base += 32 * kHeld) {
+    take(base);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (base + i * 32 >= f1) break;
+      if (e[i] < E && lane == __ffs(peers[i]) - 1) hist[warp][e[i]] += __popc(peers[i]);
+      __syncwarp();
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int sum = 0;
+    int c[kOrderWarps], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kOrderWarps; ++w) c[w] = hist[w][e];
 #pragma unroll
     for (int w = 0; w < kOrderWarps; ++w) {
-      const int c = hist[w][e];
       hist[w][e] = sum;
-      sum += c;
+      sum += c[w];
     }
     cta_total[e] = sum;
   }
@@ -113,17 +146,20 @@ __global__ void __cluster_dims__(kOrderCtas, 1, 1) __launch_bounds__(kOrderWarps
     }
   }
   __syncthreads();
-  for (int64_t base = f0; base < f1; base += 32) {
-    const int64_t f = base + lane;
-    const int e = f < f1 ? local_expert(p.ids[f], p.start, E) : -1;
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    int row = -1;
-    if (e >= 0) row = hist[warp][e] + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(peers) - 1) hist[warp][e] += __popc(peers);
-    __syncwarp();
-    if (f < f1) p.inverse[f] = row;
-    if (row >= 0) p.source[row] = (int32_t)f;
+  for (int64_t base = f0; base < f1; base += 32 * kHeld) {
+    if (!one) take(base);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (base + i * 32 >= f1) break;
+      const int64_t f = base + i * 32 + lane;
+      int row = -1;
+      if (e[i] < E) row = hist[warp][e[i]] + __popc(peers[i] & ((1u << lane) - 1u));
+      __syncwarp();
+      if (e[i] < E && lane == __ffs(peers[i]) - 1) hist[warp][e[i]] += __popc(peers[i]);
+      __syncwarp();
+      if (f < f1) p.inverse[f] = row;
+      if (row >= 0) p.source[row] = (int32_t)f;
+    }
   }
   // rows without an assignment: between the experts, and behind the last
   const int64_t t0 = (int64_t)rank * blockDim.x + threadIdx.x, step = (int64_t)kOrderCtas * blockDim.x;
@@ -198,7 +234,7 @@ __global__ void __launch_bounds__(512) sort_few_kernel(const SortArgs p) {
   for (int f = tid; f < n; f += nt) {
     const int e = local_expert(p.ids[f], p.start, E);
     ids[f] = e;
-    if (e >= 0) atomicAdd(&count[e], 1);
+    if (e < E) atomicAdd(&count[e], 1);
   }
   __syncthreads();
   if (tid < 32) scan_offsets(count, off, E, p.align, tid);
@@ -224,7 +260,7 @@ __global__ void __launch_bounds__(512) sort_few_kernel(const SortArgs p) {
     return;
   }
   if (tid < k) {
-    const int f = (int)t * k + tid, e = ids[f], r = e >= 0 ? off[e] + rank[tid] : -1;
+    const int f = (int)t * k + tid, e = ids[f], r = e < E ? off[e] + rank[tid] : -1;
     row[tid] = r;
     p.inverse[f] = r;
     if (r >= 0) p.source[r] = f;
