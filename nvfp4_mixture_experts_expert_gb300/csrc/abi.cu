@@ -1533,6 +1533,7 @@ int nvfp4_linear_grad(const nvfp4_linear_shape* s, const void* dy, int64_t ld_dy
     t.M = (int)s->M;
     t.K = (int)wide;
     t.b_mn = 1;
+    t.before = dw != nullptr;
     if (int rc = run_linear_gemm(t, s, dz, s->M, wide, ld_dz, w, G, wide, s->K, s->K, dev, stream)) return rc;
   }
   if (dw) {
@@ -1544,6 +1545,7 @@ int nvfp4_linear_grad(const nvfp4_linear_shape* s, const void* dy, int64_t ld_dy
     t.M = (int)wide;
     t.K = (int)s->M;
     t.a_mn = t.b_mn = t.by_k = 1;
+    t.beside = dx != nullptr;
     if (int rc = run_linear_gemm(t, s, dz, s->M, wide, ld_dz, x, 1, s->M, s->K, ld_x, dev, stream)) return rc;
   }
   return NVFP4_OK;

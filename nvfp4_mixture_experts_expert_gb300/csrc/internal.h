@@ -376,6 +376,10 @@ struct LinearArgs {
   int a_mn, b_mn;  // operand stored with its output dimension contiguous
   int by_k;      // the groups' rows are the contraction (weight gradients)
   int second;    // rows of B from the first to the second half of a tile
+  // Two products that do not depend on each other, launched one after the other: the
+  // first lets the second start once its own inputs are there (before), the second takes
+  // the SMs that the first's last round leaves idle and waits for it at its end (beside).
+  int before, beside;
   int stall;     // failure-detection check: only a tile's first K-block is loaded
   int bn, pair, split;         // columns of a tile, CTA pairs, CTAs that share a tile's K: set by linear_gemm_plan
   int m_tiles, n_tiles, tiles; // set by the launch (tiles: where the host knows them)

@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
       tmem_relinquish();
     }
   }
-  pdl_wait();
+  if (!p.beside) pdl_wait();
+  if (p.before) pdl_trigger();
   read_groups<C::UNIT_ROWS>(p, L);
   tc_fence_before();
   __syncthreads();
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   if (warp == 1 && (!PAIR || cluster_ctarank() == 0)) mma_loop<BN, SPLIT, PAIR, SWIGLU>(p, L, tmem);
   if (warp >= kEpiWarp0) epilogue_loop<BN, SPLIT, PAIR, EPI>(p, L, tmem);
   __syncwarp();
+  if (p.beside) pdl_wait();  // this kernel's end is also the end of the one it ran beside
   if constexpr (SPLIT) {
     cluster_sync_all();
     if (warp >= kEpiWarp0) join_ranges<BN, SWIGLU>(p, L);

@@ -71,7 +71,6 @@ __device__ __forceinline__ void scan_offsets(const int32_t* count, int32_t* s_of
 // rows.  49152 assignments: 6 steps of 32 a warp and phase.
 __global__ void __cluster_dims__(kOrderCtas, 1, 1) __launch_bounds__(kOrderWarps * 32) token_order_kernel(
     const SortArgs p) {
-  pdl_trigger();
   __shared__ int32_t hist[kOrderWarps][kMaxExperts];
   __shared__ int32_t cta_total[kMaxExperts], total[kMaxExperts], below[kMaxExperts], s_off[kMaxExperts + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
@@ -79,6 +78,7 @@ __global__ void __cluster_dims__(kOrderCtas, 1, 1) __launch_bounds__(kOrderWarps
   for (int i = threadIdx.x; i < kOrderWarps * kMaxExperts; i += blockDim.x) (&hist[0][0])[i] = 0;
   __syncthreads();
   pdl_wait();
+  pdl_trigger();  // only now: copy_rows_kernel reads x before it waits for this one
   const int64_t n = p.T * p.k, g = (int64_t)rank * kOrderWarps + warp, warps = kOrderCtas * kOrderWarps;
   const int64_t f0 = n * g / warps, f1 = n * (g + 1) / warps;
   const int bits = 32 - __clz(E);  // of 0 .. E; E: no expert held here
@@ -187,27 +187,41 @@ __device__ __forceinline__ void zero_pad_row(uint8_t* rows, int64_t ld, int nvec
   for (int c = lane; c < nvec; c += 32) store16(rows + r * ld + c * 16, make_uint4(0, 0, 0, 0));
 }
 
-// One token's vectors to its rows, two in flight.
-__device__ __forceinline__ void copy_token(const SortArgs& p, int64_t t, const int32_t* row) {
+// Two of a token's vectors: c and c + blockDim.x.
+struct TokenPiece {
+  uint4 a, b;
+  bool two;
+};
+__device__ __forceinline__ TokenPiece load_piece(const SortArgs& p, int64_t t, int c) {
   const uint8_t* x = p.x + t * p.ld_x;
+  TokenPiece v = {};
+  v.two = c + (int)blockDim.x < p.nvec;
+  if (c < p.nvec) v.a = load16(x + c * 16);
+  if (v.two) v.b = load16(x + (c + blockDim.x) * 16);
+  return v;
+}
+// A token's vectors, of which `v` is the thread's first piece, to its rows.
+__device__ __forceinline__ void copy_token(const SortArgs& p, int64_t t, const int32_t* row, TokenPiece v) {
   const int nt = blockDim.x;
   for (int c = threadIdx.x; c < p.nvec; c += 2 * nt) {
-    const bool two = c + nt < p.nvec;
-    const uint4 a = load16(x + c * 16), b = two ? load16(x + (c + nt) * 16) : a;
+    if (c != threadIdx.x) v = load_piece(p, t, c);
     for (int j = 0; j < p.k; ++j) {
       const int64_t r = row[j];
       if (r < 0) continue;
-      store16(p.rows + r * p.ld_rows + c * 16, a);
-      if (two) store16(p.rows + r * p.ld_rows + (c + nt) * 16, b);
+      store16(p.rows + r * p.ld_rows + c * 16, v.a);
+      if (v.two) store16(p.rows + r * p.ld_rows + (c + nt) * 16, v.b);
     }
   }
 }
 
-// A token per block, then blocks that write pad rows, a row per warp.
+// A token per block, then blocks that write pad rows, a row per warp.  x is there as
+// soon as the ordering kernel has begun (it waits for what came before it).
 __global__ void __launch_bounds__(512) copy_rows_kernel(const SortArgs p) {
   pdl_trigger();
-  pdl_wait();
   const int64_t t = blockIdx.x;
+  TokenPiece first = {};
+  if (t < p.T) first = load_piece(p, t, threadIdx.x);
+  pdl_wait();
   if (t >= p.T) {
     const int warps = blockDim.x >> 5;
     zero_pad_row(p.rows, p.ld_rows, p.nvec, p.offsets, p.counts, p.E, p.align,
@@ -217,7 +231,7 @@ __global__ void __launch_bounds__(512) copy_rows_kernel(const SortArgs p) {
   __shared__ int32_t row[kMaxTopK];
   if (threadIdx.x < p.k) row[threadIdx.x] = p.inverse[t * p.k + threadIdx.x];
   __syncthreads();
-  copy_token(p, t, row);
+  copy_token(p, t, row, first);
 }
 
 // The same with the order worked out by every block: counts and aligned offsets
@@ -239,6 +253,8 @@ __global__ void __launch_bounds__(512) sort_few_kernel(const SortArgs p) {
   __syncthreads();
   if (tid < 32) scan_offsets(count, off, E, p.align, tid);
   const int64_t t = blockIdx.x;
+  TokenPiece first = {};
+  if (t < p.T && p.rows) first = load_piece(p, t, tid);
   if (t < p.T) {
     const int mine = (int)t * k;
     for (int f = tid; f < mine + k; f += nt) {  // the ones before an assignment with its expert
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(512) sort_few_kernel(const SortArgs p) {
     for (int64_t r = off[E] + tid; r < p.capacity; r += nt) p.source[r] = -1;
   }
   __syncthreads();
-  if (p.rows) copy_token(p, t, row);
+  if (p.rows) copy_token(p, t, row, first);
 }
 
 // ------------------------------------------------------------------ sums over a token's rows
