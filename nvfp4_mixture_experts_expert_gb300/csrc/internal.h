@@ -382,7 +382,7 @@ struct LinearArgs {
   int before, beside;
   int stall;     // failure-detection check: only a tile's first K-block is loaded
   int bn, pair, split;         // columns of a tile, CTA pairs, CTAs that share a tile's K: set by linear_gemm_plan
-  int m_tiles, n_tiles, tiles; // set by the launch (tiles: where the host knows them)
+  int m_tiles, n_tiles, band;  // set by the launch
 };
 cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms);  // from the sizes, groups and activation
 cudaError_t launch_linear_gemm(LinearArgs& p, int num_sms, cudaStream_t s);

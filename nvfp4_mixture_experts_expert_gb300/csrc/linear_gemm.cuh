@@ -104,8 +104,10 @@ struct Tile {
   int64_t out_row;
 };
 
-// Walks the tiles of a role in its order; tiles of a group are neighbours, the
-// group's rows run fastest (the CTAs at work share few column tiles of B).
+// Walks the tiles of a role in its order; tiles of a group are neighbours.  Within it
+// bands of p.band m-tiles, in each of which m runs fastest: the CTAs at work then read
+// about as many rows of A as of B (8192 x 4096 x 4096 read 470 MB of memory with one
+// band, of 168 that the product needs).
 template <bool SPLIT, bool PAIR, bool SWIGLU>
 struct Walk {
   static constexpr int UNIT = PAIR ? 2 * kBM : kBM;
@@ -119,14 +121,22 @@ struct Walk {
     rank = SPLIT ? blockIdx.x % p.split : PAIR ? blockIdx.x % 2 : 0;
     step = SPLIT ? 1 << 30 : PAIR ? gridDim.x / 2 : gridDim.x;
   }
+  // Tile r of `mt` rows of tiles: its row and column.
+  __device__ __forceinline__ void place(int r, int mt, int& m, int& n) const {
+    const int band = r / (p.band * p.n_tiles), first = band * p.band, size = min(p.band, mt - first);
+    r -= first * p.n_tiles;
+    n = r / size;
+    m = first + r - n * size;
+  }
   __device__ bool next(Tile& t) {
     const int m_total = p.by_k ? p.G * p.m_tiles : L.first_tile[p.G];
     if (it >= m_total * p.n_tiles) return false;
     if (p.by_k) {
       const int per = p.m_tiles * p.n_tiles;
       g = it / per;
-      const int r = it - g * per, n = r / p.m_tiles;
-      t.m0 = (r - n * p.m_tiles) * UNIT + (PAIR ? rank * kBM : 0);
+      int m, n;
+      place(it - g * per, p.m_tiles, m, n);
+      t.m0 = m * UNIT + (PAIR ? rank * kBM : 0);
       t.n0 = n * out_cols;
       t.rows = min(kBM, p.M - t.m0);
       t.out_row = (int64_t)g * p.M + t.m0;
@@ -134,8 +144,9 @@ struct Walk {
       t.k_end = L.rows[g];
     } else {
       while (it >= L.first_tile[g + 1] * p.n_tiles) ++g;
-      const int mt = L.first_tile[g + 1] - L.first_tile[g], r = it - L.first_tile[g] * p.n_tiles, n = r / mt;
-      const int m = (r - n * mt) * UNIT + (PAIR ? rank * kBM : 0);
+      int m, n;
+      place(it - L.first_tile[g] * p.n_tiles, L.first_tile[g + 1] - L.first_tile[g], m, n);
+      m = m * UNIT + (PAIR ? rank * kBM : 0);
       t.m0 = m + L.first_row[g];
       t.n0 = n * out_cols;
       t.rows = min(kBM, L.rows[g] - m);
@@ -690,6 +701,9 @@ cudaError_t launch(LinearArgs& p, int slots, cudaStream_t s) {
   p.m_tiles = (p.M + C::UNIT_ROWS - 1) / C::UNIT_ROWS;
   p.n_tiles = (p.N + out_cols - 1) / out_cols;
   p.second = EPI == kEpiSwiglu ? p.N : BN / 2;
+  // as many rows as columns at a time: band * UNIT_ROWS = slots / band * BN
+  p.band = 1;
+  while ((p.band + 1) * (p.band + 1) * C::UNIT_ROWS <= slots * BN) ++p.band;
   cudaError_t e;
   if constexpr (BN < 256) {
     if (p.split > 1) {
