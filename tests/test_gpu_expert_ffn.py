@@ -86,6 +86,18 @@ def test_layer_and_its_gradients(T, H, I, E, k, model, dtype):
         assert err <= 16 * R.half_step(x.dtype), float(err)
 
 
+def test_layer_without_tokens_or_experts():
+    import torch
+    layer, x, ids, p, res = _layer(20, 128, 72, 3, 2, 3, "bfloat16")
+    out, kept = layer(x[:0], ids[:0], p[:0], keep=True)
+    dx, dp, d13, d2 = layer.grad(out, kept)
+    assert out.shape == dx.shape == (0, 128) and dp.shape == (0, 2) and not d13.any() and not d2.any()
+    ids.fill_(77)  # all held elsewhere
+    out, kept = layer(x, ids, p, res, keep=True)
+    assert torch.equal(out, res)
+    assert all(not g.any() for g in layer.grad(res, kept))
+
+
 def test_layer_in_a_graph_and_two_layers_at_once():
     import torch
     a, x, ids, p, res = _layer(300, 264, 136, 8, 2, 8, "bfloat16")

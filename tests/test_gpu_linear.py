@@ -76,6 +76,64 @@ def test_linear_larger(M, N, K):
     assert torch.equal(out, api.linear(x, w, b, residual=res, out_dtype=torch.float32))
 
 
+# Sizes at which the plan takes each tile form (64, 128 and 256 columns, CTA pairs, K over a cluster) with 152 SMs,
+# for each of the three epilogues
+FORMS = [(777, 4240, 72), (135, 1560, 2824), (2600, 4640, 72), (390, 4944, 584), (1300, 4448, 72), (260, 4872, 40),
+         (135, 776, 2856), (135, 4872, 584)]
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+@pytest.mark.parametrize("act,dtype", [(None, "bfloat16"), ("gelu", "float16"), ("swiglu", "bfloat16")])
+def test_linear_tile_forms(M, N, K, act, dtype):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    x, w, b, res = _inputs(M, N, K, dtype, act, "same", True, seed=M)
+    limits = (1.5, 0.75) if act == "swiglu" else (INF, INF)
+    buf = torch.full((M + 1, N + 16), float("nan"), dtype=x.dtype, device="cuda")
+    out, z = api.linear(x, w, b, act, res, *limits, preact=True, out=buf[1:, 8:N + 8])
+    _check(x, w, b, res, act, limits, x.dtype, out, z)
+    assert buf[0].isnan().all() and buf[:, :8].isnan().all() and buf[:, N + 8:].isnan().all()
+    _check(x, w, None, None, act, limits, torch.float32, api.linear(x, w, None, act, None, *limits, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 1168, 2944), (3300, 3128, 72), (70, 3984, 2960), (777, 776, 2784), (2100, 16, 16),
+                                   (1300, 72, 2688), (135, 2856, 1544), (4100, 72, 2968), (777, 584, 2768)])
+@pytest.mark.parametrize("act,dtype", [(None, "float16"), ("swiglu", "bfloat16")])
+def test_linear_grad_tile_forms(M, N, K, act, dtype):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x, w, _, _ = _inputs(M, N, K, dtype, act, None, False, seed=N)
+    dy = _randn(g, M, N + 8).to(x.dtype)[:, :N]
+    z = None if act is None else (2 * _randn(g, M, 2 * N)).to(x.dtype)
+    buf = torch.full((M + 1, K + 16), float("nan"), dtype=x.dtype, device="cuda")
+    dx, dw, db = api.linear_grad(dy, x, w, z, act, 1.5, 0.75, bias=True, out=buf[1:, 8:K + 8])
+    for got, (ref, tol) in zip((dx, dw, db), R.linear_grad(dy, x, w, z, act, (1.5, 0.75), x.dtype)):
+        R.check(got, ref, tol)
+    assert buf[0].isnan().all() and buf[:, :8].isnan().all() and buf[:, K + 8:].isnan().all()
+
+
+def test_offsets_beyond_32_bits():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    M, N, K = 600000, 4096, 64
+    x, w, b, _ = _inputs(M, N, K, "bfloat16", None, "same", False, pad=0)
+    out = api.linear(x, w, b)  # 2.5e9 elements
+    for at in (slice(0, 300), slice(524200, 524400), slice(M - 300, M)):
+        _check(x[at], w, b, None, None, (INF, INF), out.dtype, out[at])
+    # dy's rows lie that far apart too; dx by its rows, dw over all of them
+    dx, dw, _ = api.linear_grad(out, x, w)
+    (rx, tx), _, _ = R.linear_grad(out[-300:], x[-300:], w, None, None, (INF, INF), x.dtype)
+    R.check(dx[-300:], rx, tx)
+    dw64 = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(dw64)
+    for s in range(0, M, 20000):
+        d, v = out[s:s + 20000].double(), x[s:s + 20000].double()
+        dw64 += d.T @ v
+        mag += d.abs().T @ v.abs()
+    R.check(dw, dw64, R.rounded(dw64, mag * ((M / 16 * 2 + 40) * R.U32), dw.dtype))
+
+
 def test_rows_depend_on_themselves_alone_and_extremes():
     import torch
     from nvfp4_mixture_experts_expert_gb300 import api
@@ -208,8 +266,12 @@ def _experts(T, k, E, model, K, N, dtype, act, bias, seed=0, align=1, skew=False
     return rows, w, b, res, order
 
 
+# the last nine: the tile forms, as above
 EXPERTS = [(1, 6, 32, 32, 264, 136), (9, 2, 5, 10, 72, 264), (40, 4, 12, 24, 520, 72), (300, 3, 7, 7, 264, 200),
-           (1500, 2, 5, 5, 136, 1032), (700, 8, 100, 130, 72, 40)]
+           (1500, 2, 5, 5, 136, 1032), (700, 8, 100, 130, 72, 40),
+           (379, 2, 5, 5, 72, 3496), (1573, 2, 5, 5, 72, 3472), (68, 2, 5, 5, 680, 3856), (927, 2, 3, 3, 72, 2840),
+           (70, 2, 3, 3, 584, 2632), (1381, 2, 5, 5, 1968, 40), (64, 2, 5, 5, 1064, 2288), (2836, 2, 5, 5, 1992, 64),
+           (392, 2, 5, 5, 1984, 616)]
 
 
 def _slices(order):
@@ -299,6 +361,13 @@ def test_refusals_of_the_python_calls():
                  lambda: api.expert_linear(rows, w, order), lambda: api.expert_linear(rows, we[:1], order),
                  lambda: api.expert_linear(rows, we, order, bias=b)):
         with pytest.raises(ValueError):
+            call()
+    few = rows[:11]  # fewer than the order's tables name
+    for call in (lambda: api.expert_linear(few, we, order), lambda: api.expert_linear_grad(res[:11], few, we, order),
+                 lambda: api.combine_tokens(few, torch.ones(12, 1, device="cuda"), order),
+                 lambda: api.combine_tokens_grad(x, few, torch.ones(12, 1, device="cuda"), order),
+                 lambda: api.sort_tokens_grad(few, order)):
+        with pytest.raises(ValueError, match="rows of the order"):
             call()
     for call in (lambda: api.linear(x[:, :20], w[:, :20].contiguous()), lambda: api.linear(x, w[:12].contiguous()),
                  lambda: api.linear(x, w, activation="swiglu", gate_limit=-1.0)):

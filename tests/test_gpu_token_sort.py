@@ -112,6 +112,32 @@ def test_no_local_expert_and_no_tokens():
     assert api.combine_tokens_grad(x, rows, p, order)[1].shape == (0, 2)
 
 
+def test_offsets_beyond_32_bits():
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    T, H, E = 300000, 4096, 7
+    x = torch.randn(T, H, dtype=torch.bfloat16, device="cuda")
+    ids = _ids(T, 2, E).cuda()
+    rows, order = api.sort_tokens(x, ids, E)  # 2.5e9 elements
+    src = order.source.long() // 2
+    assert torch.equal(order.source.sort().values, torch.arange(2 * T, dtype=torch.int32, device="cuda"))
+    for s in (0, 524200, 2 * T - 1000):
+        assert torch.equal(rows[s:s + 1000], x[src[s:s + 1000]])
+    p = torch.rand(T, 2, device="cuda")
+    out = api.combine_tokens(rows, p, order)
+    dx = api.sort_tokens_grad(rows, order)
+    drows, dp = api.combine_tokens_grad(x, rows, p, order)
+    for at in (slice(0, 500), slice(T - 500, T)):
+        v = rows[order.inverse[at].long()].double()
+        w = p[at, :, None].double()
+        R.check(out[at], (w * v).sum(1), R.rounded((w * v).sum(1), (w * v).abs().sum(1) * (3 * R.U32), out.dtype))
+        R.check(dx[at], v.sum(1), R.rounded(v.sum(1), v.abs().sum(1) * (2 * R.U32), out.dtype))
+        want = w * x[at, None, :].double()
+        R.check(drows[order.inverse[at].long()], want, R.rounded(want, want.abs() * R.U32, out.dtype))
+        dot = v * x[at, None, :].double()
+        R.check(dp[at], dot.sum(2), dot.abs().sum(2) * ((H / 64 + 24) * R.U32))
+
+
 def test_non_finite_rows_stay_their_own():
     import torch
     from nvfp4_mixture_experts_expert_gb300 import api
