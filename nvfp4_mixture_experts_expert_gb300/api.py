@@ -328,32 +328,23 @@ def sort_tokens(x, topk_ids, E, experts_start=0, align=1, out=None, stream=None)
     return rows, TokenOrder(*tables, align)
 
 
-def _holds(rows, order: TokenOrder, name):
-    """The order's tables point into as many rows as sort_tokens returned."""
-    if rows.dim() != 2 or rows.shape[0] < order.source.shape[0]:
-        raise ValueError(f"{name} must have the {order.source.shape[0]} rows of the order, not {list(rows.shape)}")
-
-
 def sort_tokens_grad(grad_rows, order: TokenOrder, out=None, stream=None):
     """The gradient of sort_tokens' x from that of its rows: each token's rows added up."""
-    _holds(grad_rows, order, "grad_rows")
-    return C.sort_tokens_grad(grad_rows, order.inverse, out, _handle(stream))
+    return C.sort_tokens_grad(grad_rows, order.inverse, order.source, out, _handle(stream))
 
 
 def combine_tokens(rows, weights, order: TokenOrder, residual=None, out=None, stream=None):
     """out[t] = residual[t] + sum over j of weights[t][j] * (row of token t at its j-th
     expert) (see nvfp4_combine_tokens): rows bf16, f16 or f32 [capacity, H], weights f32
     [T, top_k], residual of rows' type [T, H] (rows may be strided), out may be it."""
-    _holds(rows, order, "rows")
-    return C.combine_tokens(rows, weights, order.inverse, residual, out, _handle(stream))
+    return C.combine_tokens(rows, weights, order.inverse, order.source, residual, out, _handle(stream))
 
 
 def combine_tokens_grad(grad_out, rows, weights, order: TokenOrder, out=None, stream=None):
     """The gradients of combine_tokens' rows (into out, if given; rows behind the last
     expert's are not written) and of its weights (f32).  That of residual is grad_out."""
-    _holds(rows, order, "rows")
-    return C.combine_tokens_grad(grad_out, rows, weights, order.offsets, order.counts, order.inverse, order.align, out,
-                                 _handle(stream))
+    return C.combine_tokens_grad(grad_out, rows, weights, order.offsets, order.counts, order.inverse, order.source,
+                                 order.align, out, _handle(stream))
 
 
 _ACTIVATIONS = {None: B.NVFP4_ACT_NONE, "relu": B.NVFP4_ACT_RELU, "silu": B.NVFP4_ACT_SILU, "gelu": B.NVFP4_ACT_GELU,
@@ -403,9 +394,8 @@ def expert_linear(rows, w, order: TokenOrder, bias=None, activation=None, residu
     """linear for the rows of each expert in sort_tokens' order: w [E, N, K] ([E, 2N, K]
     for "swiglu", as MoEWeights has them), bias [E, N].  Rows that belong to no expert
     are neither used nor written: out keeps what it has there, a new tensor anything."""
-    _holds(rows, order, "rows")
-    y, z = C.linear(rows, w, (order.offsets, order.counts), bias, _activation(activation), gate_limit, up_limit,
-                    residual, _f32(out_dtype, out, rows), preact, out, _handle(stream))
+    y, z = C.linear(rows, w, (order.offsets, order.counts, order.source), bias, _activation(activation), gate_limit,
+                    up_limit, residual, _f32(out_dtype, out, rows), preact, out, _handle(stream))
     return (y, z) if preact else y
 
 
@@ -413,9 +403,8 @@ def expert_linear_grad(grad, rows, w, order: TokenOrder, preact=None, activation
                        bias=False, inputs=True, weights=True, out=None, stream=None):
     """linear_grad for the rows of each expert: the gradients of rows (written where
     expert_linear writes), w and bias; an expert without rows has zeros."""
-    _holds(rows, order, "rows")
-    return C.linear_grad(grad, rows, w, (order.offsets, order.counts), preact, _activation(activation), gate_limit,
-                         up_limit, bias, inputs, weights, out, _handle(stream))
+    return C.linear_grad(grad, rows, w, (order.offsets, order.counts, order.source), preact, _activation(activation),
+                         gate_limit, up_limit, bias, inputs, weights, out, _handle(stream))
 
 
 class ExpertFFN:

@@ -29,7 +29,7 @@ __device__ __forceinline__ float activate(int act, float z) {
     case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case kActSilu: return silu(z);
     case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    case kActGeluTanh: return z * sigmoid(1.59576912f * (z + 0.044715f * z * z * z));  // (1 + tanh(a)) / 2 = sigmoid(2 a)
+    case kActGeluTanh: return z * sigmoid(1.59576912f * (z + 0.044715f * z * z * z));  // (1 + tanh a) / 2 = sigmoid 2a
     default: return z;
   }
 }

@@ -21,7 +21,8 @@ cudaError_t clusters_that_fit(const Fit** out) {
   return fit.get(dev, out, [](Fit& f) {
     if (const cudaError_t e = configure<128, true, false, kEpiPlain>()) return e;
     if (const cudaError_t e = configure<256, false, true, kEpiPlain>()) return e;
-    if (const cudaError_t e = max_clusters(linear_gemm_kernel<128, true, false, kEpiPlain>, kThreads, Cfg<128, false>::SMEM, f.split))
+    if (const cudaError_t e = max_clusters(linear_gemm_kernel<128, true, false, kEpiPlain>, kThreads,
+                                           Cfg<128, false>::SMEM, f.split))
       return e;
     return max_clusters(linear_gemm_kernel<256, false, true, kEpiPlain>, kThreads, Cfg<256, true>::SMEM, f.pair);
   });
@@ -29,11 +30,19 @@ cudaError_t clusters_that_fit(const Fit** out) {
 
 }  // namespace
 
-cudaError_t launch_linear_plain(LinearArgs& p, int slots, cudaStream_t s) { return launch_form<kEpiPlain>(p, slots, s); }
+cudaError_t launch_linear_plain(LinearArgs& p, int slots, cudaStream_t s) {
+  return launch_form<kEpiPlain>(p, slots, s);
+}
 
-// The plan whose K-blocks take least time, as for the FP8 linear: columns of a
-// tile by its rounds of tiles over the SMs, and where there is one round with SMs to
-// spare, CTAs that share a tile's K.
+// The plan that takes least time by the times of a K-block and of a tile's epilogue
+// (beside the next tile's products) in each form, and of the join where the CTAs of a
+// cluster share a tile's K (one round of tiles with SMs to spare).  Measured: pairs 25.7
+// us for 1024 x 4096 x 4096 (256 columns 28.7, 128 35), 128 columns 20 for 512 x 4096 x
+// 4096 (pairs 25, 64 columns 28), 128 columns with four CTAs a tile 11.7 for 16 x 4096 x
+// 4096 (one 19.3), 64 columns with eight 8.9 for 64 x 256 x 8192 (one 24.8).  Weight
+// gradients of groups run as single CTAs: the rows behind a group's last would have to
+// be set to zero in both CTAs' operands (remote stores and a fence of the cluster: 521
+// us instead of 427 for 32 groups of 384 rows, 4096 x 4096).
 cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms) {
   const Fit* fit = nullptr;
   const cudaError_t e = clusters_that_fit(&fit);
@@ -41,7 +50,8 @@ cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms) {
   struct Form {
     int bn, pair, block_ns, tile_ns, join_ns;
   };
-  constexpr Form kForms[4] = {{256, 1, 310, 3100, 0}, {256, 0, 385, 2700, 0}, {128, 0, 250, 1600, 4500}, {64, 0, 190, 1000, 3000}};
+  constexpr Form kForms[4] = {
+      {256, 1, 310, 3100, 0}, {256, 0, 385, 2700, 0}, {128, 0, 250, 1600, 4500}, {64, 0, 190, 1000, 3000}};
   const bool pairs = p.ep.act == kActSwiglu;
   const int64_t k = p.counts && p.by_k ? (p.K + p.G - 1) / p.G : p.K;  // of a group, on average
   const int64_t kbs = (k + kBK - 1) / kBK;
@@ -50,9 +60,12 @@ cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms) {
     const int rows = f.pair ? 2 * kBM : kBM, out_cols = pairs ? f.bn / 2 : f.bn;
     const int64_t slots = f.pair ? fit->pair.most[2] : num_sms;
     if (slots == 0 || (f.pair && p.by_k && p.counts)) continue;
-    // rows of groups: half a tile more for each
-    const int64_t mt = p.by_k ? (int64_t)p.G * ((p.M + rows - 1) / rows)
-                              : (p.M + rows - 1) / rows + (p.counts ? (p.G + 1) / 2 : 0);
+    // rows of groups: half a tile more for each that can have any, at least one
+    const int64_t some = p.M < p.G ? p.M : p.G, whole = (p.M + rows - 1) / rows;
+    const int64_t mt = p.by_k               ? (int64_t)p.G * whole
+                       : !p.counts          ? whole
+                       : whole > some / 2   ? whole + some / 2
+                                            : some;
     const int64_t tiles = mt * ((p.N + out_cols - 1) / out_cols);
     for (int c = 1; c <= (f.bn < 256 && !p.counts ? kMaxSplit : 1) && c <= kbs; ++c) {
       if (c > 1 && (tiles * c > num_sms || tiles > fit->split.most[c])) continue;

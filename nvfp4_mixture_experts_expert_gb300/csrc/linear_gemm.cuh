@@ -1,6 +1,6 @@
 // 16-bit matrix products on the 5th-generation tensor cores with bias, activation
 // and residual in the epilogue, over one matrix or over groups of rows (see
-// nvfp4_linear, nvfp4_expert_linear and their gradients):
+// nvfp4_linear and nvfp4_linear_grad):
 //
 //   out[m][n] = act(sum_k A[m][k] * B[n][k] + bias[n]) + residual[m][n]
 //
@@ -18,11 +18,29 @@
 // behind the group's last are set to zero in the ring before the product.
 //
 // Persistent, tiles of 128 x BN, FP32 accumulators in TMEM, two of them, so that a
-// tile's epilogue runs beside the next one's products.  Where a problem has few
+// tile's epilogue runs beside the next one's products.  Large problems run as CTA
+// pairs (cta_group::2): 256 x 256 tiles, each CTA with its 128 rows of A and half of B,
+// both CTAs' copies counted on the issuing CTA's barrier.  Where a problem has few
 // tiles, K is split over the CTAs of a cluster, which add their sums through shared
 // memory.  10 warps: 0 TMA, 1 MMA issue (and TMEM), 2 to 9 epilogue (a lane quarter
 // and half of the columns each).  Every wait is bounded and reports in the
 // library's status word.
+//
+// Bound: the tensor pipe, then power.  8192 x 4096 x 4096 takes 143 us in a short row
+// of calls (1.92 PFLOP/s; tensor pipe 91 % busy; cuBLAS 137) and 151 over seconds
+// (cuBLAS 154), with bias and residual 150.  What made the difference, from 234 us:
+//   - pairs (163 us): a CTA alone copies 48 KB and its MMAs read 48 KB of shared memory a
+//     K-block, which is more than the 512 cycles of its products carry (385 ns a block
+//     instead of 310);
+//   - the next stage's barrier asked while this stage's products are issued (152), the
+//     second CTA's copies counted directly instead of relayed by a warp (148), a wait that
+//     sleeps in the epilogue;
+//   - tiles in bands (144);
+//   - an epilogue thread that keeps a row's 16 or 32 columns and stores whole 32-byte
+//     sectors; spilled registers cost most where an output is large (8192 x 8192 x 64:
+//     174 us with them, 38 without; 4 TB/s of writes, what a fill of memory reaches).
+// Built and not faster: the output through shared memory and bulk copies (42 to 49 us
+// there), two K-blocks a stage for pairs, the producer asking ahead as well.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -45,16 +63,16 @@ constexpr int kEpiWarp0 = 2;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kMaxGroups = 256;
-constexpr int kBiasBytes = 2 * 128 * 4;  // an epilogue warp's: the bias of up to 128 columns, SwiGLU of both halves
-constexpr int kChunkBytes = 64 * 128;       // 64 columns x 64 rows of an operand read along columns
+constexpr int kBiasBytes = 2 * 128 * 4;    // an epilogue warp's: the bias of up to 128 columns, SwiGLU of both halves
+constexpr int kChunkBytes = 64 * 128;      // 64 columns x 64 rows of an operand read along columns
 
 template <int BN, bool PAIR>
 struct Cfg {
   static constexpr int A_BYTES = kBM * kBK * 2;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // of B that this CTA holds
   static constexpr int BLOCK_BYTES = A_BYTES + B_ROWS * kBK * 2;  // a K-block's operands
-  // K-blocks of a ring stage: two take a small tile's products past what a stage costs
-  // the warps (128 columns 275 -> 250 ns a block, 64 245 -> 190); a pair's lose 5 %
+  // K-blocks of a ring stage: with two, a small tile's stage takes longer than its waits
+  // and issue (128 columns 250 ns a block instead of 275, 64 190 instead of 245); pairs lose
   static constexpr int BLOCKS = BN == 256 ? 1 : 2;
   static constexpr int STAGE_BYTES = BLOCKS * BLOCK_BYTES;
   static constexpr int STAGES = PAIR ? 6 : BN == 64 ? 4 : BN == 128 ? 3 : 4;
@@ -67,8 +85,8 @@ struct Cfg {
 };
 
 // Shared-memory addresses: ring, bias, barriers (full: a stage has landed;
-// empty: its products are done; acc_full, acc_empty: an accumulator), tiles before
-// each group.
+// empty: its products are done; acc_full, acc_empty: an accumulator), the groups'
+// tables.
 struct Smem {
   uint32_t stages, bias, full, empty, acc_full, acc_empty;
   uint32_t* tmem_slot;
@@ -97,8 +115,8 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
 }
 
 // This CTA's part of a tile: its group, where its operands start, how many of its
-// rows exist (in a pair's second half none, or less, may), and its contraction (K-blocks kb0 .. kb1 of this CTA; k0: first row with by_k; k_end:
-// length).
+// rows exist (none, or less, where a pair's second half begins behind them), and its
+// contraction (K-blocks kb0 .. kb1 of this CTA; k0: first row with by_k; k_end: length).
 struct Tile {
   int g, m0, n0, rows, kb0, kb1, k0, k_end;
   int64_t out_row;
@@ -260,10 +278,13 @@ __device__ void load_loop(const LinearArgs& p, const Smem& L) {
       if (leader) {
         const uint32_t bar = full0 + 8 * stage;
         const int blocks = min(C::BLOCKS, kb1 - kb);
-        if (!PAIR || walk.rank == 0) mbar_arrive_expect_tx(L.full + 8 * stage, (PAIR ? 2 : 1) * blocks * C::BLOCK_BYTES);
+        const uint32_t at = L.stages + stage * C::STAGE_BYTES;
+        if (!PAIR || walk.rank == 0)
+          mbar_arrive_expect_tx(L.full + 8 * stage, (PAIR ? 2 : 1) * blocks * C::BLOCK_BYTES);
 #pragma unroll
         for (int i = 0; i < C::BLOCKS; ++i)
-          if (i < blocks) load_block<BN, PAIR, SWIGLU>(p, t, walk.rank, L.stages + stage * C::STAGE_BYTES + i * C::BLOCK_BYTES, t.k0 + (kb + i) * kBK, bar);
+          if (i < blocks)
+            load_block<BN, PAIR, SWIGLU>(p, t, walk.rank, at + i * C::BLOCK_BYTES, t.k0 + (kb + i) * kBK, bar);
       }
       __syncwarp();
       issued |= 1u << stage;
@@ -358,11 +379,12 @@ __device__ void mma_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
 #pragma unroll
         for (int j = 0; j < C::BLOCKS; ++j)
           if (j < blocks) {
+            const uint32_t block = j * (C::BLOCK_BYTES >> 4);
 #pragma unroll
             for (int i = 0; i < kBK / 16; ++i)
               if (j + 1 < blocks || i < steps)
-                tc_mma_f16<PAIR>(d, ad + j * (C::BLOCK_BYTES >> 4) + i * a_step, bd + j * (C::BLOCK_BYTES >> 4) + i * b_step,
-                                 idesc, kb != t.kb0 || i != 0 || j != 0);
+                tc_mma_f16<PAIR>(d, ad + block + i * a_step, bd + block + i * b_step, idesc,
+                                 kb != t.kb0 || i != 0 || j != 0);
           }
         const bool done = kb + C::BLOCKS >= t.kb1;
         if constexpr (PAIR) {
@@ -394,7 +416,10 @@ __device__ __forceinline__ void st_shared_f4(uint32_t at, uint32_t a, uint32_t b
 }
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
   float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
@@ -453,8 +478,8 @@ template <int BN, bool SPLIT, bool PAIR, int EPI>
 __device__ void epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
   using C = Cfg<BN, PAIR>;
   constexpr bool SWIGLU = EPI == kEpiSwiglu;
-  constexpr int COLS = SWIGLU ? BN / 4 : BN / 2;                     // output columns of this warp
-  constexpr int W = EPI == kEpiPlain && COLS >= 32 ? 32 : 16;        // held at a time
+  constexpr int COLS = SWIGLU ? BN / 4 : BN / 2;               // output columns of this warp
+  constexpr int W = EPI == kEpiPlain && COLS >= 32 ? 32 : 16;  // held at a time
   volatile int* abort = L.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
@@ -718,7 +743,8 @@ cudaError_t launch(LinearArgs& p, int slots, cudaStream_t s) {
   const int64_t tiles = m * p.n_tiles;
   const int grid = (int)(tiles < slots ? tiles : slots);
   if (PAIR)
-    return launch_split<const LinearArgs>(linear_gemm_kernel<BN, false, PAIR, EPI>, 2 * grid, kThreads, C::SMEM, 2, s, p);
+    return launch_split<const LinearArgs>(linear_gemm_kernel<BN, false, PAIR, EPI>, 2 * grid, kThreads, C::SMEM, 2, s,
+                                          p);
   return launch_kernel(linear_gemm_kernel<BN, false, PAIR, EPI>, dim3(grid), dim3(kThreads), C::SMEM, s, true, p);
 }
 

@@ -330,6 +330,13 @@ const int32_t* table(const at::Tensor& t, const char* name, at::IntArrayRef shap
   return static_cast<const int32_t*>(t.data_ptr());
 }
 
+// The order's tables point into as many rows as sort_tokens returned.
+void holds(const at::Tensor& rows, const char* name, PyObject* source) {
+  const int64_t n = tensor(source, "the order's source").numel();
+  TORCH_CHECK_VALUE(rows.dim() == 2 && rows.size(0) >= n, name, " must have the ", n, " rows of the order, not ",
+                    rows.sizes());
+}
+
 // An output: the given matrix [T, cols], or a new one.
 at::Tensor output(PyObject* o, const Where& at, at::ScalarType dtype, int64_t T, int64_t cols, int64_t& ld) {
   ld = cols;
@@ -380,14 +387,14 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// drows, inverse, out | None, stream | None
+// drows, inverse, source, out | None, stream | None
 PyObject* sort_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 4)) return nullptr;
+  if (!count(n, 5)) return nullptr;
   const at::Tensor &d = tensor(a[0], "grad_rows"), &inv = tensor(a[1], "the order's inverse");
-  const std::optional<cudaStream_t> stream = handle(a[3]);
+  const std::optional<cudaStream_t> stream = handle(a[4]);
   need_cuda(d, "grad_rows");
-  two_dims(d, "grad_rows");
+  holds(d, "grad_rows", a[2]);
   two_dims(inv, "the order's inverse");
   const Where at(d, stream);
   const int type = type_of(d, "grad_rows", true);
@@ -395,20 +402,20 @@ PyObject* sort_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t ld_d = rows(d, "grad_rows", d.scalar_type(), d.size(0), H, at.dev);
   const int32_t* inverse = table(inv, "the order's inverse", {T, k}, at.dev);
   int64_t ld;
-  const at::Tensor out = output(a[2], at, d.scalar_type(), T, H, ld);
+  const at::Tensor out = output(a[3], at, d.scalar_type(), T, H, ld);
   const int rc = nvfp4_sort_tokens_grad(d.data_ptr(), ld_d, type, inverse, T, H, (int)k, out.data_ptr(), ld, at.stream);
   return rc == NVFP4_OK ? THPVariable_Wrap(out) : failed(rc);
   END_HANDLE_TH_ERRORS
 }
 
-// rows, weights, inverse, residual | None, out | None, stream | None
+// rows, weights, inverse, source, residual | None, out | None, stream | None
 PyObject* combine_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 6)) return nullptr;
+  if (!count(n, 7)) return nullptr;
   const at::Tensor &r = tensor(a[0], "rows"), &w = tensor(a[1], "weights"), &inv = tensor(a[2], "the order's inverse");
-  const std::optional<cudaStream_t> stream = handle(a[5]);
+  const std::optional<cudaStream_t> stream = handle(a[6]);
   need_cuda(r, "rows");
-  two_dims(r, "rows");
+  holds(r, "rows", a[3]);
   two_dims(inv, "the order's inverse");
   const Where at(r, stream);
   const int type = type_of(r, "rows", true);
@@ -416,27 +423,27 @@ PyObject* combine_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t ld_r = rows(r, "rows", r.scalar_type(), r.size(0), H, at.dev);
   const int32_t* inverse = table(inv, "the order's inverse", {T, k}, at.dev);
   whole(w, "weights", at::kFloat, {T, k}, at.dev);
-  const Rows res(a[3], "residual", r.scalar_type(), T, H, at.dev);
+  const Rows res(a[4], "residual", r.scalar_type(), T, H, at.dev);
   int64_t ld;
-  const at::Tensor out = output(a[4], at, r.scalar_type(), T, H, ld);
+  const at::Tensor out = output(a[5], at, r.scalar_type(), T, H, ld);
   const int rc = nvfp4_combine_tokens(r.data_ptr(), ld_r, type, static_cast<const float*>(w.data_ptr()), inverse,
                                       res.p, res.ld, T, H, (int)k, out.data_ptr(), ld, at.stream);
   return rc == NVFP4_OK ? THPVariable_Wrap(out) : failed(rc);
   END_HANDLE_TH_ERRORS
 }
 
-// dout, rows, weights, offsets, counts, inverse, align, out | None, stream | None
+// dout, rows, weights, offsets, counts, inverse, source, align, out | None, stream | None
 PyObject* combine_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 9)) return nullptr;
+  if (!count(n, 10)) return nullptr;
   const at::Tensor &d = tensor(a[0], "grad_out"), &r = tensor(a[1], "rows"), &w = tensor(a[2], "weights"),
                    &off = tensor(a[3], "the order's offsets"), &cnt = tensor(a[4], "the order's counts"),
                    &inv = tensor(a[5], "the order's inverse");
-  const int align = small_number(a[6], "align");
-  const std::optional<cudaStream_t> stream = handle(a[8]);
+  const int align = small_number(a[7], "align");
+  const std::optional<cudaStream_t> stream = handle(a[9]);
   need_cuda(d, "grad_out");
   two_dims(d, "grad_out");
-  two_dims(r, "rows");
+  holds(r, "rows", a[6]);
   two_dims(inv, "the order's inverse");
   const Where at(d, stream);
   const int type = type_of(d, "grad_out", true);
@@ -448,7 +455,7 @@ PyObject* combine_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 *counts = table(cnt, "the order's counts", {E}, at.dev),
                 *offsets = table(off, "the order's offsets", {E + 1}, at.dev);
   int64_t ld;
-  const at::Tensor out = output(a[7], at, d.scalar_type(), R, H, ld);
+  const at::Tensor out = output(a[8], at, d.scalar_type(), R, H, ld);
   at::Tensor dw = at.empty({T, k}, at::kFloat);
   const int rc = nvfp4_combine_tokens_grad(d.data_ptr(), ld_d, r.data_ptr(), ld_r, type,
                                            static_cast<const float*>(w.data_ptr()), offsets, counts, inverse, T, H,
@@ -460,7 +467,7 @@ PyObject* combine_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // What the linear and its gradient share: sizes, activation (a number) with its
-// limits, and (offsets, counts) of the experts or None.
+// limits, and (offsets, counts, source) of the experts' order or None.
 struct Shape {
   nvfp4_linear_shape s = {};
   int64_t wide, groups;
@@ -488,14 +495,15 @@ struct Shape {
     }
     TORCH_CHECK_VALUE(groups >= 1 && groups <= 256, "1 to 256 experts, not ", groups);
     whole(w, "w", x.scalar_type(), {groups, wide, s.K}, dev);
-    TORCH_CHECK_VALUE(PyTuple_Check(order) && PyTuple_GET_SIZE(order) == 2, "offsets and counts expected");
+    TORCH_CHECK_VALUE(PyTuple_Check(order) && PyTuple_GET_SIZE(order) == 3, "offsets, counts and source expected");
+    holds(x, "rows", PyTuple_GET_ITEM(order, 2));
     s.groups = (int)groups;
     s.offsets = table(tensor(PyTuple_GET_ITEM(order, 0), "the order's offsets"), "the order's offsets", {groups + 1}, dev);
     s.counts = table(tensor(PyTuple_GET_ITEM(order, 1), "the order's counts"), "the order's counts", {groups}, dev);
   }
 };
 
-// x, w, (offsets, counts) | None, bias | None, activation, gate_limit, up_limit, residual | None, f32, preact,
+// x, w, (offsets, counts, source) | None, bias | None, activation, gate_limit, up_limit, residual | None, f32, preact,
 // out | None, stream | None -> (out, preact | None)
 PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -533,7 +541,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// dy, x, w, (offsets, counts) | None, preact | None, activation, gate_limit, up_limit, bias, inputs, weights,
+// dy, x, w, (offsets, counts, source) | None, preact | None, activation, gate_limit, up_limit, bias, inputs, weights,
 // out | None, stream | None -> (dx, dw, dbias), None where not asked for
 PyObject* linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
