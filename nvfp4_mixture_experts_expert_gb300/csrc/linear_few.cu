@@ -12,7 +12,10 @@
 //
 // Bound: reading w.  Launches are chained, and a block has its part of w fetched
 // into L2 before it waits for the kernel before (not with experts: which of them
-// have rows is that kernel's result).
+// have rows is that kernel's result).  1 x 4096 x 4096 takes 7.4 us in a row of calls
+// with different w (4.5 TB/s; floor 4.9; 8.0 without the fetch): launch, first loads and
+// the join of 16 warps are ~2.5 of them.  Built and not faster: w and x through a ring of
+// bulk copies, one CTA a SM (14 us; two CTAs 9.5).
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -23,7 +26,12 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWarps = 16;
+// Warps of a block, and blocks a SM: one matrix has few blocks, of which each should
+// have all of its K in flight (1 x 4096 x 4096 7.7 us; with eight warps 11 to 13), the
+// experts together have many, which overlap one's end with the next's beginning (six
+// experts' 4096 x 4096 40 us instead of 44).
+__host__ __device__ constexpr int warps_of(bool experts) { return experts ? 8 : 16; }
+__host__ __device__ constexpr int blocks_of(bool experts) { return experts ? 5 : 2; }
 constexpr int kRows = (int)kLinearFewRows;
 static_assert(kRows == 8, "the N of one mma");
 
@@ -61,8 +69,9 @@ __device__ __forceinline__ int group_with_rows(const LinearFewArgs& p, int nth) 
   return -1;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) linear_few_kernel(const LinearFewArgs p) {
+template <bool BF16, bool EXPERTS>
+__global__ void __launch_bounds__(32 * warps_of(EXPERTS), blocks_of(EXPERTS)) linear_few_kernel(const LinearFewArgs p) {
+  constexpr int kWarps = warps_of(EXPERTS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
   const bool pairs = p.ep.act == kActSwiglu;
@@ -73,7 +82,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_few_kernel(const LinearFew
   __shared__ float sums[kRows][16];
   const uint8_t* w0 = p.w + (int64_t)min(n0 + g, p.ep.N - 1) * bytes;
   const uint8_t* w1 = p.w + (int64_t)(pairs ? p.ep.N + min(n0 + g, p.ep.N - 1) : min(n0 + g + 8, p.ep.N - 1)) * bytes;
-  if (!p.counts) {
+  if constexpr (!EXPERTS) {
     for (int kb = warp; kb < kbs; kb += kWarps) {
       const int off = kb * 128 + q * 32;
       if (off < bytes) {
@@ -84,10 +93,10 @@ __global__ void __launch_bounds__(kWarps * 32) linear_few_kernel(const LinearFew
   }
   pdl_trigger();
   pdl_wait();
-  const int group = p.counts ? group_with_rows(p, blockIdx.y) : 0;
+  const int group = EXPERTS ? group_with_rows(p, blockIdx.y) : 0;
   if (group < 0) return;
-  const int rows = p.counts ? p.counts[group] : p.M;
-  const int64_t row0 = p.counts ? p.offsets[group] : 0;
+  const int rows = EXPERTS ? p.counts[group] : p.M;
+  const int64_t row0 = EXPERTS ? p.offsets[group] : 0;
   w0 += (int64_t)group * p.ep.wide * bytes;
   w1 += (int64_t)group * p.ep.wide * bytes;
   for (int m0 = 0; m0 < rows; m0 += kRows) {
@@ -130,15 +139,21 @@ __global__ void __launch_bounds__(kWarps * 32) linear_few_kernel(const LinearFew
 
 }  // namespace
 
+// One matrix: two passes over w (the second from L2) against a 128-row tile: 16 x 4096 x
+// 4096 11.3 us against 12.4 (8 rows 7.7 against 16; 17 rows 14.9 against 12.4).  Experts
+// (of 32, 4096 x 4096): 1, 2, 3, 4 and 5 tokens of six 40, 59, 85, 115 and 104 us against
+// 57, 92, 87, 125 and 100; 16 tokens 176 against 172.
 bool linear_is_few(int64_t M, int groups) { return groups ? M <= (int64_t)groups : M <= 2 * kLinearFewRows; }
 
 cudaError_t launch_linear_few(const LinearFewArgs& p, cudaStream_t s) {
   const int out_cols = p.ep.act == kActSwiglu ? 8 : 16;
-  // at most as many experts as rows have any (a block for each of 32 experts instead of
-  // the six of one token: 45 us instead of FEW_T1)
+  // at most as many experts as rows have any
   const dim3 grid((p.ep.N + out_cols - 1) / out_cols, p.M < p.G ? p.M : p.G);
-  return launch_kernel(p.ep.type == kTypeBf16 ? linear_few_kernel<true> : linear_few_kernel<false>, grid,
-                       dim3(kWarps * 32), 0, s, true, p);
+  auto go = [&](auto bf16, auto f16, bool experts) {
+    return launch_kernel(p.ep.type == kTypeBf16 ? bf16 : f16, grid, dim3(32 * warps_of(experts)), 0, s, true, p);
+  };
+  return p.counts ? go(linear_few_kernel<true, true>, linear_few_kernel<false, true>, true)
+                  : go(linear_few_kernel<true, false>, linear_few_kernel<false, false>, false);
 }
 
 }  // namespace nvfp4
