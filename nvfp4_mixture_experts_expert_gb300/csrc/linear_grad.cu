@@ -6,7 +6,13 @@
 // tensor cores multiply (half a step of that type for each term of dx and dw; two
 // terms an element would double the products); the sums take it unrounded, in FP32:
 // 8 warps a slab of kSlabRows rows, their sums in order into one partial row a slab,
-// and a second launch adds the slabs of a group in order.  Bound: HBM.
+// and a second launch adds the slabs of a group in order.
+//
+// Bound: HBM and, close to it, the arithmetic of the slope.  12294 x 2048 (bf16) without
+// an activation, sums alone, 10 us (50 MB, floor 7.4), SiLU with dz 27 (150 MB, 22),
+// SwiGLU with dz 49 (250 MB, 37), GELU by erf 44 (its erff and exp).  A kernel for each
+// activation and type: with both chosen inside it 2048 x 6144 took 35 us instead of 17.
+// Slabs of 32 and 128 rows, four rows a warp at a time: the same or up to 40 % slower.
 #include <cuda_runtime.h>
 
 #include "internal.h"

@@ -31,6 +31,9 @@ constexpr int kMaxExperts = 256;
 constexpr int kMaxTopK = 32;
 constexpr int kOrderWarps = 32;
 constexpr int kOrderCtas = 8;
+// 512 assignments of 4096 columns 4.0 us in one launch against 6.3 in two, 1024 5.4
+// against 6.5 (512 columns 4.6 against 5.5); 2048 8.6 against 7.6 (11.7 against 5.6),
+// every block looking through all of them.
 constexpr int kFusedAssignments = 1024;
 constexpr int kHeld = 8;  // ids a lane
 
