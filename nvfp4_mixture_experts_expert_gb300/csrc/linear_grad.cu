@@ -207,7 +207,9 @@ __global__ void __launch_bounds__(kWarps * 32) linear_dbias_kernel(const LinearG
 
 int64_t linear_grad_slabs(int64_t M, int groups) { return (M + kSlabRows - 1) / kSlabRows + groups; }
 
-cudaError_t launch_linear_dz(const LinearGradArgs& p, cudaStream_t s) {
+cudaError_t launch_linear_dz(const LinearGradArgs& args, cudaStream_t s) {
+  LinearGradArgs p = args;
+  if (p.partial && !p.counts && p.M <= kSlabRows) p.partial = p.dbias;  // one slab: its sums are the bias's
   const dim3 grid((unsigned)linear_grad_slabs(p.M, p.counts ? p.G : 0), (p.N + 255) / 256);
   auto go = [&](auto bf16, auto f16) {
     return launch_kernel(p.type == kTypeBf16 ? bf16 : f16, grid, dim3(kWarps * 32), 0, s, true, p);
@@ -220,7 +222,7 @@ cudaError_t launch_linear_dz(const LinearGradArgs& p, cudaStream_t s) {
                         : p.act == kActSwiglu   ? DZ(kActSwiglu)
                                                 : DZ(kActNone);
 #undef DZ
-  if (e != cudaSuccess || !p.partial) return e;
+  if (e != cudaSuccess || !p.partial || p.partial == p.dbias) return e;
   return launch_kernel(linear_dbias_kernel, dim3((p.wide + 31) / 32, p.G), dim3(kWarps * 32), 0, s, true, p);
 }
 
