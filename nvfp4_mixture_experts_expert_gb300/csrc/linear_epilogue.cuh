@@ -146,68 +146,100 @@ __device__ __forceinline__ void activate_all(int act, float (&z)[N]) {
   }
 }
 
-// Eight consecutive values of a 16-bit or FP32 row.
-__device__ __forceinline__ void load8(const void* p, int64_t at, int type, float (&f)[8]) {
+// N (4 or 8) consecutive values of a 16-bit or FP32 row.
+template <int N>
+__device__ __forceinline__ void load_cols(const void* p, int64_t at, int type, float (&f)[N]) {
   if (type == kTypeF32) {
     const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = q[0], b = q[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 v = q[i];
+      f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+    }
     return;
   }
-  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+  uint32_t u[N / 2];
+  if constexpr (N == 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(q);
+    u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+  } else {
+    const uint2 v = *q;
+    u[0] = v.x, u[1] = v.y;
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpack2(type, u[i], f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < N / 2; ++i) unpack2(type, u[i], f[2 * i], f[2 * i + 1]);
 }
-__device__ __forceinline__ void store8(void* p, int64_t at, int type, const float (&f)[8]) {
+template <int N>
+__device__ __forceinline__ void store_cols(void* p, int64_t at, int type, const float (&f)[N]) {
   if (type == kTypeF32) {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) q[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
     return;
   }
-  uint32_t u[4];
+  uint16_t* q = static_cast<uint16_t*>(p) + at;
+  uint32_t u[N / 2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) u[i] = pack2(type, f[2 * i], f[2 * i + 1]);
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+  for (int i = 0; i < N / 2; ++i) u[i] = pack2(type, f[2 * i], f[2 * i + 1]);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(q) = make_uint4(u[0], u[1], u[2], u[3]);
+  else
+    *reinterpret_cast<uint2*>(q) = make_uint2(u[0], u[1]);
 }
 
-// The bias of eight columns (and, for SwiGLU, of their up columns) of group g.
-__device__ __forceinline__ void load_bias(const LinearEpilogue& p, int g, int col, float (&b)[8], float (&bu)[8]) {
+// What an epilogue's code has to know of the activation: a kernel that is compiled for
+// one kind holds only that code.
+enum LinearEpi { kEpiPlain, kEpiActivation, kEpiSwiglu, kEpiAny };
+
+template <int EPI>
+__device__ __forceinline__ bool is_swiglu(const LinearEpilogue& p) {
+  return EPI == kEpiSwiglu || (EPI == kEpiAny && p.act == kActSwiglu);
+}
+
+// The bias of N columns (and, for SwiGLU, of their up columns) of group g, and their
+// residual: zeros where there is none.
+template <int EPI, int N>
+__device__ __forceinline__ void load_bias(const LinearEpilogue& p, int g, int col, float (&b)[N], float (&bu)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = bu[i] = 0.f;
-  if (!p.bias) return;
+  for (int i = 0; i < N; ++i) b[i] = bu[i] = 0.f;
+  if (!p.bias || col >= p.N) return;
   const int64_t at = (int64_t)g * p.wide + col;
-  load8(p.bias, at, p.bias_type, b);
-  if (p.act == kActSwiglu) load8(p.bias, at + p.N, p.bias_type, bu);
+  load_cols<N>(p.bias, at, p.bias_type, b);
+  if (is_swiglu<EPI>(p)) load_cols<N>(p.bias, at + p.N, p.bias_type, bu);
+}
+template <int N>
+__device__ __forceinline__ void load_residual(const LinearEpilogue& p, int64_t row, int col, float (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = 0.f;
+  if (p.residual) load_cols<N>(p.residual, row * p.ld_residual + col, p.type, r);
 }
 
-// Columns col .. col + 7 of an output row from their sums z (SwiGLU: the gate's, and the up's u).
-__device__ __forceinline__ void finish8(const LinearEpilogue& p, int64_t row, int col, float (&z)[8], float (&u)[8],
-                                        const float (&b)[8], const float (&bu)[8]) {
+// Columns col .. col + N - 1 of an output row from their sums z (SwiGLU: the gate's, and
+// the up's u), bias and residual.
+template <int EPI, int N>
+__device__ __forceinline__ void finish(const LinearEpilogue& p, int64_t row, int col, float (&z)[N], float (&u)[N],
+                                       const float (&b)[N], const float (&bu)[N], const float (&r)[N]) {
+  const bool pairs = is_swiglu<EPI>(p);
+  if (p.bias) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] += b[i];
-  if (p.act == kActSwiglu) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] += bu[i];
+    for (int i = 0; i < N; ++i) z[i] += b[i], u[i] += bu[i];
   }
   if (p.preact) {
-    store8(p.preact, row * p.ld_preact + col, p.type, z);
-    if (p.act == kActSwiglu) store8(p.preact, row * p.ld_preact + p.N + col, p.type, u);
+    store_cols<N>(p.preact, row * p.ld_preact + col, p.type, z);
+    if (pairs) store_cols<N>(p.preact, row * p.ld_preact + p.N + col, p.type, u);
   }
-  if (p.act == kActSwiglu) {
+  if (pairs) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = swiglu(z[i], u[i], p.gate_limit, p.up_limit);
-  } else {
+    for (int i = 0; i < N; ++i) z[i] = swiglu(z[i], u[i], p.gate_limit, p.up_limit);
+  } else if (EPI != kEpiPlain) {
     activate_all(p.act, z);
   }
   if (p.residual) {
-    float r[8];
-    load8(p.residual, row * p.ld_residual + col, p.type, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += r[i];
+    for (int i = 0; i < N; ++i) z[i] += r[i];
   }
-  store8(p.out, row * p.ld_out + col, p.out_type, z);
+  store_cols<N>(p.out, row * p.ld_out + col, p.out_type, z);
 }
 
 }  // namespace nvfp4

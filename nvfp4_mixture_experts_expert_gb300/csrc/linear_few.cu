@@ -127,11 +127,12 @@ __global__ void __launch_bounds__(32 * warps_of(EXPERTS), blocks_of(EXPERTS)) li
     __syncthreads();
     const int per = out_cols / 8, m = threadIdx.x / per, c = threadIdx.x % per * 8, col = n0 + c;
     if (m < here && col < p.ep.N) {
-      float z[8], u[8], bias[8], bias_u[8];
-      load_bias(p.ep, group, col, bias, bias_u);
+      float z[8], u[8], b[8], bu[8], res[8];
+      load_bias<kEpiAny>(p.ep, group, col, b, bu);
+      load_residual(p.ep, row0 + m0 + m, col, res);
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] = sums[m][c + i], u[i] = sums[m][8 + i];
-      finish8(p.ep, row0 + m0 + m, col, z, u, bias, bias_u);
+      finish<kEpiAny>(p.ep, row0 + m0 + m, col, z, u, b, bu, res);
     }
     __syncthreads();
   }

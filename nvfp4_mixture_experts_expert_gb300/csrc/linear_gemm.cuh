@@ -52,9 +52,6 @@
 
 namespace nvfp4 {
 
-// Compiled apart (one source file each), so that a kernel holds only the code that it runs.
-enum LinearEpi { kEpiPlain, kEpiActivation, kEpiSwiglu };
-
 namespace linear_gemm {
 
 constexpr int kBM = 128;
@@ -575,40 +572,53 @@ __device__ void epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem)
 }
 
 // The cluster's CTAs add up the ranges' sums in K order, each its share of the
-// tile's rows, eight output columns a lane.
-template <int BN, bool SWIGLU>
+// tile's rows, four columns a thread.  A thread's columns stay the same from row to row,
+// so their bias is loaded once, and two rows' sums and residuals are in flight: what is
+// loaded only when it is needed adds its trip to memory (300 x 1000 x 3600: the join 4.1
+// us with eight columns and one row at a time, 3.5 so; by bulk copies to the owner of a
+// row 2.9, but the call 12.2 instead of 11.0).
+template <int BN, int EPI>
 __device__ void join_ranges(const LinearArgs& p, const Smem& L) {
+  constexpr bool SWIGLU = EPI == kEpiSwiglu;
+  constexpr int PER = (SWIGLU ? BN / 2 : BN) / 4, STEP = kEpiWarps * 32 / PER;  // threads a row; rows a step
+  static_assert(kEpiWarps * 32 % PER == 0, "whole rows a step");
   Walk<true, false, SWIGLU> walk(p, L, BN);
   Tile t;
   if (!walk.next(t)) return;
-  const int per = walk.out_cols / 8, rank = walk.rank;
-  const int tid = threadIdx.x - kEpiWarp0 * 32;
-  const int r0 = kBM * rank / p.split, r1 = min(kBM * (rank + 1) / p.split, t.rows);
-  for (int i = tid; i < (r1 - r0) * per; i += kEpiWarps * 32) {
-    const int r = r0 + i / per, c = i % per * 8, col = t.n0 + c;
-    if (col >= p.N) continue;
-    float z[8] = {}, u[8] = {}, b[8], bu[8];
-    load_bias(p.ep, t.g, col, b, bu);
-    auto add = [&](float(&s)[8], int at) {
+  const int tid = threadIdx.x - kEpiWarp0 * 32, c = tid % PER * 4, col = t.n0 + c;
+  const int end = col < p.N ? min(kBM * (walk.rank + 1) / p.split, t.rows) : 0;
+  float b[4], bu[4];
+  load_bias<EPI>(p.ep, t.g, col, b, bu);
+  for (int r0 = kBM * walk.rank / p.split + tid / PER; r0 < end; r0 += 2 * STEP) {
+    float res[2][4], s[2][SWIGLU ? 2 : 1][4] = {};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 v[kMaxSplit];
+    for (int j = 0; j < 2; ++j)
+      if (r0 + j * STEP < end) load_residual(p.ep, t.out_row + r0 + j * STEP, col, res[j]);
+#pragma unroll
+    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+      uint4 v[2][kMaxSplit];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = L.stages + ((r0 + j * STEP) * (BN + 4) + c + h * (BN / 2)) * 4;
 #pragma unroll
         for (int q = 0; q < kMaxSplit; ++q)
-          if (q < p.split) v[q] = ld_shared_cluster_v4(mapa_shared(L.stages + (r * (BN + 4) + at + 4 * h) * 4, q));
+          if (q < p.split && r0 + j * STEP < end) v[j][q] = ld_shared_cluster_v4(mapa_shared(at, q));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < kMaxSplit; ++q)
           if (q < p.split) {
-            s[4 * h] += __uint_as_float(v[q].x);
-            s[4 * h + 1] += __uint_as_float(v[q].y);
-            s[4 * h + 2] += __uint_as_float(v[q].z);
-            s[4 * h + 3] += __uint_as_float(v[q].w);
+            s[j][h][0] += __uint_as_float(v[j][q].x);
+            s[j][h][1] += __uint_as_float(v[j][q].y);
+            s[j][h][2] += __uint_as_float(v[j][q].z);
+            s[j][h][3] += __uint_as_float(v[j][q].w);
           }
-      }
-    };
-    add(z, c);
-    if (SWIGLU) add(u, BN / 2 + c);
-    finish8(p.ep, t.out_row + r, col, z, u, b, bu);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (r0 + j * STEP < end)
+        finish<EPI>(p.ep, t.out_row + r0 + j * STEP, col, s[j][0], s[j][SWIGLU], b, bu, res[j]);
   }
 }
 
@@ -690,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   if (p.beside) pdl_wait();  // this kernel's end is also the end of the one it ran beside
   if constexpr (SPLIT) {
     cluster_sync_all();
-    if (warp >= kEpiWarp0) join_ranges<BN, SWIGLU>(p, L);
+    if (warp >= kEpiWarp0) join_ranges<BN, EPI>(p, L);
     __syncwarp();
     cluster_arrive_relaxed();  // the other CTAs' reads of this one's shared memory
     cluster_wait();

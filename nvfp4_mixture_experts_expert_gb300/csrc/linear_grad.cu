@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) linear_dz_kernel(const LinearG
           }
         }
         if (p.dz) {
-          store8(p.dz, at, TYPE, z);
-          if (PAIRS) store8(p.dz, at + p.N, TYPE, u);
+          store_cols<8>(p.dz, at, TYPE, z);
+          if (PAIRS) store_cols<8>(p.dz, at + p.N, TYPE, u);
         }
       }
     }

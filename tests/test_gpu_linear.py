@@ -267,7 +267,7 @@ def _experts(T, k, E, model, K, N, dtype, act, bias, seed=0, align=1, skew=False
 
 
 # the last nine: the tile forms, as above
-EXPERTS = [(1, 6, 32, 32, 264, 136), (9, 2, 5, 10, 72, 264), (40, 4, 12, 24, 520, 72), (300, 3, 7, 7, 264, 200),
+EXPERTS = [(1, 6, 32, 32, 264, 136), (1, 32, 256, 256, 72, 40), (60, 4, 256, 256, 264, 72), (90, 8, 256, 300, 72, 136), (9, 2, 5, 10, 72, 264), (40, 4, 12, 24, 520, 72), (300, 3, 7, 7, 264, 200),
            (1500, 2, 5, 5, 136, 1032), (700, 8, 100, 130, 72, 40),
            (379, 2, 5, 5, 72, 3496), (1573, 2, 5, 5, 72, 3472), (68, 2, 5, 5, 680, 3856), (927, 2, 3, 3, 72, 2840),
            (70, 2, 3, 3, 584, 2632), (1381, 2, 5, 5, 1968, 40), (64, 2, 5, 5, 1064, 2288), (2836, 2, 5, 5, 1992, 64),
