@@ -50,11 +50,12 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 32 bytes at p + off (16-byte granules past `end` read as zero).
+// 32 bytes at p + off (16-byte granules past `end` read as zero).  Not by read-only loads:
+// the kernel before may write them while this one is already there.
 __device__ __forceinline__ void load32(const uint8_t* p, int off, int end, uint32_t (&v)[8]) {
   const uint4 z = make_uint4(0, 0, 0, 0);
-  const uint4 a = off < end ? __ldg(reinterpret_cast<const uint4*>(p + off)) : z;
-  const uint4 b = off + 16 < end ? __ldg(reinterpret_cast<const uint4*>(p + off + 16)) : z;
+  const uint4 a = off < end ? *reinterpret_cast<const uint4*>(p + off) : z;
+  const uint4 b = off + 16 < end ? *reinterpret_cast<const uint4*>(p + off + 16) : z;
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
