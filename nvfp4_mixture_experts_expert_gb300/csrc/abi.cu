@@ -1388,9 +1388,11 @@ static int run_linear_gemm(LinearArgs& t, const nvfp4_linear_shape* s, const voi
   t.stall = g_debug_stall_ms > 0;
   cudaError_t e = linear_gemm_plan(t, dev->sms);
   if (e != cudaSuccess) return cuda_fail(e, "linear plan");
-  if (int rc = make_half_map(&t.map_a, a, 1, a_rows, a_cols, ld_a, t.a_mn ? 64 : 128, s->type, false)) return rc;
-  if (int rc = make_half_map(&t.map_b, b, b_depth, b_rows, b_cols, ld_b, t.b_mn ? 64 : t.pair || t.ep.act == kActSwiglu ? t.bn / 2 : t.bn, s->type, true))
-    return rc;
+  const bool halves = t.ep.act == kActSwiglu;
+  const int b_box = t.b_mn ? 64 : t.turned ? (halves ? 64 : 128) : t.pair || halves ? t.bn / 2 : t.bn;
+  CUtensorMap *of_a = t.turned ? &t.map_b : &t.map_a, *of_b = t.turned ? &t.map_a : &t.map_b;
+  if (int rc = make_half_map(of_a, a, 1, a_rows, a_cols, ld_a, t.a_mn ? 64 : 128, s->type, false)) return rc;
+  if (int rc = make_half_map(of_b, b, b_depth, b_rows, b_cols, ld_b, b_box, s->type, true)) return rc;
   e = launch_linear_gemm(t, dev->sms, (cudaStream_t)stream);
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "linear launch");
 }

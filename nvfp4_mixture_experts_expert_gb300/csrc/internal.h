@@ -383,7 +383,8 @@ struct LinearArgs {
   // the others (gradients of 2048 x 2048 x 2048 53 us instead of 46).
   int before, beside;
   int stall;     // failure-detection check: only a tile's first K-block is loaded
-  int bn, pair, split;         // columns of a tile, CTA pairs, CTAs that share a tile's K: set by linear_gemm_plan
+  // set by linear_gemm_plan: columns of a tile, CTA pairs (turned: w is A, the rows are B), CTAs that share a tile's K
+  int bn, pair, turned, split;
   int m_tiles, n_tiles, band;  // set by the launch
 };
 cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms);  // from the sizes, groups and activation

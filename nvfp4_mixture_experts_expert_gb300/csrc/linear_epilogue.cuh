@@ -65,14 +65,15 @@ __device__ __forceinline__ uint32_t pack2(int type, float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// W consecutive values of a row (16 or 32), of which `left` exist (a multiple of 8);
-// v8: the addresses are multiples of 32 bytes, and whole sectors are moved.
+// W consecutive values of a row (8, 16 or 32), of which `left` exist (a multiple of 8);
+// v8: the addresses are multiples of 32 bytes, and whole sectors are moved (of eight
+// 16-bit values, half a sector, a lane moves one half and its neighbour the other).
 template <int WORDS>
 __device__ __forceinline__ void load_row(const void* p, bool v8, int left, uint32_t (&u)[WORDS]) {
   const uint32_t* q = static_cast<const uint32_t*>(p);
-  if (v8 && left >= 2 * WORDS) {
+  if (WORDS % 8 == 0 && v8 && left >= 2 * WORDS) {
 #pragma unroll
-    for (int i = 0; i < WORDS; i += 8)
+    for (int i = 0; i + 8 <= WORDS; i += 8)
       asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                    : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3]), "=r"(u[i + 4]), "=r"(u[i + 5]),
                      "=r"(u[i + 6]), "=r"(u[i + 7])
@@ -97,9 +98,9 @@ __device__ __forceinline__ void add_row(int type, const uint32_t (&r)[W / 2], fl
 template <int W, int WORDS>
 __device__ __forceinline__ void store_words(void* p, bool v8, int left, const uint32_t (&u)[WORDS]) {
   uint32_t* q = static_cast<uint32_t*>(p);
-  if (v8 && left >= W) {
+  if (WORDS % 8 == 0 && v8 && left >= W) {
 #pragma unroll
-    for (int i = 0; i < WORDS; i += 8)
+    for (int i = 0; i + 8 <= WORDS; i += 8)
       st_global_v8(q + i, u[i], u[i + 1], u[i + 2], u[i + 3], u[i + 4], u[i + 5], u[i + 6], u[i + 7]);
     return;
   }

@@ -39,7 +39,11 @@ cudaError_t launch_linear_plain(LinearArgs& p, int slots, cudaStream_t s) {
 // cluster share a tile's K (one round of tiles with SMs to spare).  Measured: pairs 25.7
 // us for 1024 x 4096 x 4096 (256 columns 28.7, 128 35), 128 columns 20 for 512 x 4096 x
 // 4096 (pairs 25, 64 columns 28), 128 columns with four CTAs a tile 11.7 for 16 x 4096 x
-// 4096 (one 19.3), 64 columns with eight 8.9 for 64 x 256 x 8192 (one 24.8).  Weight
+// 4096 (one 19.3), 64 columns with eight 8.9 for 64 x 256 x 8192 (one 24.8).  Pairs on
+// groups of rows run turned, a K-block in less time where a tile has fewer tokens, and
+// with an epilogue that SwiGLU's arithmetic makes longer: 32 groups of 300 rows, 4096 x
+// 4096, 257 us (256 columns 319, 128 361; not turned 315), of 1024 rows of 512 inputs,
+// SwiGLU, 138 (256 columns 109).  Weight
 // gradients of groups run as single CTAs: the rows behind a group's last would have to
 // be set to zero in both CTAs' operands (remote stores and a fence of the cluster: 521
 // us instead of 427 for 32 groups of 384 rows, 4096 x 4096).
@@ -56,7 +60,7 @@ cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms) {
   const int64_t k = p.counts && p.by_k ? (p.K + p.G - 1) / p.G : p.K;  // of a group, on average
   const int64_t kbs = (k + kBK - 1) / kBK;
   int64_t least = INT64_MAX;
-  for (const Form& f : kForms) {
+  for (Form f : kForms) {
     const int rows = f.pair ? 2 * kBM : kBM, out_cols = pairs ? f.bn / 2 : f.bn;
     const int64_t slots = f.pair ? fit->pair.most[2] : num_sms;
     if (slots == 0 || (f.pair && p.by_k && p.counts)) continue;
@@ -66,12 +70,18 @@ cudaError_t linear_gemm_plan(LinearArgs& p, int num_sms) {
                        : !p.counts          ? whole
                        : whole > some / 2   ? whole + some / 2
                                             : some;
+    const bool turned = f.pair && p.counts && !p.by_k;
+    if (turned) {
+      const int64_t tokens = (p.M + mt - 1) / mt + 16;  // of a tile, in steps of 32
+      f.block_ns = 135 + 7 * (int)(tokens < 256 ? tokens : 256) / 10;
+      if (pairs) f.tile_ns = 4100;
+    }
     const int64_t tiles = mt * ((p.N + out_cols - 1) / out_cols);
     for (int c = 1; c <= (f.bn < 256 && !p.counts ? kMaxSplit : 1) && c <= kbs; ++c) {
       if (c > 1 && (tiles * c > num_sms || tiles > fit->split.most[c])) continue;
       const int64_t loop_ns = (kbs + c - 1) / c * f.block_ns, rounds = (tiles * c + slots - 1) / slots;
       const int64_t ns = rounds * (loop_ns > f.tile_ns ? loop_ns : f.tile_ns) + f.tile_ns + (c > 1 ? f.join_ns : 0);
-      if (ns < least) least = ns, p.bn = f.bn, p.pair = f.pair, p.split = c;
+      if (ns < least) least = ns, p.bn = f.bn, p.pair = f.pair, p.turned = turned, p.split = c;
     }
   }
   return cudaSuccess;

@@ -15,7 +15,12 @@
 //
 // Groups: an expert's rows offsets[g] .. + counts[g] are tiled by themselves, a
 // tile's rows behind the group's last are computed and not stored.  With by_k, rows
-// behind the group's last are set to zero in the ring before the product.
+// behind the group's last are set to zero in the ring before the product.  CTA pairs on
+// groups by rows run turned (TURN): w is the M operand and the group's rows the N one,
+// whose length an instruction takes in steps of 32 where M is always 256, so the tiles
+// of a group share its rows evenly.  A lane of the accumulator is then an output column,
+// and the epilogue turns it through shared memory.  32 groups of 300 rows, 4096 x 4096:
+// 257 us instead of 315, 48 skewed ones of 1024 on average 932 instead of 970.
 //
 // Persistent, tiles of 128 x BN, FP32 accumulators in TMEM, two of them, so that a
 // tile's epilogue runs beside the next one's products.  Large problems run as CTA
@@ -61,9 +66,12 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kMaxGroups = 256;
 constexpr int kBiasBytes = 2 * 128 * 4;    // an epilogue warp's: the bias of up to 128 columns, SwiGLU of both halves
+constexpr int kTurnTokens = 16;            // tokens that a warp turns at a time, 32 columns of each:
+constexpr int kTurnPitch = 36;             // floats a token, so that eight lanes' 16 bytes meet no bank twice
+constexpr int kTurnBytes = kTurnTokens * kTurnPitch * 4;
 constexpr int kChunkBytes = 64 * 128;      // 64 columns x 64 rows of an operand read along columns
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, bool TURN = false>
 struct Cfg {
   static constexpr int A_BYTES = kBM * kBK * 2;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // of B that this CTA holds
@@ -76,7 +84,8 @@ struct Cfg {
   static constexpr int UNIT_ROWS = PAIR ? 2 * kBM : kBM;  // of a tile
   static constexpr int BUFS = 2;
   static constexpr int TMEM_COLS = BUFS * BN;
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kEpiWarps * kBiasBytes +
+  static constexpr int EPI_BYTES = TURN ? kTurnBytes : kBiasBytes;  // of an epilogue warp
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + kEpiWarps * EPI_BYTES +
                                  8 * (2 * STAGES + 2 * BUFS) + 16 + 4 * (3 * kMaxGroups + 4);
   static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
@@ -92,14 +101,14 @@ struct Smem {
   int *first_row, *rows;  // [G], of the groups: read by every role for every tile
 };
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, bool TURN>
 __device__ __forceinline__ Smem carve(uint8_t* raw) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, TURN>;
   Smem s;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   s.stages = smem_u32(base);
   s.bias = s.stages + C::STAGES * C::STAGE_BYTES;
-  s.full = s.bias + kEpiWarps * kBiasBytes;
+  s.full = s.bias + kEpiWarps * C::EPI_BYTES;
   s.empty = s.full + 8 * C::STAGES;
   s.acc_full = s.empty + 8 * C::STAGES;
   s.acc_empty = s.acc_full + 8 * C::BUFS;
@@ -116,6 +125,7 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
 // contraction (K-blocks kb0 .. kb1 of this CTA; k0: first row with by_k; k_end: length).
 struct Tile {
   int g, m0, n0, rows, kb0, kb1, k0, k_end;
+  int tokens;  // TURN: that the tile's products cover
   int64_t out_row;
 };
 
@@ -123,7 +133,7 @@ struct Tile {
 // bands of p.band m-tiles, in each of which m runs fastest: the CTAs at work then read
 // about as many rows of A as of B (8192 x 4096 x 4096 read 470 MB of memory with one
 // band, of 168 that the product needs).
-template <bool SPLIT, bool PAIR, bool SWIGLU>
+template <bool SPLIT, bool PAIR, bool SWIGLU, bool TURN = false>
 struct Walk {
   static constexpr int UNIT = PAIR ? 2 * kBM : kBM;
   const LinearArgs& p;
@@ -161,10 +171,16 @@ struct Walk {
       while (it >= L.first_tile[g + 1] * p.n_tiles) ++g;
       int m, n;
       place(it - L.first_tile[g] * p.n_tiles, L.first_tile[g + 1] - L.first_tile[g], m, n);
-      m = m * UNIT + (PAIR ? rank * kBM : 0);
+      if constexpr (TURN) {  // the group's tiles share its rows evenly, in steps of 32
+        const int mt = L.first_tile[g + 1] - L.first_tile[g];
+        t.tokens = (L.rows[g] + 32 * mt - 1) / (32 * mt) * 32;
+        m *= t.tokens;
+      } else {
+        m = m * UNIT + (PAIR ? rank * kBM : 0);
+      }
       t.m0 = m + L.first_row[g];
       t.n0 = n * out_cols;
-      t.rows = min(kBM, L.rows[g] - m);
+      t.rows = min(TURN ? t.tokens : kBM, L.rows[g] - m);
       t.out_row = t.m0;
       t.k0 = 0;
       t.k_end = p.K;
@@ -233,11 +249,25 @@ __device__ __forceinline__ uint32_t idesc_f16(int type, int a_mn, int b_mn, int 
 }
 
 // The operands of the K-block from k on.
-template <int BN, bool PAIR, bool SWIGLU>
+template <int BN, bool PAIR, bool SWIGLU, bool TURN>
 __device__ __forceinline__ void load_block(const LinearArgs& p, const Tile& t, int rank, uint32_t a, int k,
                                            uint32_t bar) {
   using C = Cfg<BN, PAIR>;
   const uint32_t b = a + C::A_BYTES;
+  if constexpr (TURN) {
+    const int n0 = t.n0 + rank * (SWIGLU ? kBM / 2 : kBM);
+    if (p.b_mn) {
+#pragma unroll
+      for (int i = 0; i < kBM / 64; ++i) load_box<PAIR>(a + i * kChunkBytes, &p.map_a, n0 + 64 * i, k, t.g, bar);
+    } else if (SWIGLU) {  // 64 rows of the gate, and their 64 of the up half
+      load_box<PAIR>(a, &p.map_a, k, n0, t.g, bar);
+      load_box<PAIR>(a + kChunkBytes, &p.map_a, k, p.N + n0, t.g, bar);
+    } else {
+      load_box<PAIR>(a, &p.map_a, k, n0, t.g, bar);
+    }
+    load_box<PAIR>(b, &p.map_b, k, t.m0 + rank * (t.tokens / 2), bar);
+    return;
+  }
   if (p.a_mn) {
 #pragma unroll
     for (int i = 0; i < kBM / 64; ++i) load_box<PAIR>(a + i * kChunkBytes, &p.map_a, t.m0 + 64 * i, k, bar);
@@ -256,15 +286,15 @@ __device__ __forceinline__ void load_block(const LinearArgs& p, const Tile& t, i
   }
 }
 
-template <int BN, bool SPLIT, bool PAIR, bool SWIGLU>
+template <int BN, bool SPLIT, bool PAIR, bool SWIGLU, bool TURN>
 __device__ void load_loop(const LinearArgs& p, const Smem& L) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, TURN>;
   volatile int* abort = L.abort_flag;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
   uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;
-  Walk<SPLIT, PAIR, SWIGLU> walk(p, L, BN);
+  Walk<SPLIT, PAIR, SWIGLU, TURN> walk(p, L, BN);
   const uint32_t full0 = PAIR ? mapa_shared(L.full, 0) : L.full;
   Tile t;
   while (ok && !*abort && walk.next(t)) {
@@ -281,7 +311,7 @@ __device__ void load_loop(const LinearArgs& p, const Smem& L) {
 #pragma unroll
         for (int i = 0; i < C::BLOCKS; ++i)
           if (i < blocks)
-            load_block<BN, PAIR, SWIGLU>(p, t, walk.rank, at + i * C::BLOCK_BYTES, t.k0 + (kb + i) * kBK, bar);
+            load_block<BN, PAIR, SWIGLU, TURN>(p, t, walk.rank, at + i * C::BLOCK_BYTES, t.k0 + (kb + i) * kBK, bar);
       }
       __syncwarp();
       issued |= 1u << stage;
@@ -327,26 +357,28 @@ __device__ __forceinline__ int end_of_group(uint32_t at, int left, int lane) {
   return (left + 15) / 16;
 }
 
-template <int BN, bool SPLIT, bool PAIR, bool SWIGLU>
+template <int BN, bool SPLIT, bool PAIR, bool SWIGLU, bool TURN>
 __device__ void mma_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, TURN>;
   volatile int* abort = L.abort_flag;
   const int lane = threadIdx.x & 31;
   const bool leader = elect_one();
-  const uint32_t idesc = idesc_f16(p.ep.type, p.a_mn, p.b_mn, C::UNIT_ROWS, BN);
+  const int a_mn = TURN ? p.b_mn : p.a_mn, b_mn = TURN ? 0 : p.b_mn;
+  uint32_t idesc = idesc_f16(p.ep.type, a_mn, b_mn, C::UNIT_ROWS, BN);
   // by rows: 8-row groups 1024 bytes apart; along columns: the same for 8 of K, 64-column chunks kChunkBytes apart
-  const uint64_t a0 = smem_desc(L.stages, p.a_mn ? kChunkBytes : 16, 1024, 2);
-  const uint64_t b0 = smem_desc(L.stages + C::A_BYTES, p.b_mn ? kChunkBytes : 16, 1024, 2);
-  const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;  // 16 of K
+  const uint64_t a0 = smem_desc(L.stages, a_mn ? kChunkBytes : 16, 1024, 2);
+  const uint64_t b0 = smem_desc(L.stages + C::A_BYTES, b_mn ? kChunkBytes : 16, 1024, 2);
+  const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;  // 16 of K
   uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1, last = 0, last_phase = 0;
   bool issued = false, ok = true, ready = false;
   const bool ends = !PAIR && p.by_k && p.counts;  // not planned as pairs
-  Walk<SPLIT, PAIR, SWIGLU> walk(p, L, BN);
+  Walk<SPLIT, PAIR, SWIGLU, TURN> walk(p, L, BN);
   Tile t;
   while (ok && walk.next(t)) {
     if (t.kb0 == t.kb1) continue;  // nothing to add up: the epilogue takes zeros
     ok = warp_wait(L.acc_empty + 8 * buf, buf_phase, abort, p.status);
     if (!ok) break;
+    if constexpr (TURN) idesc = idesc_f16(p.ep.type, a_mn, b_mn, C::UNIT_ROWS, t.tokens);
     const uint32_t d = tmem + buf * BN;
     for (int kb = t.kb0; kb < t.kb1; kb += C::BLOCKS) {
       if (!ready) {
@@ -411,6 +443,9 @@ __device__ void mma_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
 __device__ __forceinline__ void st_shared_f4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void st_shared_u32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -418,6 +453,15 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
                : "r"(at)
                : "memory");
   return v;
+}
+
+template <int W>
+__device__ __forceinline__ void get_cols(uint32_t at, float (&f)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; i += 4) {
+    const float4 v = ld_shared_f4(at + 4 * i);
+    f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+  }
 }
 
 // The bias of the warp's columns col .. col + n - 1 (and, for SwiGLU, of their up
@@ -571,6 +615,127 @@ __device__ void epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem)
   __syncwarp();
 }
 
+// The W columns from col on of a token's row, turned, at `from` of shared memory (SwiGLU:
+// the up's kTurnBytes behind).
+template <int EPI, int W>
+__device__ __forceinline__ void finish_turned(const LinearEpilogue& ep, int64_t row, int col, uint32_t from,
+                                              const float (&b)[W / 8][8], const float (&bu)[W / 8][8]) {
+  constexpr bool SWIGLU = EPI == kEpiSwiglu;
+  const int left = ep.N - col, out_size = ep.out_type == kTypeF32 ? 4 : 2;
+  float z[W], u[SWIGLU ? W : 1];
+  uint32_t r[W / 2];
+  if (ep.residual)
+    load_row(static_cast<const uint8_t*>(ep.residual) + (row * ep.ld_residual + col) * 2, ep.residual_v8, left, r);
+  get_cols(from, z);
+  if constexpr (SWIGLU) get_cols(from + kTurnBytes, u);
+  if (ep.bias) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] += b[i / 8][i % 8];
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) u[i] += bu[i / 8][i % 8];
+    }
+  }
+  if (ep.preact) {
+    uint8_t* to = static_cast<uint8_t*>(ep.preact) + (row * ep.ld_preact + col) * 2;
+    store_row(to, ep.type, ep.preact_v8, left, z);
+    if constexpr (SWIGLU) store_row(to + 2 * ep.N, ep.type, ep.preact_v8, left, u);
+  }
+  if constexpr (SWIGLU) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] = swiglu(z[i], u[i], ep.gate_limit, ep.up_limit);
+  }
+  if constexpr (EPI == kEpiActivation) activate_all(ep.act, z);
+  if (ep.residual) add_row(ep.type, r, z);
+  uint8_t* out = static_cast<uint8_t*>(ep.out) + (row * ep.ld_out + col) * out_size;
+  store_row(out, ep.out_type, ep.out_v8, left, z);
+}
+
+// Whether both warps that share a barrier say so.
+__device__ __forceinline__ bool both(bool ok, int barrier) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.and.pred p, %2, 64, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(barrier)
+      : "memory");
+  return r;
+}
+
+// The epilogue of a turned tile: an accumulator's lane is an output column, its columns
+// are tokens.  A warp turns 16 tokens of its 32 lanes at a time through shared memory;
+// then a lane has 16 columns of a token (SwiGLU, where two warps turn a gate's lanes and
+// their up's: eight of each).
+template <int BN, int EPI>
+__device__ void turned_epilogue_loop(const LinearArgs& p, const Smem& L, uint32_t tmem) {
+  using C = Cfg<BN, true, true>;
+  constexpr bool SWIGLU = EPI == kEpiSwiglu;
+  constexpr int W = SWIGLU ? 8 : 16;  // output columns of a lane
+  volatile int* abort = L.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
+  // SwiGLU: a gate's warp and its up's share what they turn
+  const int with = SWIGLU ? quarter >> 1 : 0, first = half * 4 + (SWIGLU ? quarter % 2 * 2 : quarter);
+  const int at = with * 32 + lane, token = at / (32 / W), my_col = at % (32 / W) * W;
+  const uint32_t turn = L.bias + first * C::EPI_BYTES;
+  const uint32_t to = turn + with * C::EPI_BYTES + lane * 4, from = turn + (token * kTurnPitch + my_col) * 4;
+  auto meet = [&] {
+    if constexpr (SWIGLU)
+      asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + half * 2 + quarter % 2) : "memory");
+    else
+      __syncwarp();
+  };
+  const LinearEpilogue& ep = p.ep;
+  const uint32_t acc_empty = cluster_ctarank() ? mapa_shared(L.acc_empty, 0) : L.acc_empty;
+  uint32_t buf = 0, phase = 0;
+  Walk<false, true, SWIGLU, true> walk(p, L, BN);
+  Tile t;
+  while (walk.next(t)) {
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN;
+    const int col = t.n0 + (SWIGLU ? walk.rank * 64 + quarter % 2 * 32 : walk.rank * 128 + quarter * 32) + my_col;
+    float b[W / 8][8], bu[W / 8][8];
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) load_bias<EPI>(ep, t.g, col + 8 * i, b[i], bu[i]);
+    bool ok = warp_wait_asleep(L.acc_full + 8 * buf, phase, abort, p.status);
+    if constexpr (SWIGLU) ok = both(ok, 1 + half * 2 + quarter % 2);  // neither waits for one that has left
+    if (!ok) break;
+    tc_fence_after();
+    // the next tokens are on their way from the accumulator while these are stored
+    uint32_t v[kTurnTokens];
+    auto take = [&](int c) {
+      if (c < t.rows) tmem_load_cols(lanes + c, v);
+    };
+    take(half * kTurnTokens);
+    for (int c = half * kTurnTokens;; c += 2 * kTurnTokens) {
+      __syncwarp();
+      tmem_load_wait();
+      if (c >= t.rows) break;
+      meet();  // the reads of the tokens before are done
+#pragma unroll
+      for (int i = 0; i < kTurnTokens; ++i) {
+        asm volatile("" : "+r"(v[i]));  // no use moves above the wait
+        st_shared_u32(to + i * kTurnPitch * 4, v[i]);
+      }
+      meet();
+      take(c + 2 * kTurnTokens);
+      if (c + token < t.rows && col < p.N) finish_turned<EPI, W>(ep, t.out_row + c + token, col, from, b, bu);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (acc_empty != L.acc_empty)
+        mbar_arrive_remote(acc_empty + 8 * buf);
+      else
+        mbar_arrive(acc_empty + 8 * buf);
+    }
+    if (++buf == C::BUFS) {
+      buf = 0;
+      phase ^= 1u;
+    }
+  }
+  __syncwarp();
+}
+
 // The cluster's CTAs add up the ranges' sums in K order, each its share of the
 // tile's rows, four columns a thread.  A thread's columns stay the same from row to row,
 // so their bias is loaded once, and two rows' sums and residuals are in flight: what is
@@ -655,11 +820,11 @@ __device__ void read_groups(const LinearArgs& p, const Smem& L) {
   if (lane == 0) L.first_tile[p.G] = sum;
 }
 
-template <int BN, bool SPLIT, bool PAIR, int EPI>
+template <int BN, bool SPLIT, bool PAIR, int EPI, bool TURN = false>
 __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ LinearArgs p) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, TURN>;
   extern __shared__ uint8_t smem_raw[];
-  const Smem L = carve<BN, PAIR>(smem_raw);
+  const Smem L = carve<BN, PAIR, TURN>(smem_raw);
   constexpr bool SWIGLU = EPI == kEpiSwiglu;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -693,9 +858,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers are initialised, their TMEM allocated
   tc_fence_after();
   const uint32_t tmem = *L.tmem_slot;
-  if (warp == 0) load_loop<BN, SPLIT, PAIR, SWIGLU>(p, L);
-  if (warp == 1 && (!PAIR || cluster_ctarank() == 0)) mma_loop<BN, SPLIT, PAIR, SWIGLU>(p, L, tmem);
-  if (warp >= kEpiWarp0) epilogue_loop<BN, SPLIT, PAIR, EPI>(p, L, tmem);
+  if (warp == 0) load_loop<BN, SPLIT, PAIR, SWIGLU, TURN>(p, L);
+  if (warp == 1 && (!PAIR || cluster_ctarank() == 0)) mma_loop<BN, SPLIT, PAIR, SWIGLU, TURN>(p, L, tmem);
+  if (warp >= kEpiWarp0) {
+    if constexpr (TURN)
+      turned_epilogue_loop<BN, EPI>(p, L, tmem);
+    else
+      epilogue_loop<BN, SPLIT, PAIR, EPI>(p, L, tmem);
+  }
   __syncwarp();
   if (p.beside) pdl_wait();  // this kernel's end is also the end of the one it ran beside
   if constexpr (SPLIT) {
@@ -717,21 +887,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
   }
 }
 
-template <int BN, bool SPLIT, bool PAIR, int EPI>
+template <int BN, bool SPLIT, bool PAIR, int EPI, bool TURN = false>
 cudaError_t configure() {
   static PerDevice<char, cudaError_t> done;
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev)) return e;
   const char* none = nullptr;
   return done.get(dev, &none, [](char&) {
-    return cudaFuncSetAttribute(linear_gemm_kernel<BN, SPLIT, PAIR, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Cfg<BN, PAIR>::SMEM);
+    return cudaFuncSetAttribute(linear_gemm_kernel<BN, SPLIT, PAIR, EPI, TURN>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN, PAIR, TURN>::SMEM);
   });
 }
 
-template <int BN, bool PAIR, int EPI>
+template <int BN, bool PAIR, int EPI, bool TURN = false>
 cudaError_t launch(LinearArgs& p, int slots, cudaStream_t s) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, TURN>;
   const int out_cols = EPI == kEpiSwiglu ? BN / 2 : BN;
   p.m_tiles = (p.M + C::UNIT_ROWS - 1) / C::UNIT_ROWS;
   p.n_tiles = (p.N + out_cols - 1) / out_cols;
@@ -747,19 +917,20 @@ cudaError_t launch(LinearArgs& p, int slots, cudaStream_t s) {
                                             kThreads, C::SMEM, p.split, s, p);
     }
   }
-  if ((e = configure<BN, false, PAIR, EPI>()) != cudaSuccess) return e;
+  if ((e = configure<BN, false, PAIR, EPI, TURN>()) != cudaSuccess) return e;
   // groups by rows: at most one tile more than the rows' for each
   const int64_t m = p.by_k ? (int64_t)p.G * p.m_tiles : p.counts ? (int64_t)p.m_tiles + p.G : p.m_tiles;
   const int64_t tiles = m * p.n_tiles;
   const int grid = (int)(tiles < slots ? tiles : slots);
   if (PAIR)
-    return launch_split<const LinearArgs>(linear_gemm_kernel<BN, false, PAIR, EPI>, 2 * grid, kThreads, C::SMEM, 2, s,
-                                          p);
+    return launch_split<const LinearArgs>(linear_gemm_kernel<BN, false, PAIR, EPI, TURN>, 2 * grid, kThreads, C::SMEM,
+                                          2, s, p);
   return launch_kernel(linear_gemm_kernel<BN, false, PAIR, EPI>, dim3(grid), dim3(kThreads), C::SMEM, s, true, p);
 }
 
 template <int EPI>
 cudaError_t launch_form(LinearArgs& p, int slots, cudaStream_t s) {
+  if (p.pair && p.turned) return launch<256, true, EPI, true>(p, slots, s);
   if (p.pair) return launch<256, true, EPI>(p, slots, s);
   return p.bn == 256   ? launch<256, false, EPI>(p, slots, s)
          : p.bn == 128 ? launch<128, false, EPI>(p, slots, s)

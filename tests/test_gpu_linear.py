@@ -329,6 +329,74 @@ def test_expert_linear_grad(T, k, E, model, K, N, act, dtype, align, skew):
     assert (dx[~used] == 7).all()
 
 
+# Rows of experts at the edges of tiles: none, one, around 32 and 256, several tiles, many.
+COUNTS = (0, 1, 31, 33, 256, 257, 300, 513, 1793)
+
+
+def _experts_of(counts, K, N, dtype, act, bias, align, seed):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    ids = torch.repeat_interleave(torch.arange(len(counts), dtype=torch.int32), torch.tensor(counts))
+    ids = ids[torch.randperm(ids.numel(), generator=torch.Generator().manual_seed(seed))][:, None]
+    t = getattr(torch, dtype)
+    _, order = api.sort_tokens(torch.zeros(ids.shape[0], 8, dtype=t, device="cuda"), ids.cuda(), len(counts), 0, align)
+    assert order.counts.tolist() == list(counts)
+    rows, w, b, res = _inputs(order.source.numel(), N, K, dtype, act, bias, True, seed=seed, experts=len(counts))
+    nan = torch.full_like(rows, float("nan"))
+    return torch.where((order.source >= 0)[:, None], rows, nan), w, b, res, order
+
+
+@pytest.mark.parametrize("act,dtype,bias,f32", [(None, "bfloat16", None, False), (None, "float16", "same", True),
+                                                ("swiglu", "bfloat16", "f32", False), ("swiglu", "float16", "same", True),
+                                                ("silu", "bfloat16", "same", True), ("gelu", "float16", "f32", False)])
+@pytest.mark.parametrize("K,N,align", [(1032, 1000, 1), (1032, 1000, 16), (1992, 1176, 1), (2048, 1304, 128)])
+def test_expert_linear_counts(K, N, align, act, dtype, bias, f32):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    rows, w, b, res, order = _experts_of(COUNTS, K, N, dtype, act, bias, align, seed=K + align)
+    limits = (1.5, 0.75) if act == "swiglu" else (INF, INF)
+    n, out_dtype = rows.shape[0], torch.float32 if f32 else rows.dtype
+    pad = torch.full((n + 1, N + 24), 7.0, dtype=out_dtype, device="cuda")
+    for residual in (None, res):
+        out = pad[1:, 8:N + 8]
+        got, z = api.expert_linear(rows, w, order, b, act, residual, *limits, preact=True, out=out)
+        used = torch.zeros_like(pad, dtype=torch.bool)
+        for e, at in enumerate(_slices(order)):
+            used[1:, 8:N + 8][at] = True
+            _check(rows[at], w[e], None if b is None else b[e], None if residual is None else residual[at], act, limits,
+                   out_dtype, out[at], z[at])
+        assert (pad[~used] == 7).all()
+    if not f32:  # in place of the residual, and without the sums
+        want, place = out.clone(), res.clone()
+        api.expert_linear(rows, w, order, b, act, place, *limits, out=place)
+        for at in _slices(order):
+            assert torch.equal(place[at], want[at])
+    again = api.expert_linear(rows, w, order, b, act, res, *limits, out_dtype=out_dtype)
+    for at in _slices(order):
+        assert torch.equal(again[at], out[at])
+
+
+@pytest.mark.parametrize("act,dtype", [(None, "bfloat16"), ("swiglu", "float16"), ("silu", "bfloat16")])
+@pytest.mark.parametrize("K,N,align", [(1000, 1032, 1), (1304, 2048, 16), (2600, 1096, 1)])
+def test_expert_linear_grad_counts(K, N, align, act, dtype):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    rows, w, _, res, order = _experts_of(COUNTS, K, N, dtype, act, None, align, seed=N)
+    used = (order.source >= 0)[:, None]
+    nan = lambda t: torch.where(used, t, torch.full_like(t, float("nan")))
+    dy = nan(res)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    z = None if act is None else nan((2 * _randn(g, rows.shape[0], w.shape[1])).to(rows.dtype))
+    limits = (1.5, 0.75) if act == "swiglu" else (INF, INF)
+    out = torch.full((rows.shape[0], K + 8), 7.0, dtype=rows.dtype, device="cuda")
+    dx, dw, db = api.expert_linear_grad(dy, rows, w, order, z, act, *limits, bias=True, out=out[:, :K])
+    for e, at in enumerate(_slices(order)):
+        want = R.linear_grad(dy[at], rows[at], w[e], None if z is None else z[at], act, limits, rows.dtype)
+        for got, (ref, tol) in zip((dx[at], dw[e], db[e]), want):
+            R.check(got, ref, tol)
+    assert (out[:, K:] == 7).all() and (dx[~used[:, 0]] == 7).all()
+
+
 def test_expert_linear_without_rows():
     import torch
     from nvfp4_mixture_experts_expert_gb300 import api
@@ -414,3 +482,21 @@ def test_a_stalled_product_is_reported():
         binding.nvfp4_moe_set_debug_stall(0)
     assert binding.nvfp4_device_status(reset=True) == binding.NVFP4_ERR_DEVICE_TIMEOUT
     assert torch.equal(api.linear(x, w), want) and binding.nvfp4_device_status() == 0
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_a_stalled_expert_product_is_reported(act):
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api, binding
+    rows, w, _, _, order = _experts_of(COUNTS, 1032, 1000, "bfloat16", act, None, 1, seed=3)
+    want = api.expert_linear(rows, w, order, activation=act)
+    torch.cuda.synchronize()
+    assert binding.nvfp4_device_status(reset=True) == 0
+    binding.nvfp4_moe_set_debug_stall(50)
+    try:
+        api.expert_linear(rows, w, order, activation=act)
+        torch.cuda.synchronize()
+    finally:
+        binding.nvfp4_moe_set_debug_stall(0)
+    assert binding.nvfp4_device_status(reset=True) == binding.NVFP4_ERR_DEVICE_TIMEOUT
+    assert torch.equal(api.expert_linear(rows, w, order, activation=act), want) and binding.nvfp4_device_status() == 0
