@@ -669,8 +669,9 @@ int nvfp4_combine_tokens_grad(const void* dout, int64_t ld_dout, const void* row
  *   out       device [M][N] of out_type (`type` or NVFP4_F32), row stride ld_out; may be
  *             residual itself (same type and stride)
  * 0 <= M <= 2^22 (0: no work), N and K multiples of 8 up to 131072; row strides
- * multiples of 8; pointers 16-byte aligned, tables 4.  A device-side timeout is
- * reported in the library's status word (nvfp4_device_status).
+ * multiples of 8; pointers 16-byte aligned, tables 4.  Outputs overlap no input (out:
+ * none but the residual).  A device-side timeout is reported in the library's status
+ * word (nvfp4_device_status).
  */
 typedef struct {
   int64_t M, N, K;
@@ -697,7 +698,7 @@ int nvfp4_linear(const nvfp4_linear_shape* shape, const void* x, int64_t ld_x, c
  * M == 0 writes zeros there.  The gradient of residual is dy.
  *   workspace device scratch of nvfp4_linear_grad_workspace_size() bytes (0: none
  *             needed), 256-byte aligned, for one call at a time
- * Sizes, strides and alignment as nvfp4_linear.
+ * Sizes, strides and alignment as nvfp4_linear; outputs overlap no input.
  */
 size_t nvfp4_linear_grad_workspace_size(const nvfp4_linear_shape* shape, int products, int dbias);
 int nvfp4_linear_grad(const nvfp4_linear_shape* shape, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
