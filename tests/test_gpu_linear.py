@@ -500,3 +500,41 @@ def test_a_stalled_expert_product_is_reported(act):
         binding.nvfp4_moe_set_debug_stall(0)
     assert binding.nvfp4_device_status(reset=True) == binding.NVFP4_ERR_DEVICE_TIMEOUT
     assert torch.equal(api.expert_linear(rows, w, order, activation=act), want) and binding.nvfp4_device_status() == 0
+
+
+def test_expert_products_in_a_graph_and_on_two_streams():
+    import dataclasses
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    calls = []
+    for seed, counts in ((1, COUNTS), (2, COUNTS[::-1])):
+        rows, w, b, res, order = _experts_of(counts, 1032, 1000, "bfloat16", "swiglu", "same", 1, seed=seed)
+        calls.append((rows, w, b, res, order))
+
+    def run(rows, w, b, res, order, stream=None):
+        y, z = api.expert_linear(rows, w, order, b, "swiglu", res, preact=True, stream=stream)
+        return (y, *api.expert_linear_grad(res, rows, w, order, z, "swiglu", bias=True, stream=stream))
+
+    want = [run(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        got = [run(*c, stream=s) for c, s in zip(calls, streams)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+    # a captured call takes the tables that it finds at its replay
+    inputs = [t.clone() if torch.is_tensor(t) else
+              dataclasses.replace(t, **{f: getattr(t, f).clone() for f in ("offsets", "counts", "source", "inverse")})
+              for t in calls[0]]
+    run(*inputs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(*inputs)
+    for c, w in zip(calls[::-1], want[::-1]):
+        for to, of in zip(inputs[:4], c[:4]):
+            to.copy_(of)
+        for f in ("offsets", "counts", "source", "inverse"):
+            getattr(inputs[4], f).copy_(getattr(c[4], f))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
