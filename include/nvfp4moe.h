@@ -687,7 +687,8 @@ int nvfp4_linear(const nvfp4_linear_shape* shape, const void* x, int64_t ld_x, c
 /*
  * nvfp4_linear_grad -- the gradients of nvfp4_linear from dy, that of its output:
  *   dz = dy * act'(z)      (FP32, rounded to `type` as an operand of the products; limits
- *                           pass the gradient up to and at their value; relu'(0) = 0)
+ *                           pass the gradient up to and at their value; relu'(0) = 0,
+ *                           and where relu' is 0 dz is 0 whatever dy is)
  *   dx = dz w,  dw = dz^T x  (FP32 sums, rounded once),  dbias = sum over m of dz (FP32, unrounded dz)
  *   dy        device [M][N] of `type`, row stride ld_dy
  *   preact    device [M][wide] of `type` contiguous: z; not used without an activation

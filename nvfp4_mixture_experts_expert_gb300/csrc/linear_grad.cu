@@ -32,7 +32,6 @@ constexpr float kFar = 1e4f;
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
   const float f = at_least(at_most(z, kFar), -kFar);
-  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
   if constexpr (ACT == kActSilu) {
     const float s = sigmoid(z);
     return s + f * s * (1.f - s);
@@ -44,6 +43,14 @@ __device__ __forceinline__ float slope(float z) {
     return s + f * s * (1.f - s) * (1.59576912f * (1.f + 0.134145f * f * f));
   }
   return 1.f;
+}
+// dy act'(z).  Where relu' is 0 nothing of dy passes, also not an infinity (a product's
+// 0 * inf would reach a row of dx and of dw, and dbias); z NaN: NaN.
+template <int ACT>
+__device__ __forceinline__ float through(float d, float z) {
+  if constexpr (ACT == kActNone) return d;
+  if constexpr (ACT == kActRelu) return z > 0.f ? d : z <= 0.f ? 0.f : z;
+  return d * slope<ACT>(z);
 }
 
 // What eight columns of a row need of dy and z, as loaded (z and u: SwiGLU's gate and up).
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) linear_dz_kernel(const LinearG
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            z[i] = ACT == kActNone ? d[i] : d[i] * slope<ACT>(z[i]);
+            z[i] = through<ACT>(d[i], z[i]);
             sum[i] = __fadd_rn(sum[i], z[i]);
           }
         }
