@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) linear_dz_kernel(const LinearG
             const float g = at_least(at_most(z[i], p.gate_limit), -kFar);
             const float uc = at_least(at_most(u[i], p.up_limit), -p.up_limit);
             const float sg = sigmoid(g), h = g * sg;
-            z[i] = z[i] > p.gate_limit ? 0.f : __fmul_rn(d[i] * uc, fmaf(h, 1.f - sg, sg));
+            // a gate without a limit may be infinite: h is cut as slope() cuts z
+            z[i] = z[i] > p.gate_limit ? 0.f : __fmul_rn(d[i] * uc, fmaf(at_most(h, kFar), 1.f - sg, sg));
             u[i] = u[i] == uc ? __fmul_rn(d[i], h) : 0.f;
             const float du = u[i];
             sum[i] = __fadd_rn(sum[i], z[i]), sum_u[i] = __fadd_rn(sum_u[i], du);
