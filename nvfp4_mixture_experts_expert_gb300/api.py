@@ -305,6 +305,11 @@ class FFNBlock:
         return self.layer(y, logits, self.weights, *self.limits, stream=stream), s
 
 
+# The calls from here to ExpertFFN have gradients that are calls of their own, and record
+# no graph: a tensor that requires grad is refused (ValueError) where autograd is on, that
+# is outside of torch.no_grad() and of an autograd.Function.
+
+
 @dataclass
 class TokenOrder:
     """Where sort_tokens has put the tokens' rows (see nvfp4_sort_tokens).  The tables
@@ -411,7 +416,8 @@ class ExpertFFN:
     """The MoE layer's experts on unquantized weights, for given routing: tokens sorted by
     expert, gate and up product with SwiGLU, down product, and back with the routing
     weights.  w13 [E, 2I, H] and w2 [E, H, I] bf16 or f16, as quantize_moe_weights takes
-    them (bf16); the layer holds the experts [experts_start, experts_start + E)."""
+    them (bf16); the layer holds the experts [experts_start, experts_start + E).  It runs
+    under torch.no_grad() where a tensor requires grad: its gradients come from grad()."""
 
     def __init__(self, w13, w2, experts_start=0, gate_limit=10.0, up_limit=10.0):
         self.w13, self.w2, self.experts_start = w13, w2, experts_start

@@ -4,6 +4,7 @@
 // one output and 19 us for four, longer than the kernels; this takes 3 to 4 us.
 // api.py documents the calls and is their public form.
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -285,6 +286,18 @@ PyObject* moe_few_tokens(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The calls below have gradients that are calls of their own and record no graph:
+// backward() through their results would leave their part out in silence, so a tensor
+// that autograd follows is refused (not under no_grad, and not inside an
+// autograd.Function, which runs so).
+void no_graph(PyObject* const* a, Py_ssize_t n) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (Py_ssize_t i = 0; i < n; ++i)
+    TORCH_CHECK_VALUE(!THPVariable_Check(a[i]) || !THPVariable_Unpack(a[i]).requires_grad(),
+                      "a tensor requires grad, and this call records no graph: call it under torch.no_grad() (or in an "
+                      "autograd.Function) and take the gradients from the operator's own call for them");
+}
+
 // Element type of rows of tokens (`all`) or of a linear's operands (16 bits).
 int type_of(const at::Tensor& t, const char* name, bool all) {
   switch (t.scalar_type()) {
@@ -358,6 +371,7 @@ PyObject* tuple_of(std::initializer_list<std::optional<at::Tensor>> parts) {
 PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 7)) return nullptr;
+  no_graph(a, n);
   const at::Tensor &x = tensor(a[0], "x"), &ids = tensor(a[1], "topk_ids");
   const int E = small_number(a[2], "E"), start = small_number(a[3], "experts_start"), align = small_number(a[4], "align");
   const std::optional<cudaStream_t> stream = handle(a[6]);
@@ -391,6 +405,7 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* sort_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 5)) return nullptr;
+  no_graph(a, n);
   const at::Tensor &d = tensor(a[0], "grad_rows"), &inv = tensor(a[1], "the order's inverse");
   const std::optional<cudaStream_t> stream = handle(a[4]);
   need_cuda(d, "grad_rows");
@@ -412,6 +427,7 @@ PyObject* sort_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 7)) return nullptr;
+  no_graph(a, n);
   const at::Tensor &r = tensor(a[0], "rows"), &w = tensor(a[1], "weights"), &inv = tensor(a[2], "the order's inverse");
   const std::optional<cudaStream_t> stream = handle(a[6]);
   need_cuda(r, "rows");
@@ -436,6 +452,7 @@ PyObject* combine_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 10)) return nullptr;
+  no_graph(a, n);
   const at::Tensor &d = tensor(a[0], "grad_out"), &r = tensor(a[1], "rows"), &w = tensor(a[2], "weights"),
                    &off = tensor(a[3], "the order's offsets"), &cnt = tensor(a[4], "the order's counts"),
                    &inv = tensor(a[5], "the order's inverse");
@@ -508,6 +525,7 @@ struct Shape {
 PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 12)) return nullptr;
+  no_graph(a, n);
   const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
   const bool f32 = truth(a[8]), keep = truth(a[9]);
   const std::optional<cudaStream_t> stream = handle(a[11]);
@@ -546,6 +564,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!count(n, 13)) return nullptr;
+  no_graph(a, n);
   const at::Tensor &dy = tensor(a[0], "grad"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
   const bool bias = truth(a[8]), inputs = truth(a[9]), weights = truth(a[10]);
   const std::optional<cudaStream_t> stream = handle(a[12]);
