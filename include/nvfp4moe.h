@@ -429,9 +429,10 @@ int nvfp4_debug_gemm_trace(void* buffer, int stages, int tiles, int kind);
  * GEMM gives up, records NVFP4_ERR_DEVICE_TIMEOUT in that call's workspace
  * status word and returns; the rest of the forward runs on whatever the L2
  * input buffer held (its output is meaningless, nothing faults).  While it is
- * on, nvfp4_fp8_linear (above 8 rows) loads a tile's first K-block alone and the
- * few-token MoE layer a CTA's first tile; their waits give up after their own
- * limit (about a second).  0 switches it off.  Process-wide; 0 <= timeout_ms <= 10000.
+ * on, nvfp4_fp8_linear (above 8 rows), nvfp4_linear (above its few rows) and the
+ * products of nvfp4_linear_grad load a tile's first K-block alone and the few-token
+ * MoE layer a CTA's first tile; their waits give up after their own limit (about a
+ * second).  0 switches it off.  Process-wide; 0 <= timeout_ms <= 10000.
  */
 int nvfp4_moe_set_debug_stall(int timeout_ms);
 
@@ -705,6 +706,16 @@ size_t nvfp4_linear_grad_workspace_size(const nvfp4_linear_shape* shape, int pro
 int nvfp4_linear_grad(const nvfp4_linear_shape* shape, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                       const void* w, const void* preact, void* dx, int64_t ld_dx, void* dw, float* dbias,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_debug_linear_form -- which kernel form the current device runs a linear's
+ * product in, for tests and measurements; nothing is launched.
+ *   product  0: nvfp4_linear; 1, 2: dx, dw of nvfp4_linear_grad
+ *   form     host i32[4]: columns of a tile (0: the kernel for few rows), 1 for CTA
+ *            pairs, 1 for tiles with w as the M operand, CTAs that share a tile's K
+ * The shape's tables are looked at no further than for NULL.
+ */
+int nvfp4_debug_linear_form(const nvfp4_linear_shape* shape, int product, int32_t* form);
 
 #ifdef __cplusplus
 }

@@ -142,6 +142,8 @@ _linear = _sig("nvfp4_linear", c_int, [ctypes.POINTER(LinearShape), c_ptr, c_i64
 _linear_grad_ws = _sig("nvfp4_linear_grad_workspace_size", c_size, [ctypes.POINTER(LinearShape), c_int, c_int])
 _linear_grad = _sig("nvfp4_linear_grad", c_int, [ctypes.POINTER(LinearShape), c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_ptr,
                                                  c_ptr, c_i64, c_ptr, c_ptr, c_ptr, c_size, c_ptr])
+_linear_form = _sig("nvfp4_debug_linear_form", c_int, [ctypes.POINTER(LinearShape), c_int,
+                                                       ctypes.POINTER(ctypes.c_int32)])
 _moe_set_swap_l2 = _sig("nvfp4_moe_set_swap_l2", c_int, [c_int, ctypes.POINTER(c_int)])
 
 
@@ -431,3 +433,10 @@ def nvfp4_linear_grad(shape, dy, ld_dy, x, ld_x, w, preact, dx, ld_dx, dw, dbias
                       stream=None):
     _check(_linear_grad(ctypes.byref(shape), _p(dy), ld_dy, _p(x), ld_x, _p(w), _p(preact), _p(dx), ld_dx, _p(dw),
                         _p(dbias), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_debug_linear_form(shape, product=0):
+    """(columns of a tile, 1 for CTA pairs, 1 for w as the M operand, CTAs that share a tile's K)."""
+    form = (ctypes.c_int32 * 4)()
+    _check(_linear_form(ctypes.byref(shape), product, form))
+    return tuple(form)

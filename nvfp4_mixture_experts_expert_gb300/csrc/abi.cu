@@ -1374,6 +1374,12 @@ static int whole_sectors(const void* p, int64_t ld, int size) {
   return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld * size % 32 == 0;
 }
 
+static void set_groups(LinearArgs& t, const nvfp4_linear_shape* s) {
+  t.G = s->groups ? s->groups : 1;
+  t.offsets = s->groups ? s->offsets : nullptr;
+  t.counts = s->groups ? s->counts : nullptr;
+}
+
 // Plan, maps and launch of one product (args filled in but for these).
 static int run_linear_gemm(LinearArgs& t, const nvfp4_linear_shape* s, const void* a, int64_t a_rows, int64_t a_cols,
                            int64_t ld_a, const void* b, int64_t b_depth, int64_t b_rows, int64_t b_cols, int64_t ld_b,
@@ -1381,9 +1387,7 @@ static int run_linear_gemm(LinearArgs& t, const nvfp4_linear_shape* s, const voi
   t.ep.out_v8 = whole_sectors(t.ep.out, t.ep.ld_out, t.ep.out_type == NVFP4_F32 ? 4 : 2);
   t.ep.residual_v8 = whole_sectors(t.ep.residual, t.ep.ld_residual, 2);
   t.ep.preact_v8 = whole_sectors(t.ep.preact, t.ep.ld_preact, 2) && t.ep.N % 16 == 0;
-  t.G = s->groups ? s->groups : 1;
-  t.offsets = s->groups ? s->offsets : nullptr;
-  t.counts = s->groups ? s->counts : nullptr;
+  set_groups(t, s);
   t.status = dev->status;
   t.stall = g_debug_stall_ms > 0;
   cudaError_t e = linear_gemm_plan(t, dev->sms);
@@ -1550,6 +1554,37 @@ int nvfp4_linear_grad(const nvfp4_linear_shape* s, const void* dy, int64_t ld_dy
     t.beside = dx != nullptr;
     if (int rc = run_linear_gemm(t, s, dz, s->M, wide, ld_dz, x, 1, s->M, s->K, ld_x, dev, stream)) return rc;
   }
+  return NVFP4_OK;
+}
+
+int nvfp4_debug_linear_form(const nvfp4_linear_shape* s, int product, int32_t* form) {
+  g_err[0] = 0;
+  if (int rc = check_linear(s)) return rc;
+  if (!form) return fail(NVFP4_ERR_INVALID_ARG, "null pointer");
+  if (product < 0 || product > 2) return fail(NVFP4_ERR_INVALID_ARG, "product must be 0, 1 or 2");
+  if (s->M == 0) return fail(NVFP4_ERR_INVALID_ARG, "no rows, no product");
+  if (product == 0 && linear_is_few(s->M, s->groups)) {
+    form[0] = form[1] = form[2] = 0;
+    form[3] = 1;
+    return NVFP4_OK;
+  }
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  const int wide = (int)linear_wide(s);
+  LinearArgs t;
+  memset(&t, 0, sizeof(t));
+  t.M = product == 2 ? wide : (int)s->M;
+  t.N = (int)(product == 0 ? s->N : s->K);
+  t.K = product == 0 ? (int)s->K : product == 1 ? wide : (int)s->M;
+  t.by_k = product == 2;
+  if (product == 0) t.ep.act = s->activation;
+  set_groups(t, s);
+  const cudaError_t e = linear_gemm_plan(t, dev->sms);
+  if (e != cudaSuccess) return cuda_fail(e, "linear plan");
+  form[0] = t.bn;
+  form[1] = t.pair;
+  form[2] = t.turned;
+  form[3] = t.split;
   return NVFP4_OK;
 }
 
