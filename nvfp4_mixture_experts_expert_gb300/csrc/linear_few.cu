@@ -142,10 +142,17 @@ __global__ void __launch_bounds__(32 * warps_of(EXPERTS), blocks_of(EXPERTS)) li
 }  // namespace
 
 // One matrix: two passes over w (the second from L2) against a 128-row tile: 16 x 4096 x
-// 4096 11.3 us against 12.4 (8 rows 7.7 against 16; 17 rows 14.9 against 12.4).  Experts
-// (of 32, 4096 x 4096): 1, 2, 3, 4 and 5 tokens of six 40, 59, 85, 115 and 104 us against
-// 57, 92, 87, 125 and 100; 16 tokens 176 against 172.
-bool linear_is_few(int64_t M, int groups) { return groups ? M <= (int64_t)groups : M <= 2 * kLinearFewRows; }
+// 4096 11.3 us against 12.4 (8 rows 7.7 against 16; 17 rows 14.9 against 12.4).
+// Experts: as many rows as experts, and at most four passes should all of them fall to
+// one.  us here and (in brackets) on tiles, each row of another expert / all of one:
+//   rows                       8                    32                     256
+//   32 of 4096 x 4096         48 (57) / 11 (20)    173 (163) / 27 (19)
+//   256 of 4096 x 4096        49 (67) / 13 (29)    176 (173) / 34 (29)    1328 (1260) / 222 (35)
+//   256 of 768 x 2048 SwiGLU  15 (27) / 5 (18)      41 (48) / 13 (18)      268 (247) / 89 (24)
+constexpr int64_t kMostRowsOfExperts = 32;
+bool linear_is_few(int64_t M, int groups) {
+  return groups ? M <= (groups < kMostRowsOfExperts ? groups : kMostRowsOfExperts) : M <= 2 * kLinearFewRows;
+}
 
 cudaError_t launch_linear_few(const LinearFewArgs& p, cudaStream_t s) {
   const int out_cols = p.ep.act == kActSwiglu ? 8 : 16;

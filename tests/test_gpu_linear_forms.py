@@ -229,3 +229,27 @@ def test_gradient_against_differences_away_from_kinks(act):
             args[which][at] -= 2 * h
             diff = (up - loss(*args)) / (2 * h)
             assert abs(float(got[at]) - float(diff)) <= float(tol[at]) + 1e-6, (act, which, at)
+
+
+@pytest.mark.parametrize("M,groups", [(32, 32), (32, 256), (33, 256), (24, 24), (25, 24), (250, 256)])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("share", [1, 0.5, 0])
+def test_rows_as_many_as_experts(M, groups, act, share):
+    """All rows of one expert, half of them, each of an expert of its own (as far as there are any)."""
+    import torch
+    from nvfp4_mixture_experts_expert_gb300 import api
+    N, K = 72, 264
+    assert (_form(M, N, K, act, groups) == FEW) == (M <= min(groups, 32))
+    g = torch.Generator(device="cuda").manual_seed(M)
+    ids = (torch.arange(M, dtype=torch.int32) * 7 + 3) % groups
+    ids[:int(share * M)] = groups - 2
+    _, order = api.sort_tokens(torch.zeros(M, 8, dtype=torch.bfloat16, device="cuda"), ids[:, None].cuda(), groups)
+    wide = 2 * N if act else N
+    x, res = _randn(g, M, K).bfloat16(), _randn(g, M, N).bfloat16()
+    w, b = (_randn(g, groups, wide, K) / math.sqrt(K)).bfloat16(), _randn(g, groups, wide).bfloat16()
+    out, z = api.expert_linear(x, w, order, b, act, res, 1.5, 0.75, out_dtype=torch.float32, preact=True)
+    for e, at in enumerate(_slices(order)):
+        if at.start < at.stop:
+            zr, zt, yr, yt = R.linear(x[at], w[e], b[e], act, res[at], (1.5, 0.75), out.dtype)
+            R.check(out[at], yr, yt)
+            R.check(z[at], zr, R.rounded(zr, zt, z.dtype))

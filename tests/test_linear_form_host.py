@@ -31,3 +31,13 @@ def test_few_rows(B):
     few = (0, 0, 0, 1)
     assert B.nvfp4_debug_linear_form(_shape(B)) == few and B.nvfp4_debug_linear_form(_shape(B, M=16)) == few
     assert B.nvfp4_debug_linear_form(_shape(B, M=6, groups=32, offsets=4, counts=4)) == few
+    assert B.nvfp4_debug_linear_form(_shape(B, M=32, groups=256, offsets=4, counts=4)) == few
+
+
+def test_many_rows_of_many_experts_are_not_few(B):
+    """All of them may fall to one expert, whose matrix the few-row kernel goes over for every eighth row."""
+    for M in (33, 200, 256):
+        try:
+            assert B.nvfp4_debug_linear_form(_shape(B, M=M, groups=256, offsets=4, counts=4))[0] > 0
+        except B.Nvfp4Error as e:  # the tiles' plan asks the device
+            assert e.status in (B.NVFP4_ERR_CUDA, B.NVFP4_ERR_DEVICE)
