@@ -594,8 +594,11 @@ enum {
 
 /*
  * nvfp4_sort_tokens -- rows of tokens copied into the order of the experts, as the
- * MoE forward orders its slots, for products outside of it (nvfp4_expert_linear,
- * nvfp4_quantize and nvfp4_grouped_gemm).
+ * MoE forward orders its slots, for products outside of it: nvfp4_linear with groups,
+ * and with align 128 nvfp4_quantize and nvfp4_grouped_gemm (offsets are its
+ * padded_offsets).  nvfp4_quantize takes a scale that it is not given from all rows:
+ * those behind the last expert's must be zeros then.  nvfp4_grouped_gemm writes its
+ * D expert by expert (group_stride_d), not in this order.
  *
  * Assignment f = t * top_k + j of token t belongs to expert topk_ids[t][j] -
  * experts_start where that lies in [0, E), else to none (an expert held elsewhere).

@@ -328,7 +328,8 @@ def sort_tokens(x, topk_ids, E, experts_start=0, align=1, out=None, stream=None)
     expert's first row is a multiple of it (128: the slots of grouped_gemm), with rows
     of zeros between.  Returns (rows [capacity, H], TokenOrder); capacity is T * top_k
     with align 1.  Rows behind the last expert's are not written: out keeps what it has
-    there, a new tensor anything."""
+    there, a new tensor anything.  quantize takes a scale that it is not given from all
+    rows, so for it out is zeros at every call."""
     rows, *tables = C.sort_tokens(x, topk_ids, E, experts_start, align, out, _handle(stream))
     return rows, TokenOrder(*tables, align)
 
