@@ -581,7 +581,8 @@ int nvfp4_moe_few_tokens_routed(const void* hidden, int64_t ld_hidden, const int
                                 const void* w2, const void* w2_sf, const float* w2_gs, float gate_limit,
                                 float up_limit, void* workspace, size_t workspace_bytes, void* out, void* stream);
 
-/* Element types and activations of the calls below. */
+/* Element types and activations of the calls below (in FP32 as the formulas stand: of
+ * -infinity NVFP4_ACT_SILU and both GELU are NaN, a product with 0). */
 enum { NVFP4_BF16 = 0, NVFP4_F16 = 1, NVFP4_F32 = 2 };
 enum {
   NVFP4_ACT_NONE = 0,
@@ -692,7 +693,8 @@ int nvfp4_linear(const nvfp4_linear_shape* shape, const void* x, int64_t ld_x, c
  * nvfp4_linear_grad -- the gradients of nvfp4_linear from dy, that of its output:
  *   dz = dy * act'(z)      (FP32, rounded to `type` as an operand of the products; limits
  *                           pass the gradient up to and at their value; relu'(0) = 0,
- *                           and where relu' is 0 dz is 0 whatever dy is)
+ *                           and where relu' is 0 dz is 0 whatever dy is;
+ *                           an FP16 dz above 65504 is infinite)
  *   dx = dz w,  dw = dz^T x  (FP32 sums, rounded once),  dbias = sum over m of dz (FP32, unrounded dz)
  *   dy        device [M][N] of `type`, row stride ld_dy
  *   preact    device [M][wide] of `type` contiguous: z; not used without an activation

@@ -376,10 +376,10 @@ def linear(x, w, bias=None, activation=None, residual=None, gate_limit=_INF, up_
            preact=False, out=None, stream=None):
     """activation(x @ w.T + bias) + residual (see nvfp4_linear): x bf16 or f16 [M, K]
     (rows may be strided), w [N, K] of x's type, bias [N] of x's type or f32, residual
-    [M, N] of x's type; the result is of x's type or f32.  activation: None, "relu",
-    "silu", "gelu", "gelu_tanh" or "swiglu", whose w (and bias) has 2N rows, the gate's
-    and the up's, with the two limits.  preact=True: returns (result, x @ w.T + bias),
-    the latter as linear_grad takes it."""
+    [M, N] of x's type; the result is of x's type or f32 (out's, where it is given).
+    activation: None, "relu", "silu", "gelu", "gelu_tanh" or "swiglu", whose w (and bias)
+    has 2N rows, the gate's and the up's, with the two limits.  preact=True: returns
+    (result, x @ w.T + bias), the latter as linear_grad takes it."""
     y, z = C.linear(x, w, None, bias, _activation(activation), gate_limit, up_limit, residual,
                     _f32(out_dtype, out, x), preact, out, _handle(stream))
     return (y, z) if preact else y

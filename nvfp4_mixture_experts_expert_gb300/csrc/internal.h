@@ -366,7 +366,7 @@ struct LinearEpilogue {
   int residual_v8, preact_v8, out_v8;  // their rows' 16-column pieces lie on multiples of 32 bytes
 };
 struct LinearArgs {
-  CUtensorMap map_a;  // see linear_gemm.cu
+  CUtensorMap map_a;  // see linear_gemm.cuh
   CUtensorMap map_b;
   LinearEpilogue ep;
   const int32_t *offsets, *counts;  // rows of each group, or null: one group of M rows

@@ -11,8 +11,11 @@
 namespace nvfp4 {
 
 // 1 / (1 + exp(-z)) by an exponential in (0, 1] and the reciprocal of a number in
-// (1, 2], both of a few FP32 units in the last place (of the result's size where it is
-// near 0: an absolute 2^-22): an accurate expf and a division take z / (1 + expf(-z))
+// (1, 2].  __expf(-|z|) is within 2 + 1.18 |z| units in the last place (CUDA's bound),
+// the reciprocal within one: below an absolute 2^-21 everywhere, but relative to a result
+// near 0 the error grows with |z| (2^-19 at z = -6, 2^-16 at -87: less than the rounding to
+// 16 bits, which FP32 outputs and bias sums do not have).  An accurate expf and a division
+// take z / (1 + expf(-z))
 // to the slow path of the division for far negative z (8192 x 4096 x 4096 with silu 243
 // us instead of 160), and a gradient's pass over dy and z to its arithmetic.
 __device__ __forceinline__ float sigmoid(float z) {
@@ -66,8 +69,8 @@ __device__ __forceinline__ uint32_t pack2(int type, float a, float b) {
 }
 
 // W consecutive values of a row (8, 16 or 32), of which `left` exist (a multiple of 8);
-// v8: the addresses are multiples of 32 bytes, and whole sectors are moved (of eight
-// 16-bit values, half a sector, a lane moves one half and its neighbour the other).
+// v8: the addresses are multiples of 32 bytes, and whole sectors are moved (eight 16-bit
+// values, half a sector, by 16 bytes all the same).
 template <int WORDS>
 __device__ __forceinline__ void load_row(const void* p, bool v8, int left, uint32_t (&u)[WORDS]) {
   const uint32_t* q = static_cast<const uint32_t*>(p);

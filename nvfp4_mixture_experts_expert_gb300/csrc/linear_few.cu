@@ -12,10 +12,11 @@
 //
 // Bound: reading w.  Launches are chained, and a block has its part of w fetched
 // into L2 before it waits for the kernel before (not with experts: which of them
-// have rows is that kernel's result).  1 x 4096 x 4096 takes 7.4 us in a row of calls
-// with different w (4.5 TB/s; floor 4.9; 8.0 without the fetch): launch, first loads and
-// the join of 16 warps are ~2.5 of them.  Built and not faster: w and x through a ring of
-// bulk copies, one CTA a SM (14 us; two CTAs 9.5).
+// have rows is that kernel's result).  1 x 4096 x 4096 takes 7.1 us in a row of calls
+// with different w (4.7 TB/s; floor 4.9; 0.6 more without the fetch): launch, first loads
+// and the join of 16 warps are ~2 of them.  One token of six experts of 4096 x 4096: 40 us
+// (5.0 TB/s; floor 30).  Built and not faster: w and x through a ring of bulk copies, one
+// CTA a SM (twice the time; two CTAs 1.3 times).
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -27,9 +28,10 @@ namespace nvfp4 {
 namespace {
 
 // Warps of a block, and blocks a SM: one matrix has few blocks, of which each should
-// have all of its K in flight (1 x 4096 x 4096 7.7 us; with eight warps 11 to 13), the
+// have all of its K in flight (1 x 4096 x 4096 with eight warps 1.5 times as long), the
 // experts together have many, which overlap one's end with the next's beginning (six
-// experts' 4096 x 4096 40 us instead of 44).
+// experts' 4096 x 4096 40 us instead of 44).  Five blocks of eight warps leave 48 registers,
+// of which the kernel spills a little (84 bytes of stores, 52 of loads a thread).
 __host__ __device__ constexpr int warps_of(bool experts) { return experts ? 8 : 16; }
 __host__ __device__ constexpr int blocks_of(bool experts) { return experts ? 5 : 2; }
 constexpr int kRows = (int)kLinearFewRows;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(32 * warps_of(EXPERTS), blocks_of(EXPERTS)) li
 }  // namespace
 
 // One matrix: two passes over w (the second from L2) against a 128-row tile: 16 x 4096 x
-// 4096 11.3 us against 12.4 (8 rows 7.7 against 16; 17 rows 14.9 against 12.4).
+// 4096 10.7 us against 12.3 (8 rows 7.1 against 17; 17 rows 14.3 against 12.4).
 // Experts: as many rows as experts, and at most four passes should all of them fall to
 // one.  us here and (in brackets) on tiles, each row of another expert / all of one:
 //   rows                       8                    32                     256

@@ -42,7 +42,7 @@ cudaError_t launch_linear_plain(LinearArgs& p, int slots, cudaStream_t s) {
 // 4096 (one 19.3), 64 columns with eight 8.9 for 64 x 256 x 8192 (one 24.8).  Pairs on
 // groups of rows run turned, a K-block in less time where a tile has fewer tokens, and
 // with an epilogue that SwiGLU's arithmetic makes longer: 32 groups of 300 rows, 4096 x
-// 4096, 257 us (256 columns 319, 128 361; not turned 315), of 1024 rows of 512 inputs,
+// 4096, 260 us (256 columns 319, 128 361; not turned 315), of 1024 rows of 512 inputs,
 // SwiGLU, 138 (256 columns 109).  Weight
 // gradients of groups run as single CTAs: the rows behind a group's last would have to
 // be set to zero in both CTAs' operands (by remote stores and a fence of the cluster 521

@@ -20,7 +20,7 @@
 // whose length an instruction takes in steps of 32 where M is always 256, so the tiles
 // of a group share its rows evenly.  A lane of the accumulator is then an output column,
 // and the epilogue turns it through shared memory.  32 groups of 300 rows, 4096 x 4096:
-// 257 us instead of 315, 48 skewed ones of 1024 on average 932 instead of 970.
+// 260 us instead of 315, 48 skewed ones of 1024 on average 932 instead of 970.
 //
 // Persistent, tiles of 128 x BN, FP32 accumulators in TMEM, two of them, so that a
 // tile's epilogue runs beside the next one's products.  Large problems run as CTA
@@ -31,9 +31,9 @@
 // and half of the columns each).  Every wait is bounded and reports in the
 // library's status word.
 //
-// Bound: the tensor pipe, then power.  8192 x 4096 x 4096 takes 143 us in a short row
-// of calls (1.92 PFLOP/s; tensor pipe 91 % busy; cuBLAS 137) and 151 over seconds
-// (cuBLAS 154), with bias and residual 150.  What made the difference, from 234 us:
+// Bound: the tensor pipe, then power.  8192 x 4096 x 4096 takes 144 us in a short row
+// of calls (1.91 PFLOP/s; tensor pipe 91 % busy; torch.mm 140) and 164 over seconds
+// (torch.mm 158), with bias and residual 152 and 174.  What made the difference, from 234 us:
 //   - pairs (163 us): a CTA alone copies 48 KB and its MMAs read 48 KB of shared memory a
 //     K-block, which is more than the 512 cycles of its products carry (385 ns a block
 //     instead of 310);
@@ -43,7 +43,8 @@
 //   - tiles in bands (144);
 //   - an epilogue thread that keeps a row's 16 or 32 columns and stores whole 32-byte
 //     sectors; spilled registers cost most where an output is large (8192 x 8192 x 64:
-//     174 us with them, 38 without; 4 TB/s of writes, what a fill of memory reaches).
+//     174 us with them, 38 without; 4 TB/s of writes, what a fill of memory reaches).  Left
+//     are 20 bytes of stores and 44 of loads a thread in the pairs without an activation.
 // Built and not faster: the output through shared memory and bulk copies (42 to 49 us
 // there), two K-blocks a stage for pairs, the producer asking ahead as well.
 #pragma once
