@@ -18,16 +18,19 @@ _NAMES = {(0, 0, 0, False): FEW, (64, 0, 0, False): C64, (64, 0, 0, True): C64_S
 ACT = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 E = 5  # experts
 
-# form -> (M, N, K), (M, N, K) with SwiGLU; experts: M rows over E of them
+# form -> (M, N, K), (M, N, K) with SwiGLU; experts: M rows over E of them.  The plan knows how many clusters of a size
+# a device holds: sizes are such that the form is the same with some fewer of them.
 LINEAR = {FEW: [(16, 72, 264)] * 2, C64: [(41, 136, 72)] * 2, C64_SPLIT: [(35, 136, 2056)] * 2,
-          C128: [(777, 4240, 72)] * 2, C128_SPLIT: [(300, 1000, 3600), (300, 504, 3600)], C256: [(2600, 4640, 72)] * 2,
+          C128: [(777, 4240, 72)] * 2, C128_SPLIT: [(300, 2504, 7688), (300, 1256, 7688)], C256: [(2600, 4640, 72)] * 2,
           PAIR: [(803, 3032, 720)] * 2}
 EXPERTS = {FEW: [(5, 72, 136)] * 2, C64: [(41, 72, 136)] * 2, C128: [(60, 3096, 360)] * 2,
            C256: [(2470, 4552, 72)] * 2, TURNED: [(900, 2056, 1032)] * 2}
+SPLIT = (C64_SPLIT, C128_SPLIT)  # one or the other, by the device's clusters
 # M, N, K, activation, form of dx, form of dw
 GRADS = [(41, 72, 136, None, C64, C64), (2100, 16, 16, None, C64, C64_SPLIT),
          (70, 1168, 2944, "swiglu", C64_SPLIT, C128), (1300, 72, 2688, None, C128, C64),
-         (3300, 3128, 72, None, C128_SPLIT, C128_SPLIT), (4100, 72, 2968, "gelu", C256, C128_SPLIT),
+         (300, 7688, 2504, None, C128_SPLIT, C128), (7688, 304, 2504, "relu", C128, C128_SPLIT),
+         (3300, 3128, 72, None, SPLIT, SPLIT), (4100, 72, 2968, "gelu", C256, SPLIT),
          (777, 776, 2784, None, PAIR, PAIR), (777, 776, 2784, "swiglu", PAIR, C256)]
 EXPERT_GRADS = [(41, 72, 136, None, C64, C64), (60, 328, 2456, "swiglu", C128, C128),
                 (64, 744, 3888, None, C256, C128), (900, 1032, 2056, "silu", TURNED, C256)]
@@ -78,8 +81,8 @@ def test_the_lists_name_every_form(experts):
     forms = set(_NAMES.values()) - ({PAIR, C64_SPLIT, C128_SPLIT} if experts else {TURNED})
     assert set(EXPERTS if experts else LINEAR) == forms
     grads = EXPERT_GRADS if experts else GRADS
-    assert {g[4] for g in grads} == forms - {FEW}
-    assert {g[5] for g in grads} == forms - {FEW, TURNED}  # groups' rows as the contraction: single CTAs
+    assert {g[4] for g in grads} - {SPLIT} == forms - {FEW}
+    assert {g[5] for g in grads} - {SPLIT} == forms - {FEW, TURNED}  # groups' rows as the contraction: single CTAs
 
 
 @pytest.mark.parametrize("form,act,M,N,K,experts", [(*c, False) for c in _all(LINEAR)] + [(*c, True) for c in _all(EXPERTS)])
@@ -164,7 +167,8 @@ def test_gradients(M, N, K, act, dx_form, dw_form, experts):
     import torch
     from nvfp4_mixture_experts_expert_gb300 import api
     groups = E if experts else 0
-    assert (_form(M, N, K, act, groups, 1), _form(M, N, K, act, groups, 2)) == (dx_form, dw_form)
+    for product, form in ((1, dx_form), (2, dw_form)):
+        assert _form(M, N, K, act, groups, product) in (form if form is SPLIT else (form,))
     g = torch.Generator(device="cuda").manual_seed(N)
     wide, lead = (2 * N if act == "swiglu" else N), (E,) if experts else ()
     x, dy = _randn(g, M, K).bfloat16(), _randn(g, M, N + 8).bfloat16()[:, :N]
@@ -175,6 +179,8 @@ def test_gradients(M, N, K, act, dx_form, dw_form, experts):
         dx, dw, db = api.expert_linear_grad(dy, x, w, order, z, act, 1.5, 0.75, bias=True)
     else:
         dx, dw, db = api.linear_grad(dy, x, w, z, act, 1.5, 0.75, bias=True)
+    if act == "relu":  # relu'(0) = 0, where the reference's derivative of clamp is 1; z decides on the slope alone
+        z = torch.where(z == 0, torch.full_like(z, -1), z)
     for e, at in enumerate(_slices(order) if experts else [slice(0, M)]):
         want = R.linear_grad(dy[at], x[at], w[e] if experts else w, None if z is None else z[at], act, (1.5, 0.75), x.dtype)
         for got, (ref, tol) in zip((dx[at], dw[e], db[e]) if experts else (dx, dw, db), want):
